@@ -81,6 +81,8 @@ enum pk_dtype { PK_BF16 = 0, PK_FP32 = 1 };
                                    max_blocks_per_seq * block_size */
 #define PK_DEVERR_TIMEOUT  0x10u /* a kernel gave up waiting on one of its own pipeline
                                     barriers (never expected; the results are invalid) */
+#define PK_DEVERR_SCALE    0x40u /* a scale of the 8-bit cache (pagedkv_fp8.h) is outside
+                                    [2^-64, 2^64] or not a number */
 #define PK_DEVERR_POINTER  0x20u /* a per-layer pointer of a *_layers call is NULL or not
                                     16-byte aligned (that layer was skipped) */
 
@@ -321,6 +323,50 @@ int pk_reshape_and_cache(const void *k, const void *v, void *k_cache, void *v_ca
                          const int64_t *slot_mapping, int num_tokens,
                          int num_kv_heads, int head_dim, int num_blocks,
                          int block_size, pk_stream_t stream);
+
+/*
+ * The rotary position embedding of new tokens and their append, in one pass:
+ * q_out = rotated q, and the rotated k and v as they are go to their cache
+ * slots.  The pages start after the rotation ("PagedAttention from First
+ * Principles", §2: the cache holds keys as they are attended); every model
+ * that fills this cache with rotary positions runs it just before the append.
+ *
+ * Of each head of D elements the first rot_dim are rotated and the others
+ * pass.  Pair i < rot_dim / 2 is (x[i], x[i + rot_dim / 2]), or with
+ * interleaved != 0 (x[2 i], x[2 i + 1]), and becomes, at position t,
+ *   factor * (x1 cos(t f_i) - x2 sin(t f_i), x2 cos(t f_i) + x1 sin(t f_i)).
+ * The angle is kept modulo a turn in 64-bit fixed point, so that far positions
+ * lose nothing; products and sums are fp32, rounded once to bf16.
+ *
+ *   q             [num_tokens, num_heads, head_dim] bf16, tokens q_stride
+ *                 elements apart (heads dense within a token): a slice of a
+ *                 fused projection's output needs no copy.  num_heads 0: no
+ *                 queries (q and q_out unused).
+ *   q_out         [num_tokens, num_heads, head_dim] bf16, q_out_stride apart;
+ *                 may be q itself with the same stride (rotated in place), and
+ *                 must not overlap the inputs otherwise
+ *   k, v          [num_tokens, num_kv_heads, head_dim] bf16, k_stride and
+ *                 v_stride apart
+ *   k_cache, v_cache, slot_mapping, num_blocks, block_size
+ *                 as for pk_reshape_and_cache (a negative slot is padding: its
+ *                 K and V are not written; its query is rotated all the same)
+ *   positions     [num_tokens] int64 device array; exact to 2^-33 turns for
+ *                 |position| < 2^31
+ *   inv_freq      [rot_dim / 2] fp32 device array, radians a position, below
+ *                 2^32 (others turn nothing); scaling for long contexts is in
+ *                 these values
+ *   rot_dim       0 (no rotation; positions and inv_freq unused) to head_dim,
+ *                 a multiple of 16
+ *   factor        scales what is rotated (the attention factor of long-context
+ *                 scalings; 1 otherwise), in [2^-20, 2^20]
+ * Strides are multiples of 8 elements (whole 16-byte vectors) and not less
+ * than the heads of a token.  num_tokens == 0 is a no-op.
+ */
+int pk_rope_and_cache(void *q_out, const void *q, const void *k, const void *v, int64_t q_out_stride,
+                      int64_t q_stride, int64_t k_stride, int64_t v_stride, void *k_cache, void *v_cache,
+                      const int64_t *slot_mapping, const int64_t *positions, const float *inv_freq,
+                      int rot_dim, int interleaved, float factor, int num_tokens, int num_heads,
+                      int num_kv_heads, int head_dim, int num_blocks, int block_size, pk_stream_t stream);
 
 /*
  * Copy whole blocks, K and V, one launch for all pairs ("vLLM —

@@ -11,6 +11,7 @@ import os
 from . import build as _build
 
 c_int, c_float, c_size_t, c_void_p, c_uint = ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_uint
+c_int64 = ctypes.c_int64
 
 # name -> (restype, argtypes), in the header's order.
 SIGNATURES = {
@@ -62,6 +63,43 @@ SIGNATURES = {
         c_int, c_int, c_int, c_int, c_int, c_void_p]),
     "pk_get_device_error": (c_int, [ctypes.POINTER(c_uint), c_void_p]),
     "pk_set_decode_path": (c_int, [c_int]),
+    "pk_rope_and_cache": (c_int, [
+        c_void_p, c_void_p, c_void_p, c_void_p,                  # q_out, q, k, v
+        c_int64, c_int64, c_int64, c_int64,                      # their token strides
+        c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,        # k_cache, v_cache, slot_mapping, positions, inv_freq
+        c_int, c_int, c_float, c_int, c_int,                     # rot_dim, interleaved, factor, num_tokens, num_heads
+        c_int, c_int, c_int, c_int, c_void_p]),                  # num_kv_heads, head_dim, num_blocks, block_size, stream
+    # include/pagedkv_fp8.h
+    "pk_rope_and_cache_fp8": (c_int, [
+        c_void_p, c_void_p, c_void_p, c_void_p,                  # q_out, q, k, v
+        c_int64, c_int64, c_int64, c_int64,                      # their token strides
+        c_void_p, c_void_p, c_void_p, c_void_p,                  # k_cache, v_cache, k_scales, v_scales
+        c_void_p, c_int, c_void_p,                               # block_tables, max_blocks_per_seq, seq_lens
+        c_void_p, c_int, c_int,                                  # cu_q_lens, max_q_len, num_seqs
+        c_void_p, c_void_p, c_int, c_int, c_float,               # positions, inv_freq, rot_dim, interleaved, factor
+        c_int, c_int, c_int, c_int, c_int, c_int, c_void_p]),    # tokens, heads, kv_heads, head_dim, blocks, block_size, stream
+    "pk_decode_fp8_workspace_bytes": (c_size_t, [c_int, c_int, c_int, c_int, c_int]),
+    "pk_paged_attention_decode_fp8": (c_int, [
+        c_void_p, c_int, c_void_p,                               # out, out_dtype, q
+        c_void_p, c_void_p, c_void_p, c_void_p,                  # k_cache, v_cache, k_scales, v_scales
+        c_void_p, c_int, c_void_p, c_int,                        # block_tables, max_blocks_per_seq, seq_lens, max_seq_len
+        c_int, c_int, c_int, c_int, c_int, c_int, c_float,       # seqs, heads, kv_heads, head_dim, blocks, block_size, scale
+        c_void_p, c_size_t, c_void_p]),                          # workspace, workspace_bytes, stream
+    "pk_paged_attention_multi_query_fp8": (c_int, [
+        c_void_p, c_int, c_void_p, c_int, c_void_p, c_int,       # out, out_dtype, q, total_q, cu_q_lens, max_q_len
+        c_void_p, c_void_p, c_void_p, c_void_p,
+        c_void_p, c_int, c_void_p, c_int,
+        c_int, c_int, c_int, c_int, c_int, c_int, c_float,
+        c_void_p, c_size_t, c_void_p]),
+    "pk_gather_kv_fp8": (c_int, [
+        c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,   # out_k, out_v, k_cache, v_cache, k_scales, v_scales
+        c_void_p, c_int, c_void_p, c_void_p, c_int64,            # block_tables, max_blocks_per_seq, seq_lens, cu_seq_lens, out_rows
+        c_int, c_int, c_int, c_int, c_int, c_int, c_void_p]),    # max_seq_len, seqs, kv_heads, head_dim, blocks, block_size, stream
+    "pk_copy_blocks_fp8": (c_int, [
+        c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_int, c_void_p]),
+    "pk_swap_blocks_fp8": (c_int, [
+        c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+        c_int, c_int, c_int, c_int, c_int, c_int, c_void_p]),
     # include/pagedkv_block_manager.h
     "pk_bm_create": (c_void_p, [c_int, c_int]),
     "pk_bm_destroy": (None, [c_void_p]),
@@ -88,7 +126,7 @@ STATUS_NAMES = {
 }
 PK_ERR_NO_BLOCKS, PK_ERR_UNKNOWN_SEQUENCE, PK_ERR_SEQUENCE_EXISTS = -8, -9, -10
 DEVERR_BLOCK_ID, DEVERR_SLOT, DEVERR_PAIR, DEVERR_SEQ_LEN, DEVERR_TIMEOUT = 0x1, 0x2, 0x4, 0x8, 0x10
-DEVERR_POINTER = 0x20
+DEVERR_POINTER, DEVERR_SCALE = 0x20, 0x40
 PATH_AUTO, PATH_CUDA_CORE, PATH_TENSOR_CORE = 0, 1, 2
 
 _lib = None

@@ -227,6 +227,97 @@ def pk_reshape_and_cache(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor
 reshape_and_cache = pk_reshape_and_cache
 
 
+def _need_rows(t: torch.Tensor, name: str, device):
+    """[tokens, heads, D] bf16 rows whose heads are dense; the tokens may be any
+    stride apart (a slice of a fused projection).  Returns that stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have 3 dims, got shape {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (this library has no CPU path)")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    T, heads, D = t.shape
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 and D > 1) or (s1 != D and heads > 1):
+        raise ValueError(f"the heads of a token of {name} must be contiguous")
+    return s0 if T > 1 else max(s0, heads * D + -(heads * D) % 8)
+
+
+def _rope_args(q, k, v, inv_freq, q_out, dev):
+    """Checks what the two rotary appends share; returns the queries' output,
+    the number of query heads, the rotated elements and the token strides."""
+    k_stride, v_stride = _need_rows(k, "k", dev), _need_rows(v, "v", dev)
+    T, _, D = k.shape
+    if v.shape != k.shape:
+        raise ValueError("k and v must have the same shape")
+    rot = 0
+    if inv_freq is not None:
+        _need(inv_freq, "inv_freq", torch.float32, 1, dev)
+        rot = 2 * inv_freq.shape[0]
+        if rot > D:
+            raise ValueError(f"inv_freq has {rot // 2} frequencies for a head dim of {D}")
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out without q")
+        return None, 0, rot, (0, 0, k_stride, v_stride)
+    q_stride = _need_rows(q, "q", dev)
+    if q.shape[0] != T or q.shape[2] != D:
+        raise ValueError("q must have k's tokens and head dim")
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        out_stride = q.shape[1] * D
+    else:
+        out_stride = _need_rows(q_out, "q_out", dev)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+    return q_out, q.shape[1], rot, (out_stride, q_stride, k_stride, v_stride)
+
+
+def pk_rope_and_cache(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
+                      v_cache: torch.Tensor, slot_mapping: torch.Tensor, positions: Optional[torch.Tensor],
+                      inv_freq: Optional[torch.Tensor], *, interleaved: bool = False, factor: float = 1.0,
+                      q_out: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
+    """Rotate q and k ([T, H, D] and [T, Hkv, D] bf16, tokens any stride apart) by
+    their int64 positions, write k and v to their int64 slots of the bf16 cache and
+    return the rotated queries (in ``q_out`` if given; it may be q).  The first
+    ``2 * len(inv_freq)`` elements of a head are rotated; ``inv_freq`` None
+    rotates nothing, q None has no queries.  See the C header."""
+    dev = k_cache.device
+    _need(k_cache, "k_cache", torch.bfloat16, 4, dev)
+    _need(v_cache, "v_cache", torch.bfloat16, 4, dev)
+    _need(slot_mapping, "slot_mapping", torch.int64, 1, dev)
+    given = q_out is not None
+    q_out, H, rot, strides = _rope_args(q, k, v, inv_freq, q_out, dev)
+    T, Hkv, D = k.shape
+    P, B, Hc, Dc = k_cache.shape
+    if (Hc, Dc) != (Hkv, D) or v_cache.shape != k_cache.shape:
+        raise ValueError("k / v / cache shapes disagree")
+    if slot_mapping.shape[0] != T:
+        raise ValueError("slot_mapping must have one entry per token")
+    if rot:
+        if positions is None:
+            raise ValueError("a rotation needs positions")
+        _need(positions, "positions", torch.int64, 1, dev)
+        if positions.shape[0] != T:
+            raise ValueError("positions must have one entry per token")
+    with torch.cuda.device(dev):
+        st = load().pk_rope_and_cache(
+            _ptr(q_out), _ptr(q), _ptr(k), _ptr(v), *strides, _ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping),
+            _ptr(positions), _ptr(inv_freq), rot, int(interleaved), float(factor), T, H, Hkv, D, P, B,
+            _stream(dev, stream))
+    check("pk_rope_and_cache", st)
+    if stream is not None and q_out is not None and not given:
+        q_out.record_stream(stream)
+    return q_out
+
+
+rope_and_cache = pk_rope_and_cache
+
+
 def pk_copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor, src_dst_pairs: torch.Tensor,
                    stream=None) -> None:
     """Copy whole blocks for every (src, dst) row of an int64 [n, 2] tensor.  See the C header."""

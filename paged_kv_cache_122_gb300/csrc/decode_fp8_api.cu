@@ -1,0 +1,113 @@
+// Host entry points of attention over the 8-bit paged cache: argument checks
+// and the launch.
+#include "decode_fp8.cuh"
+
+#include <cmath>
+
+namespace {
+
+bool group_supported(int G) { return G == 1 || G == 2 || G == 4 || G == 8 || G == 16; }
+
+// Both calls; cu_q_lens is NULL for one query token a sequence.
+int attend(void *out, int out_dtype, const void *q, int total_q, const int32_t *cu_q_lens, int max_q_len,
+           const void *k_cache, const void *v_cache, const float *k_scales, const float *v_scales,
+           const int32_t *block_tables, int max_blocks_per_seq, const int32_t *seq_lens, int max_seq_len, int num_seqs,
+           int num_heads, int num_kv_heads, int head_dim, int num_blocks, int block_size, float scale, void *workspace,
+           size_t workspace_bytes, pk_stream_t stream, bool multi) {
+    if (num_seqs < 0 || num_heads <= 0 || num_kv_heads <= 0 || num_blocks < 0 || max_blocks_per_seq < 0 ||
+        max_seq_len < 0 || block_size <= 0 || total_q < 0 || max_q_len < 0)
+        return PK_ERR_SHAPE;
+    if (num_heads % num_kv_heads) return PK_ERR_SHAPE;
+    if (static_cast<int64_t>(max_seq_len) > static_cast<int64_t>(max_blocks_per_seq) * block_size)
+        return PK_ERR_SHAPE;
+    if (out_dtype != PK_BF16 && out_dtype != PK_FP32) return PK_ERR_UNSUPPORTED;
+    if (head_dim != 64 && head_dim != 128) return PK_ERR_UNSUPPORTED;
+    if (block_size != 8 && block_size != 16 && block_size != 32) return PK_ERR_UNSUPPORTED;
+    const int G = num_heads / num_kv_heads;
+    if (!group_supported(G)) return PK_ERR_UNSUPPORTED;
+    int q_len = 1;                                  // query tokens a sequence, padded to a power of two
+    while (q_len < max_q_len && q_len <= 16) q_len <<= 1;
+    if (G * q_len > 16) return PK_ERR_UNSUPPORTED;
+    if (!std::isfinite(scale)) return PK_ERR_SHAPE;
+    // A piece (block, KV head) is one step of a TMA coordinate.
+    if (num_seqs > 65535 || num_kv_heads * 2 > 65535 ||
+        static_cast<int64_t>(num_blocks) * num_kv_heads > 0x7fffffff)
+        return PK_ERR_SHAPE;
+    if (num_seqs == 0 || total_q == 0) return PK_OK;
+    if (!out || !q || !seq_lens || (multi && !cu_q_lens) ||
+        (max_seq_len > 0 && (!k_cache || !v_cache || !k_scales || !v_scales || !block_tables)))
+        return PK_ERR_NULL;
+    if (!pk::aligned16(out) || !pk::aligned16(q) || !pk::aligned16(k_cache) || !pk::aligned16(v_cache))
+        return PK_ERR_ALIGNMENT;
+
+    pk::DecodeFp8Params p{};
+    p.out = out;
+    p.out_fp32 = out_dtype == PK_FP32;
+    p.q = static_cast<const uint16_t *>(q);
+    p.k8 = static_cast<const uint8_t *>(k_cache);
+    p.v8 = static_cast<const uint8_t *>(v_cache);
+    p.k_scales = k_scales;
+    p.v_scales = v_scales;
+    p.block_tables = block_tables;
+    p.seq_lens = seq_lens;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.max_seq_len = max_seq_len;
+    p.num_seqs = num_seqs;
+    p.num_heads = num_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.head_dim = head_dim;
+    p.num_blocks = num_blocks;
+    p.block_size = block_size;
+    p.scale_log2 = scale * pk::kLog2e;
+    p.cu_q_lens = cu_q_lens;
+    p.q_len = q_len;
+    p.total_q = total_q;
+    if (max_seq_len > 128) {       // a longer sequence may span several CTAs: its parts need slots
+        if (!workspace || workspace_bytes < pk::tc_workspace_bytes()) return PK_ERR_WORKSPACE;
+        if (!pk::aligned16(workspace)) return PK_ERR_ALIGNMENT;
+        p.tc_slots = workspace;
+    }
+    p.err = pk::error_word_ptr();
+    if (!p.err) return PK_ERR_NO_DEVICE;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (max_seq_len == 0) {        // every sequence is empty: the rows are zeros
+        const size_t bytes = static_cast<size_t>(total_q) * num_heads * head_dim * (p.out_fp32 ? 4 : 2);
+        return cudaMemsetAsync(out, 0, bytes, st) == cudaSuccess ? PK_OK : PK_ERR_CUDA;
+    }
+    return pk::launch_decode_fp8_tensor_core(p, st) == cudaSuccess ? PK_OK : PK_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" size_t pk_decode_fp8_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                                int max_seq_len) {
+    if (num_seqs < 0 || num_heads <= 0 || num_kv_heads <= 0 || max_seq_len < 0) return 0;
+    if (num_heads % num_kv_heads) return 0;
+    if (head_dim != 64 && head_dim != 128) return 0;
+    return max_seq_len > 128 ? pk::tc_workspace_bytes() : 0;
+}
+
+extern "C" int pk_paged_attention_decode_fp8(void *out, int out_dtype, const void *q, const void *k_cache,
+                                             const void *v_cache, const float *k_scales, const float *v_scales,
+                                             const int32_t *block_tables, int max_blocks_per_seq,
+                                             const int32_t *seq_lens, int max_seq_len, int num_seqs, int num_heads,
+                                             int num_kv_heads, int head_dim, int num_blocks, int block_size,
+                                             float scale, void *workspace, size_t workspace_bytes,
+                                             pk_stream_t stream) {
+    return attend(out, out_dtype, q, num_seqs, nullptr, 1, k_cache, v_cache, k_scales, v_scales, block_tables,
+                  max_blocks_per_seq, seq_lens, max_seq_len, num_seqs, num_heads, num_kv_heads, head_dim, num_blocks,
+                  block_size, scale, workspace, workspace_bytes, stream, false);
+}
+
+extern "C" int pk_paged_attention_multi_query_fp8(void *out, int out_dtype, const void *q, int total_q,
+                                                  const int32_t *cu_q_lens, int max_q_len, const void *k_cache,
+                                                  const void *v_cache, const float *k_scales, const float *v_scales,
+                                                  const int32_t *block_tables, int max_blocks_per_seq,
+                                                  const int32_t *seq_lens, int max_seq_len, int num_seqs,
+                                                  int num_heads, int num_kv_heads, int head_dim, int num_blocks,
+                                                  int block_size, float scale, void *workspace,
+                                                  size_t workspace_bytes, pk_stream_t stream) {
+    return attend(out, out_dtype, q, total_q, cu_q_lens, max_q_len, k_cache, v_cache, k_scales, v_scales,
+                  block_tables, max_blocks_per_seq, seq_lens, max_seq_len, num_seqs, num_heads, num_kv_heads, head_dim,
+                  num_blocks, block_size, scale, workspace, workspace_bytes, stream, true);
+}

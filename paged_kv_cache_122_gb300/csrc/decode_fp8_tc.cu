@@ -1,0 +1,984 @@
+// Attention over the 8-bit paged cache on the 5th-generation tensor cores.
+//
+// Mathematics.  With ks, vs the scales of a token's block and KV head,
+//   s_j = scale * ks_j * (q . k_j),  out = sum_j 2^(t_j - m) v_j / sum_j 2^(t_j - m) / vs_j,
+//   t_j = s_j log2(e) + log2(vs_j),
+// k_j and v_j the stored e4m3 rows.  Both contractions run on kind::f8f6f4
+// MMAs straight from the pages as TMA lands them: nothing widens K or V.  The
+// other operands are split into e4m3 terms that each take columns of their own:
+//   q * 2^k = h + l / 32, 2^k bringing the row's largest to [128, 256): two
+//     terms hold a bf16 value exactly down to 2^-13 of the row's largest, and
+//     what is smaller to 2^-22 of it.
+//   u = 2^(t - m) = h1 + h2 / 32 + h3 / 2^16, u <= 256: 9 bits or more of the
+//     largest weights, 13 of those below 4, and nothing above 2^-27 is lost
+//     (of a largest weight that is 16 or more: see the reference below).
+// The extra columns cost MMA time only, and a tile's MMAs take a tenth of the
+// time its bytes take from HBM.
+//
+// Bound: HBM bytes of the cache, 2 D a token and KV head.  The work split, the
+// reference maximum that moves rarely, the merge of cut segments and the
+// bounded waits are those of the bf16 kernel (decode_tc.cu, decode_split.cuh).
+//
+// Per 128-token tile, inside a CTA (256 threads):
+//   warp 0    producer: block-table entries one tile ahead (a lane per page),
+//             one box of K and one of V per page and KV head -- B D contiguous
+//             bytes -- into a ring of six stages, and the pages' scales by
+//             cp.async beside them;
+//   warp 1    MMA issuer (one thread, event loop);
+//   warps 2-5 softmax, thread <-> token (TMEM lane);
+//   warps 6-7 queries: take the (sequence, head) segments in turn, split their
+//             rows into h and l and write them in the MMA's layout, ahead of
+//             the tiles.
+// At head dim 64 a tile holds two adjacent KV heads (HP = 2) where their number
+// is even and the group small enough, so that its bytes are those of head dim 128.
+#include "decode_fp8.cuh"
+#include "decode_split.cuh"
+#include "fp8.cuh"
+#include "sm100.cuh"
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <mutex>
+
+namespace pk {
+namespace {
+
+using namespace sm100;
+
+constexpr int kThreads = 256;
+constexpr int kStages = 6;
+constexpr int kQBytes = 8192;                                // all query buffers
+constexpr int kQRing = 8;                                    // query scales kept, by segment
+constexpr uint64_t kWaitLimitNs = 1000000000ull;             // 1 s: far beyond any legal wait
+constexpr int kLenCache = 2048;                              // lengths kept in shared memory up to this batch
+constexpr float kLevel2 = 1.f / 32, kLevel3 = 1.f / 65536;   // what the terms of u stand for
+constexpr float kHeadroom = 8.f;                             // u <= 2^8: e4m3 holds 256
+constexpr float kStart = 4.f;                                // the largest u when the reference moves: 2^4
+
+constexpr uint32_t kLayoutSw64 = 4;
+
+// Instruction descriptor for kind::f8f6f4: fp32 accumulator, e4m3 A and B.
+__host__ __device__ constexpr uint32_t idesc_e4m3(uint32_t m, uint32_t n, uint32_t a_mn_major, uint32_t b_mn_major) {
+    return (1u << 4) | (a_mn_major << 15) | (b_mn_major << 16) | ((n >> 3) << 17) | ((m >> 4) << 24);
+}
+
+SM100_DEV void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+SM100_DEV void cp_async4(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+// One arrival on `bar` when this thread's cp.async so far have landed.
+SM100_DEV void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+SM100_DEV void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+struct Misc {
+    uint64_t full[kStages];       // K rows of a stage landed
+    uint64_t vfull[kStages];      // V rows of a stage landed
+    uint64_t sfull[kStages];      // its pages' scales landed
+    uint64_t empty[kStages];
+    uint64_t qfull[kQRing];       // a segment's queries written (by buffer)
+    uint64_t qempty[kQRing];
+    uint64_t s_full[2];
+    uint64_t p_full[2];
+    uint64_t o_full[2];       // P.V of a tile complete (per tile parity)
+    uint64_t o_free[2];       // a segment's O buffer has been read out
+    uint64_t drain;
+    int64_t scan[kThreads / 32 + 1];
+    int64_t scan_w[kThreads / 32 + 1];
+    int64_t bnd[2];
+    int64_t rem0;
+    int32_t s0;
+    int32_t first_cta;
+    uint32_t tmem_base;
+    int abort;
+    int never;
+    uint32_t mask[kStages][4];
+    int4 meta[kStages];            // (sequence, KV head group, tile, tiles in segment) of a stage's tile
+    int4 qmeta[kStages];           // (first query row, query tokens, first query position, 0) of it
+    float scales[kStages][16][2][2];   // [page][K, V][head of the pair]
+    float qscale[kQRing][kNPad];   // by segment: what the stored query values of a column stand for
+    float red[4][kNPad];
+    float lsum[4][kNPad];
+    int lens[kLenCache];
+};
+
+// 32 consecutive columns of this thread's TMEM lane.
+SM100_DEV void tmem_ld32(uint32_t taddr, float (&v)[32]) {
+    uint32_t r[32];
+    __syncwarp();
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// The weights of the cut, as for the bf16 kernel's (decode_tc.cu).
+constexpr int64_t kTileCost = 400;
+constexpr int kTokCost = 1;
+template <int NUSED, int HP>
+constexpr int64_t seg_cost() { return (NUSED > 8 ? 200 : 56) / HP; }
+
+// What follows from (head dim, query columns per KV head, KV heads per tile).
+template <int D, int NC, int HP>
+struct Shape {
+    static_assert(D == 64 || D == 128, "head_dim");
+    static_assert(NC >= 1 && NC <= kNPad, "query columns");
+    static_assert(HP == 1 || (HP == 2 && D == 64 && NC <= 8), "head pairs: head dim 64, at most 8 columns each");
+    static constexpr int CW = HP == 2 ? 8 : kNPad;          // columns per head in slots and lsum
+    static constexpr int NCOL = HP == 2 ? 8 + NC : NC;      // columns 0 .. NCOL - 1 may be in use
+    static constexpr int HL = NC <= 8 ? 8 : 16;             // rows of h (and of l) in a query buffer
+    static constexpr int NS = 2 * HL;                       // MMA N of S^T per head: h columns, then l columns
+    static constexpr int PW = (HP == 2 || NC > 8) ? 16 : 8; // columns of one term of u
+    static constexpr int NP = PW == 8 ? 32 : 48;            // MMA N of O^T: three terms (and padding to 16)
+    static constexpr uint32_t HeadBytes = kTile * D;        // one head's rows of a tile
+    static constexpr uint32_t StageBytes = 2 * HP * HeadBytes;
+    static constexpr uint32_t VOff = HP * HeadBytes;
+    static constexpr uint32_t QHeadBytes = NS * D;
+    static constexpr uint32_t QBufBytes = HP * QHeadBytes;
+    static constexpr int QBufs = kQBytes / QBufBytes < 4 ? kQBytes / QBufBytes : 4;
+    static constexpr uint32_t PBytes = kTile * NP;
+    static constexpr uint32_t SCols = HP * NS;
+    static constexpr uint32_t tS = 0, tO = 2 * SCols;
+    static constexpr uint32_t TmemCols = tO + 2 * NP <= 128 ? 128 : 256;
+    static constexpr size_t SmemBytes = 1024 + kStages * StageBytes + kQBytes + 2 * PBytes + sizeof(Misc);
+    static_assert(QBufs >= 2 && QBufs + 2 < kQRing, "query scales outlive their buffers");
+    static_assert(tO + 2 * NP <= 256, "TMEM");
+    static_assert(SmemBytes <= 227 * 1024, "shared memory");
+};
+
+template <int D, int NC, bool MQ, int HP>
+__global__ void __launch_bounds__(kThreads, 1)
+decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                     const DecodeFp8Params p) {
+    using C_ = Shape<D, NC, HP>;
+    constexpr int CW = C_::CW, NCOL = C_::NCOL, HL = C_::HL, NS = C_::NS, PW = C_::PW, NP = C_::NP;
+    constexpr uint32_t kLayout = D == 128 ? kLayoutSw128 : kLayoutSw64;
+    constexpr uint32_t kAtom = 8 * D;                 // eight rows: the swizzle's atom
+    constexpr uint32_t kIdescQK = idesc_e4m3(kTile, NS, 0, 0);   // A = K (K-major), B = Q (K-major)
+    constexpr uint32_t kIdescPV = idesc_e4m3(128, NP, 1, 1);     // A = V^T (MN-major), B = P^T (MN-major)
+    constexpr int64_t kSegCost = seg_cost<HP * NC, HP>();
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_addr = smem_u32(smem_raw);
+    uint8_t *smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+    uint8_t *stage_ptr = smem;
+    uint8_t *q_ptr = smem + kStages * C_::StageBytes;
+    uint8_t *p_ptr = q_ptr + kQBytes;
+    Misc *misc = reinterpret_cast<Misc *>(p_ptr + 2 * C_::PBytes);
+    const uint32_t stage_addr = smem_u32(stage_ptr);
+    const uint32_t q_addr = smem_u32(q_ptr);
+    const uint32_t p_addr = smem_u32(p_ptr);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c = blockIdx.x, C = gridDim.x;
+    // Hkv counts the tile's KV head groups (segments per sequence).
+    const int N = p.num_seqs, Hkv = p.num_kv_heads / HP, H = p.num_heads, B = p.block_size;
+    const int lgB = __ffs(B) - 1;
+    const int cap = min(p.max_seq_len, p.max_blocks_per_seq * B);
+    const int Gq = H / p.num_kv_heads, lgG = __ffs(Gq) - 1;     // query heads per KV head (a power of two)
+    Slot *slots = static_cast<Slot *>(p.tc_slots);
+    const uint64_t lim = kWaitLimitNs;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(smem_u32(&misc->full[i]), 1);
+            mbar_init(smem_u32(&misc->vfull[i]), 1);
+            mbar_init(smem_u32(&misc->sfull[i]), 32);
+            mbar_init(smem_u32(&misc->empty[i]), 1);
+        }
+        for (int i = 0; i < C_::QBufs; ++i) {
+            mbar_init(smem_u32(&misc->qfull[i]), 1);
+            mbar_init(smem_u32(&misc->qempty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&misc->s_full[i]), 1);
+            mbar_init(smem_u32(&misc->p_full[i]), 4);
+            mbar_init(smem_u32(&misc->o_full[i]), 1);
+            mbar_init(smem_u32(&misc->o_free[i]), 4);
+        }
+        mbar_init(smem_u32(&misc->drain), 1);
+        misc->abort = 0;
+        misc->never = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&misc->tmem_base), C_::TmemCols);
+        tmem_relinquish();
+    }
+    if (warp == 0 && lane == 0) {
+        prefetch_tmap(&tm_k);
+        prefetch_tmap(&tm_v);
+    }
+    // ---- this CTA's range of the flattened tile space, as in decode_tc_kernel:
+    // planned before the wait on the previous grid, checked after it.
+    const bool cached = N <= kLenCache;
+    const LenSrc lens{cached ? misc->lens : nullptr, p.seq_lens, cap};
+    int64_t T = 0;
+    int odd = 0;
+    auto first_tile = [&]() -> Walk {
+        Walk w{};
+        w.nh = Hkv;
+        w.ns = N;
+        w.s = misc->s0;
+        w.load(lens);
+        w.h = static_cast<int>(misc->rem0 / w.nt);
+        w.t = static_cast<int>(misc->rem0 % w.nt);
+        return w;
+    };
+    auto wait_prev = [&]() {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (threadIdx.x == 0 && slots) slots[2 * c].flag = 0;
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    };
+    bool ahead = cached;
+    if (cached) {
+        for (int s = threadIdx.x; s < N; s += kThreads) misc->lens[s] = ld_cg(p.seq_lens + s);
+        __syncthreads();
+    } else {
+        wait_prev();
+    }
+    for (;;) {
+        T = plan_range<kThreads>(lens, misc, N, Hkv, c, C, kSegCost, kTileCost, kTokCost, &odd);
+        if (!ahead) break;
+        ahead = false;
+        wait_prev();
+        int changed = 0;
+        for (int s = threadIdx.x; s < N; s += kThreads) changed |= ld_cg(p.seq_lens + s) != misc->lens[s];
+        if (!__syncthreads_or(changed)) break;
+        for (int s = threadIdx.x; s < N; s += kThreads) misc->lens[s] = ld_cg(p.seq_lens + s);
+        __syncthreads();
+    }
+    const int64_t beg = misc->bnd[0], end = misc->bnd[1];
+    if (threadIdx.x == 0 && slots) slots[2 * c].range_beg = beg;
+    const int n_tiles = static_cast<int>(end - beg);
+    // Lengths outside [0, cap] are reported, and empty sequences get zeros,
+    // by CTA s % C.
+    if (odd || MQ) {
+        for (int s = c; s < N; s += C) {
+            const int raw = lens.raw(s);
+            if ((raw < 0 || raw > cap) && threadIdx.x == 0) set_error(p.err, PK_DEVERR_SEQ_LEN);
+            const int L = lens(s);
+            if constexpr (MQ) {
+                // A sequence has at most L query tokens (they are its newest tokens).
+                const int r0 = p.cu_q_lens[s], r1 = p.cu_q_lens[s + 1];
+                const bool bad = r0 < 0 || r1 < r0 || r1 > p.total_q || r1 - r0 > p.q_len;
+                if ((bad || r1 - r0 > L) && threadIdx.x == 0) set_error(p.err, PK_DEVERR_SEQ_LEN);
+                if (L != 0 || bad) continue;
+                for (int64_t i = threadIdx.x; i < static_cast<int64_t>(r1 - r0) * H * D; i += kThreads)
+                    store_out(p, static_cast<size_t>(r0) * H * D + i, 0.f);
+            } else {
+                if (L != 0) continue;
+                for (int i = threadIdx.x; i < H * D; i += kThreads) store_out(p, static_cast<size_t>(s) * H * D + i, 0.f);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = misc->tmem_base;
+
+    Walk w0{};
+    w0.nh = Hkv;
+    w0.ns = N;
+    if (n_tiles > 0) w0 = first_tile();
+
+    // The sequence's query rows (first, number): its newest tokens.  Rows that
+    // are not within the queries given, or more than the columns hold, are
+    // none (reported above).
+    auto query_rows = [&](int s) -> int2 {
+        if constexpr (MQ) {
+            const int r0 = p.cu_q_lens[s], r1 = p.cu_q_lens[s + 1];
+            if (r0 < 0 || r1 < r0 || r1 > p.total_q || r1 - r0 > p.q_len) return make_int2(0, 0);
+            return make_int2(r0, r1 - r0);
+        } else {
+            return make_int2(s, 1);
+        }
+    };
+
+    if (warp == 0) {
+        // ================= producer =================
+        Walk w = w0;
+        const int MB = p.max_blocks_per_seq;
+        int issued = 0;
+        auto fetch = [&](const Walk &ww) -> int {
+            const int fp = ww.t * (kTile >> lgB);
+            return (lane < (kTile >> lgB) && fp + lane < MB)
+                       ? p.block_tables[static_cast<size_t>(ww.s) * MB + fp + lane] : -1;
+        };
+        int phys_next = n_tiles > 0 ? fetch(w) : -1;
+        for (int i = 0; i < n_tiles; ++i) {
+            const int st = i % kStages;
+            const int phys = phys_next;
+            int got = 1;
+            if (lane == 0)
+                got = mbar_wait(smem_u32(&misc->empty[st]), ((i / kStages) & 1) ^ 1, &misc->abort, lim);
+            if (!__shfl_sync(0xffffffffu, got, 0)) {      // one decision for the whole warp
+                if (lane == 0) {
+                    misc->abort = 1;
+                    set_error(p.err, PK_DEVERR_TIMEOUT);
+                }
+                break;
+            }
+            const int vlen = min(kTile, w.L - w.t * kTile);
+            const int pages = (vlen + B - 1) >> lgB;
+            bool ok = false;
+            if (lane < pages) {
+                ok = phys >= 0 && phys < p.num_blocks;
+                if (!ok) set_error(p.err, PK_DEVERR_BLOCK_ID);
+            }
+            uint32_t bits = 0;
+            const int r0 = lane << lgB;
+            if (ok) {
+                const int nrows = min(B, vlen - r0);
+                bits = (nrows >= 32 ? 0xffffffffu : ((1u << nrows) - 1u)) << (r0 & 31);
+            }
+            const int word = r0 >> 5;
+            const uint32_t m0 = __reduce_or_sync(0xffffffffu, word == 0 ? bits : 0u);
+            const uint32_t m1 = __reduce_or_sync(0xffffffffu, word == 1 ? bits : 0u);
+            const uint32_t m2 = __reduce_or_sync(0xffffffffu, word == 2 ? bits : 0u);
+            const uint32_t m3 = __reduce_or_sync(0xffffffffu, word == 3 ? bits : 0u);
+            const uint32_t nok = __popc(__ballot_sync(0xffffffffu, ok));
+            const uint32_t full = smem_u32(&misc->full[st]);
+            const uint32_t vfull = smem_u32(&misc->vfull[st]);
+            const uint32_t sbase = stage_addr + st * C_::StageBytes;
+            if (lane == 0) {
+                misc->mask[st][0] = m0;
+                misc->mask[st][1] = m1;
+                misc->mask[st][2] = m2;
+                misc->mask[st][3] = m3;
+                misc->meta[st] = make_int4(w.s, w.h, w.t, w.nt);
+                if constexpr (MQ) {
+                    const int2 qr = query_rows(w.s);
+                    misc->qmeta[st] = make_int4(qr.x, qr.y, w.L - qr.y, 0);
+                }
+                mbar_arrive_expect_tx(full, nok * (HP * D) << lgB);
+                mbar_arrive_expect_tx(vfull, nok * (HP * D) << lgB);
+            }
+            __syncwarp();
+            if (ok) {
+                // The (block, head) piece: B rows of D bytes, at the page's place in each head's tile.
+                const int piece = phys * p.num_kv_heads + w.h * HP;
+                const uint32_t at = sbase + static_cast<uint32_t>(r0) * D;
+#pragma unroll
+                for (int hd = 0; hd < HP; ++hd)
+                    tma_load_3d(at + hd * C_::HeadBytes, &tm_k, full, 0, 0, piece + hd);
+#pragma unroll
+                for (int hd = 0; hd < HP; ++hd)
+                    tma_load_3d(at + C_::VOff + hd * C_::HeadBytes, &tm_v, vfull, 0, 0, piece + hd);
+#pragma unroll
+                for (int hd = 0; hd < HP; ++hd) {
+                    cp_async4(smem_u32(&misc->scales[st][lane][0][hd]), p.k_scales + piece + hd);
+                    cp_async4(smem_u32(&misc->scales[st][lane][1][hd]), p.v_scales + piece + hd);
+                }
+            }
+            cp_async_arrive(smem_u32(&misc->sfull[st]));
+            ++issued;
+            w.next(lens);
+            if (i + 1 < n_tiles) phys_next = fetch(w);
+        }
+        cp_async_wait_all();
+        // On abort, let this warp's copies land before the CTA can exit.
+        if (misc->abort && lane == 0) {
+            for (int i = max(0, issued - kStages); i < issued; ++i) {
+                mbar_wait(smem_u32(&misc->full[i % kStages]), (i / kStages) & 1, &misc->never, lim);
+                mbar_wait(smem_u32(&misc->vfull[i % kStages]), (i / kStages) & 1, &misc->never, lim);
+            }
+        }
+    } else if (warp == 1) {
+        // ================= MMA issuer =================
+        if (lane == 0) {
+            int pv_seg = -1, qk_seg = -1;
+            auto pv = [&](int j, bool first, int sg) {
+                const int pb = j & 1;
+                tc_fence_after();
+                const uint32_t vbase = stage_addr + (j % kStages) * C_::StageBytes + C_::VOff;
+                const uint32_t pbase = p_addr + pb * C_::PBytes;
+#pragma unroll
+                for (int kk = 0; kk < kTile / 32; ++kk) {
+                    // Tokens 32 kk .. 32 kk + 31: four 8-row atoms of V.  Head dim 64: the second
+                    // 64 rows of O^T come from the pair's second head (HP == 2) or are not used.
+                    const uint64_t a = smem_desc(vbase + kk * 4 * kAtom, HP == 2 ? C_::HeadBytes : kAtom, kAtom, kLayout);
+                    const uint64_t b = smem_desc(pbase + kk * 32 * NP, 8 * NP, 128, kLayoutNone);
+                    mma_e4m3(tmem + C_::tO + (sg & 1) * NP, a, b, kIdescPV, (first && kk == 0) ? 0u : 1u);
+                }
+                mma_commit(smem_u32(&misc->o_full[pb]));
+                mma_commit(smem_u32(&misc->empty[j % kStages]));
+            };
+            auto qk = [&](int i, int sg, bool last) {
+                tc_fence_after();
+                const uint32_t kbase = stage_addr + (i % kStages) * C_::StageBytes;
+                const uint32_t qbase = q_addr + (sg % C_::QBufs) * C_::QBufBytes;
+#pragma unroll
+                for (int hd = 0; hd < HP; ++hd) {
+#pragma unroll
+                    for (int kk = 0; kk < D / 32; ++kk) {
+                        const uint64_t a = smem_desc(kbase + hd * C_::HeadBytes + kk * 32, 16, kAtom, kLayout);
+                        const uint64_t b = smem_desc(qbase + hd * C_::QHeadBytes + kk * 256, 128, 8 * D, kLayoutNone);
+                        mma_e4m3(tmem + C_::tS + (i & 1) * C_::SCols + hd * NS, a, b, kIdescQK, kk > 0 ? 1u : 0u);
+                    }
+                }
+                mma_commit(smem_u32(&misc->s_full[i & 1]));
+                if (last) mma_commit(smem_u32(&misc->qempty[sg % C_::QBufs]));
+            };
+            // Event loop, as in decode_tc_kernel; the scores of a segment's
+            // first tile also wait for its queries.
+            int nq = 0, np = 0;
+            uint64_t t_idle = 0;
+            uint32_t spins = 0;
+            while (np < n_tiles) {
+                bool prog = false;
+                if (np < nq && mbar_test_wait(smem_u32(&misc->p_full[np & 1]), (np >> 1) & 1) &&
+                    mbar_test_wait(smem_u32(&misc->vfull[np % kStages]), (np / kStages) & 1)) {
+                    const bool first = np == 0 || misc->meta[np % kStages].z == 0;
+                    const int sg = pv_seg + (first ? 1 : 0);
+                    // A new segment's O buffer must have been read out (segment sg - 2).
+                    if (!first || mbar_test_wait(smem_u32(&misc->o_free[sg & 1]), ((sg >> 1) & 1) ^ 1)) {
+                        pv(np, first, sg);
+                        pv_seg = sg;
+                        ++np;
+                        prog = true;
+                    }
+                }
+                if (nq < n_tiles && nq <= np + 1 &&
+                    mbar_test_wait(smem_u32(&misc->full[nq % kStages]), (nq / kStages) & 1)) {
+                    const int4 mt = misc->meta[nq % kStages];
+                    const bool first = nq == 0 || mt.z == 0;
+                    const int sg = qk_seg + (first ? 1 : 0);
+                    if (!first || mbar_test_wait(smem_u32(&misc->qfull[sg % C_::QBufs]), (sg / C_::QBufs) & 1)) {
+                        qk(nq, sg, nq == n_tiles - 1 || mt.z == mt.w - 1);
+                        qk_seg = sg;
+                        ++nq;
+                        prog = true;
+                    }
+                }
+                if (prog) {
+                    spins = 0;
+                } else if ((++spins & 255u) == 0) {
+                    const uint64_t now = globaltimer_ns();
+                    if (spins == 256) t_idle = now;
+                    else if (misc->abort || now - t_idle > lim) {
+                        misc->abort = 1;
+                        set_error(p.err, PK_DEVERR_TIMEOUT);
+                        break;
+                    }
+                }
+            }
+            // Let every issued MMA finish before the CTA can release TMEM.
+            mma_commit(smem_u32(&misc->drain));
+            mbar_wait(smem_u32(&misc->drain), 0, &misc->never, lim);
+        }
+        __syncwarp();
+    } else if (warp >= 6) {
+        // ================= queries =================
+        // Warp 6 takes the even segments, warp 7 the odd ones.
+        constexpr int kE = D / 32;                    // elements of a row a lane holds
+        Walk w = w0;
+        int i = 0;
+        for (int sg = 0; i < n_tiles; ++sg) {
+            const int left = min(w.nt - w.t, n_tiles - i);
+            if ((sg & 1) == warp - 6) {
+                const int2 qr = query_rows(w.s);
+                uint32_t raw[HP][NC][kE / 2];
+#pragma unroll
+                for (int hd = 0; hd < HP; ++hd) {
+#pragma unroll
+                    for (int cq = 0; cq < NC; ++cq) {
+                        // Column cq: query token cq / G, query head cq % G of the KV head.
+                        const int r = cq >> lgG;
+#pragma unroll
+                        for (int x = 0; x < kE / 2; ++x) raw[hd][cq][x] = 0;
+                        if (r < qr.y) {
+                            const size_t head = static_cast<size_t>(qr.x + r) * H + (w.h * HP + hd) * Gq + (cq & (Gq - 1));
+                            const uint16_t *src = p.q + head * D + lane * kE;
+                            if constexpr (kE == 4) {
+                                const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src));
+                                raw[hd][cq][0] = v.x;
+                                raw[hd][cq][1] = v.y;
+                            } else {
+                                raw[hd][cq][0] = __ldg(reinterpret_cast<const uint32_t *>(src));
+                            }
+                        }
+                    }
+                }
+                const int qb = sg % C_::QBufs;
+                int got = 1;
+                if (lane == 0)
+                    got = mbar_wait(smem_u32(&misc->qempty[qb]), ((sg / C_::QBufs) & 1) ^ 1, &misc->abort, lim);
+                if (!__shfl_sync(0xffffffffu, got, 0)) {
+                    if (lane == 0) {
+                        misc->abort = 1;
+                        set_error(p.err, PK_DEVERR_TIMEOUT);
+                    }
+                    break;
+                }
+                uint8_t *buf = q_ptr + qb * C_::QBufBytes;
+#pragma unroll
+                for (int hd = 0; hd < HP; ++hd) {
+#pragma unroll
+                    for (int cq = 0; cq < NC; ++cq) {
+                        // The row's largest magnitude: bf16 bits without the sign order as integers.
+                        uint32_t top = 0;
+#pragma unroll
+                        for (int x = 0; x < kE / 2; ++x) {
+                            const uint32_t v = raw[hd][cq][x] & 0x7fff7fffu;
+                            top = max(top, max(v & 0xffffu, v >> 16));
+                        }
+                        top = __reduce_max_sync(0xffffffffu, top);
+                        // 2^k brings it to [128, 256); |k| <= 120 keeps 2^k and 2^-k normal.
+                        const int k = min(7 - (max(static_cast<int>(top >> 7), 1) - 127), 120);
+                        const bool finite = top < 0x7f80u;
+                        const float up = __uint_as_float(static_cast<uint32_t>((finite ? k : 0) + 127) << 23);
+                        if (lane == 0)
+                            misc->qscale[sg % kQRing][hd * CW + cq] =
+                                finite ? __uint_as_float(static_cast<uint32_t>(127 - k) << 23) : __int_as_float(0x7fffffff);
+                        uint32_t hi = 0, lo = 0;
+#pragma unroll
+                        for (int x = 0; x < kE / 2; ++x) {
+                            const float a = bf16_lo(raw[hd][cq][x]) * up, b = bf16_hi(raw[hd][cq][x]) * up;
+                            const uint32_t h2 = e4m3x2(a, b);
+                            float ha, hb;
+                            e4m3x2_to_float(h2, ha, hb);
+                            hi |= h2 << (16 * x);
+                            lo |= e4m3x2((a - ha) * 32.f, (b - hb) * 32.f) << (16 * x);
+                        }
+                        // K-major, no swizzle: 8 rows of 16 bytes side by side, 128 bytes
+                        // to the next 16 of the row, 8 D to the next 8 rows.
+                        const int byte = lane * kE;
+                        uint8_t *dst = buf + hd * C_::QHeadBytes + (cq >> 3) * 8 * D + (byte >> 4) * 128 + (cq & 7) * 16 +
+                                       (byte & 15);
+                        if constexpr (kE == 4) {
+                            *reinterpret_cast<uint32_t *>(dst) = hi;
+                            *reinterpret_cast<uint32_t *>(dst + HL * D) = lo;
+                        } else {
+                            *reinterpret_cast<uint16_t *>(dst) = static_cast<uint16_t>(hi);
+                            *reinterpret_cast<uint16_t *>(dst + HL * D) = static_cast<uint16_t>(lo);
+                        }
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&misc->qfull[qb]));
+            }
+            i += left;
+            w.t += left - 1;
+            w.next(lens);
+        }
+    } else {
+        // ================= softmax (warps 2-5): thread <-> tile row =================
+        const int quad = warp & 3;
+        const int row = quad * 32 + lane;
+        const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+        // Columns: HP == 1, query column j; HP == 2, 0-7 the pair's first head's and 8-15 the second's.
+        float qf[NCOL], m_ref[NCOL], l_run[NCOL], m_prev[NCOL], l_prev[NCOL];
+#pragma unroll
+        for (int j = 0; j < NCOL; ++j) qf[j] = m_ref[j] = l_run[j] = m_prev[j] = l_prev[j] = 0.f;
+        const int hr = HP == 2 ? row >> 6 : 0;          // head of the pair of this O^T row
+        const int dd = HP == 2 ? (row & 63) : row;      // its element
+        const bool row_ok = HP == 2 || row < D;
+        int seg = -1, seg_t0 = 0, seg_i0 = 0;
+        bool pending = false;            // a finished segment awaits its read-out
+        int pend_seg = 0, pend_s = 0, pend_h = 0, pend_i = 0, pend_t0 = 0, pend_i0 = 0, pend_q0 = 0, pend_qn = 1;
+        bool pend_complete = false, pend_cut_end = false;
+        auto finalize = [&]() -> bool {
+            // P.V of the segment's last tile (pend_i) complete.
+            if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&misc->o_full[pend_i & 1]), (pend_i >> 1) & 1,
+                                                   &misc->never, lim)))
+                return false;
+            tc_fence_after();
+            // The three terms, smallest first.
+            float ov[PW];
+            {
+                const uint32_t oaddr = lane_addr + C_::tO + (pend_seg & 1) * NP;
+                float o1[PW], o2[PW], o3[PW];
+                tmem_ld<PW>(oaddr, o1);
+                tmem_ld<PW>(oaddr + PW, o2);
+                tmem_ld<PW>(oaddr + 2 * PW, o3);
+#pragma unroll
+                for (int j = 0; j < PW; ++j) ov[j] = fmaf(o3[j], kLevel3, fmaf(o2[j], kLevel2, o1[j]));
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&misc->o_free[pend_seg & 1]));
+#pragma unroll
+            for (int j = 0; j < NCOL; ++j) {
+                const float v = warp_sum(l_prev[j]);
+                if (lane == 0) misc->lsum[quad][j] = v;
+            }
+            named_bar_sync(1, 128);
+            float l[NC], o[NC];
+#pragma unroll
+            for (int cq = 0; cq < NC; ++cq) {
+                const int j = hr * CW + cq;
+                l[cq] = misc->lsum[0][j] + misc->lsum[1][j] + misc->lsum[2][j] + misc->lsum[3][j];
+                if constexpr (HP == 2) o[cq] = hr ? ov[8 + cq] : ov[cq];
+                else o[cq] = ov[cq];
+            }
+            if (pend_complete) {
+                if (row_ok) {
+#pragma unroll
+                    for (int cq = 0; cq < NC; ++cq) {
+                        if ((cq >> lgG) >= pend_qn) continue;      // a padded query column
+                        const size_t qrow = static_cast<size_t>(MQ ? pend_q0 : pend_s) + (cq >> lgG);
+                        const int qh = (pend_h * HP + hr) * Gq + (cq & (Gq - 1));
+                        store_out(p, (qrow * H + qh) * D + dd, l[cq] != 0.f ? o[cq] / l[cq] : 0.f);
+                    }
+                }
+            } else {
+                // A cut part: slot 0 if the segment is this CTA's first, 1 if not.
+                const int slot_idx = pend_i0 == 0 ? 0 : 1;
+                Slot *sl = slots + 2 * c + slot_idx;
+                if (row_ok) {
+#pragma unroll
+                    for (int cq = 0; cq < NC; ++cq) sl->o[(hr * CW + cq) * 128 + row] = o[cq];
+                }
+                if (dd == 0 && row_ok) {
+#pragma unroll
+                    for (int cq = 0; cq < NC; ++cq) sl->l[hr * CW + cq] = l[cq];
+                }
+                if (row == 0) {
+#pragma unroll
+                    for (int j = 0; j < NCOL; ++j) sl->m[j] = m_prev[j];
+                    sl->s = pend_s;
+                    sl->h = pend_h;
+                    sl->start_tile = beg + pend_i0 - pend_t0;
+                    sl->total_tiles = T;
+                    // Cut at its start and finished here: this CTA merges it.
+                    if (slot_idx == 0) {
+                        sl->flag = (pend_t0 > 0 && pend_cut_end) ? 1 : 0;
+                        sl->first_cta = misc->first_cta;
+                    }
+                }
+            }
+            pending = false;
+            return true;
+        };
+        for (int i = 0; i < n_tiles; ++i) {
+            const int st = i % kStages;
+            const int sb = i & 1;
+            if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&misc->s_full[sb]), (i >> 1) & 1, &misc->never, lim) &&
+                                             mbar_wait(smem_u32(&misc->sfull[st]), (i / kStages) & 1, &misc->never, lim))) {
+                misc->abort = 1;
+                set_error(p.err, PK_DEVERR_TIMEOUT);
+                break;
+            }
+            const int4 mt = misc->meta[st];   // (s, h, t, nt), written with the stage
+            int4 qm = make_int4(mt.x, 1, 0, 0);
+            if constexpr (MQ) qm = misc->qmeta[st];  // (first query row, query tokens, first query position)
+            const bool seg_first = (i == 0) || (mt.z == 0);
+            const bool seg_last = (i == n_tiles - 1) || (mt.z == mt.w - 1);
+            if (seg_first) {
+                ++seg;
+                seg_t0 = mt.z;
+                seg_i0 = i;
+#pragma unroll
+                for (int j = 0; j < NCOL; ++j) {
+                    m_ref[j] = -INFINITY;
+                    l_run[j] = 0.f;
+                    if ((j % CW) < NC) qf[j] = misc->qscale[seg % kQRing][j] * p.scale_log2;
+                }
+            }
+            tc_fence_after();
+            // Scores: h columns plus 1/32 of the l columns.
+            float sv[NCOL];
+            const uint32_t saddr = lane_addr + C_::tS + sb * C_::SCols;
+            if constexpr (HP == 2 || NS == 32) {
+                float x[32];
+                tmem_ld32(saddr, x);
+#pragma unroll
+                for (int j = 0; j < NCOL; ++j) {
+                    if constexpr (HP == 2) sv[j] = fmaf(x[(j >> 3) * 16 + 8 + (j & 7)], kLevel2, x[(j >> 3) * 16 + (j & 7)]);
+                    else sv[j] = fmaf(x[16 + j], kLevel2, x[j]);
+                }
+            } else {
+                float x[16];
+                tmem_ld16(saddr, x);
+#pragma unroll
+                for (int j = 0; j < NCOL; ++j) sv[j] = fmaf(x[8 + j], kLevel2, x[j]);
+            }
+            // The token's scales; one that is out of range hides the token's head.
+            const bool in_page = (misc->mask[st][row >> 5] >> (row & 31)) & 1u;
+            bool valid[HP];
+            float ks[HP], lv[HP], ivs[HP];
+#pragma unroll
+            for (int hd = 0; hd < HP; ++hd) {
+                const float k1 = misc->scales[st][row >> lgB][0][hd], v1 = misc->scales[st][row >> lgB][1][hd];
+                valid[hd] = in_page && scale_ok(k1) && scale_ok(v1);
+                if (in_page && !valid[hd]) set_error(p.err, PK_DEVERR_SCALE);
+                ks[hd] = k1;
+                const uint32_t b = __float_as_uint(v1);
+                lv[hd] = (b & 0x7fffffu) ? __log2f(v1) : static_cast<float>(static_cast<int>(b >> 23) - 127);
+                ivs[hd] = 1.f / v1;
+            }
+            float t2[NCOL];
+            bool need = false;
+            const int jpos = mt.z * kTile + row;          // this row's token position
+#pragma unroll
+            for (int j = 0; j < NCOL; ++j) {
+                const int hd = HP == 2 ? j >> 3 : 0;
+                if ((j % CW) >= NC) {                      // padding column of a head pair
+                    t2[j] = -INFINITY;
+                    continue;
+                }
+                // Query column j % CW is query token (j % CW) / G, which sees positions <= its own.
+                const bool see = valid[hd] && (!MQ || jpos <= qm.z + ((j % CW) >> lgG));
+                t2[j] = see ? fmaf(sv[j], qf[j] * ks[hd], lv[hd]) : -INFINITY;
+                need |= t2[j] > m_ref[j] + kHeadroom;
+            }
+            if (named_bar_or(1, 128, need)) {
+                // Rare: move the references to the running maxima less kStart.
+#pragma unroll
+                for (int j = 0; j < NCOL; ++j) {
+                    const float mx = warp_max_redux(t2[j]);
+                    if (lane == 0) misc->red[quad][j] = mx;
+                }
+                named_bar_sync(1, 128);
+                float a[NCOL];
+#pragma unroll
+                for (int j = 0; j < NCOL; ++j) {
+                    const float t = fmaxf(fmaxf(misc->red[0][j], misc->red[1][j]),
+                                          fmaxf(misc->red[2][j], misc->red[3][j]));
+                    const float mn = fmaxf(m_ref[j], t - kStart);
+                    a[j] = m_ref[j] == -INFINITY ? 0.f : fast_exp2(m_ref[j] - mn);
+                    l_run[j] *= a[j];
+                    m_ref[j] = mn;
+                }
+                if (!seg_first) {
+                    // O through tile i-1, in TMEM (thread <-> head-dim row).
+                    if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&misc->o_full[(i - 1) & 1]), ((i - 1) >> 1) & 1,
+                                                           &misc->never, lim))) {
+                        misc->abort = 1;
+                        set_error(p.err, PK_DEVERR_TIMEOUT);
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t oaddr = lane_addr + C_::tO + (seg & 1) * NP;
+#pragma unroll
+                    for (int q = 0; q < 3 * PW / 8; ++q) {
+                        float o8[8];
+                        tmem_ld<8>(oaddr + 8 * q, o8);
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) {
+                            const int j = (8 * q + x) % PW;
+                            if (j < NCOL) o8[x] *= a[j < NCOL ? j : 0];
+                        }
+                        tmem_st8(oaddr + 8 * q, o8);
+                    }
+                }
+                // red[] is rewritten only in a later rare path, after the next vote.
+            }
+            // Weights in their three terms: words[term][4 columns].
+            uint32_t words[3][PW / 4];
+#pragma unroll
+            for (int x = 0; x < PW / 4; ++x) words[0][x] = words[1][x] = words[2][x] = 0;
+#pragma unroll
+            for (int j = 0; j < NCOL; j += 2) {
+                if ((j % CW) >= NC) continue;              // padding columns: weight 0
+                float u[2];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int jj = j + x < NCOL ? j + x : j;
+                    const bool used = j + x < NCOL && ((j + x) % CW) < NC;
+                    u[x] = used && t2[jj] != -INFINITY ? fast_exp2(t2[jj] - m_ref[jj]) : 0.f;
+                    if (used) l_run[jj] = fmaf(u[x], ivs[HP == 2 ? jj >> 3 : 0], l_run[jj]);
+                }
+                const uint32_t h1 = e4m3x2(u[0], u[1]);
+                float b0, b1;
+                e4m3x2_to_float(h1, b0, b1);
+                const float r0 = (u[0] - b0) * 32.f, r1 = (u[1] - b1) * 32.f;
+                const uint32_t h2 = e4m3x2(r0, r1);
+                e4m3x2_to_float(h2, b0, b1);
+                // Beyond 448 / 2048 the third term stops at 448: 2^-10 of u at most is left.
+                const uint32_t h3 = e4m3x2((r0 - b0) * 2048.f, (r1 - b1) * 2048.f);
+                const int sh = (j & 2) * 8;
+                words[0][j >> 2] |= h1 << sh;
+                words[1][j >> 2] |= h2 << sh;
+                words[2][j >> 2] |= h3 << sh;
+            }
+            // P buffer sb is free once P.V of tile i-2 is done.
+            if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&misc->o_full[sb]), ((i >> 1) & 1) ^ 1, &misc->never,
+                                                   lim))) {
+                misc->abort = 1;
+                set_error(p.err, PK_DEVERR_TIMEOUT);
+                break;
+            }
+            // Rows of hidden tokens are zeroed once this tile's V has landed: the
+            // MMA multiplies every V row by its weight, and theirs may hold stale
+            // bytes or NaN.
+            const bool hide = !valid[0] || !valid[HP - 1];
+            if (__any_sync(0xffffffffu, hide) &&
+                !__all_sync(0xffffffffu, mbar_wait(smem_u32(&misc->vfull[st]), (i / kStages) & 1, &misc->never,
+                                                   lim))) {
+                misc->abort = 1;
+                set_error(p.err, PK_DEVERR_TIMEOUT);
+                break;
+            }
+            if (hide) {
+#pragma unroll
+                for (int hd = 0; hd < HP; ++hd) {
+                    if (valid[hd]) continue;
+                    uint4 *vrow = reinterpret_cast<uint4 *>(stage_ptr + st * C_::StageBytes + C_::VOff +
+                                                            hd * C_::HeadBytes + row * D);
+#pragma unroll
+                    for (int x = 0; x < D / 16; ++x) vrow[x] = make_uint4(0, 0, 0, 0);
+                }
+            }
+            // MN-major, no swizzle: 16 columns side by side, 8 tokens 16 bytes
+            // apart, 128 bytes to the next 16 columns, 8 NP to the next 8 tokens.
+            uint8_t *prow = p_ptr + sb * C_::PBytes + (row >> 3) * (8 * NP) + (row & 7) * 16;
+            if constexpr (PW == 8) {
+                *reinterpret_cast<uint4 *>(prow) = make_uint4(words[0][0], words[0][1], words[1][0], words[1][1]);
+                *reinterpret_cast<uint4 *>(prow + 128) = make_uint4(words[2][0], words[2][1], 0, 0);
+            } else {
+#pragma unroll
+                for (int x = 0; x < 3; ++x)
+                    *reinterpret_cast<uint4 *>(prow + 128 * x) =
+                        make_uint4(words[x][0], words[x][1], words[x][PW / 4 - 2], words[x][PW / 4 - 1]);
+            }
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&misc->p_full[sb]));
+
+            // The previous segment's read-out, one tile late.
+            if (pending && !finalize()) {
+                misc->abort = 1;
+                set_error(p.err, PK_DEVERR_TIMEOUT);
+                break;
+            }
+            if (seg_last) {
+                pending = true;
+                pend_seg = seg;
+                pend_s = mt.x;
+                pend_q0 = qm.x;
+                pend_qn = qm.y;
+                pend_h = mt.y;
+                pend_i = i;
+                pend_t0 = seg_t0;
+                pend_i0 = seg_i0;
+                pend_complete = seg_t0 == 0 && mt.z == mt.w - 1;
+                pend_cut_end = mt.z == mt.w - 1;
+#pragma unroll
+                for (int j = 0; j < NCOL; ++j) {
+                    m_prev[j] = m_ref[j];
+                    l_prev[j] = l_run[j];
+                }
+                if (i == n_tiles - 1 && !finalize()) {
+                    misc->abort = 1;
+                    set_error(p.err, PK_DEVERR_TIMEOUT);
+                    break;
+                }
+            }
+        }
+        tc_fence_before();
+    }
+
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C_::TmemCols);
+    }
+}
+
+// ---------------------------------------------------------------- host side
+PFN_cuTensorMapEncodeTiled_v12000 get_encoder() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+        else
+            cudaGetLastError();
+    });
+    return fn;
+}
+
+// [P Hkv] pieces of B rows of D bytes, one piece a box.
+bool encode_piece_map(CUtensorMap *m, const void *base, const DecodeFp8Params &p) {
+    auto enc = get_encoder();
+    if (!enc) return false;
+    const cuuint64_t D = p.head_dim, B = p.block_size;
+    const cuuint64_t pieces = static_cast<cuuint64_t>(p.num_blocks > 0 ? p.num_blocks : 1) * p.num_kv_heads;
+    cuuint64_t dims[3] = {D, B, pieces};
+    cuuint64_t strides[2] = {D, B * D};
+    cuuint32_t box[3] = {static_cast<cuuint32_t>(D), static_cast<cuuint32_t>(B), 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int NC, int HP>
+cudaError_t launch_shape(const DecodeFp8Params &p, int C, cudaStream_t stream) {
+    CUtensorMap mk, mv;
+    if (!encode_piece_map(&mk, p.k8, p) || !encode_piece_map(&mv, p.v8, p)) return cudaErrorInvalidValue;
+    auto *kernel = p.cu_q_lens ? decode_fp8_tc_kernel<D, NC, true, HP> : decode_fp8_tc_kernel<D, NC, false, HP>;
+    constexpr size_t smem = Shape<D, NC, HP>::SmemBytes;
+    cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(kernel), static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(C);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, mk, mv, p);
+    if (e != cudaSuccess) return e;
+    if (!p.tc_slots) return cudaSuccess;   // no sequence longer than one tile: nothing is cut
+    cfg.blockDim = dim3(128);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, decode_tc_merge_kernel<D, NC, HP, true>, static_cast<const DecodeParams &>(p), C);
+}
+
+template <int NC>
+cudaError_t launch_dim(const DecodeFp8Params &p, int C, cudaStream_t stream) {
+    if (p.head_dim == 128) return launch_shape<128, NC, 1>(p, C, stream);
+    if constexpr (NC <= 8) {
+        if (p.num_kv_heads % 2 == 0) return launch_shape<64, NC, 2>(p, C, stream);
+    }
+    return launch_shape<64, NC, 1>(p, C, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_decode_fp8_tensor_core(const DecodeFp8Params &p, cudaStream_t stream) {
+    const int C = std::min(sm_count(), static_cast<int>(kMaxCtas));
+    if (C <= 0) return cudaErrorNoDevice;
+    // MMA columns: the group's query heads times the query tokens per sequence.
+    switch ((p.num_heads / p.num_kv_heads) * (p.cu_q_lens ? p.q_len : 1)) {
+        case 1: return launch_dim<1>(p, C, stream);
+        case 2: return launch_dim<2>(p, C, stream);
+        case 4: return launch_dim<4>(p, C, stream);
+        case 8: return launch_dim<8>(p, C, stream);
+        case 16: return launch_dim<16>(p, C, stream);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace pk

@@ -1,0 +1,129 @@
+// Rotary position angles (sm_103a) and what the two rotary appends share.
+#pragma once
+
+#include "common.cuh"
+
+namespace pk {
+
+// A frequency f (radians a position) in turns a position, as a 64-bit binary
+// fraction: the integer nearest below f / (2 pi) * 2^64, modulo 2^64 (whole
+// turns do not matter, since positions are integers).
+//
+// Why fixed point: at position 100,000 an angle in fp32 is off by 0.004
+// radians (its spacing there), and what a rotation needs is the angle modulo
+// a turn.  position * turns in 64-bit integers is exact modulo a turn, so the
+// error is that of the fraction alone, 2^-64 turns a position: below 2^-33
+// turns for every 31-bit position, at the price of two integer multiplies.
+//
+// f = m 2^e with m < 2^24, and 1 / (2 pi) = K 2^-96 (from the series of pi),
+// so the fraction is (m K) >> (32 - e); m K has at most 118 bits.  A
+// frequency that is not finite or not below 2^32 gives 0 (no rotation).
+PK_DEV uint64_t turns_per_position(float f) {
+    const uint32_t b = __float_as_uint(f);
+    const int field = static_cast<int>((b >> 23) & 0xffu);
+    if (field == 0 || field >= 127 + 32) return 0;      // zero, below 2^-126, or too large
+    const uint64_t m = (b & 0x7fffffu) | 0x800000u;
+    const int shift = 32 - (field - 150);               // 24 .. 181
+    if (shift >= 128) return 0;
+    constexpr uint64_t kHi = 0x28be60dbull, kLo = 0x9391054a7f09d5f4ull;   // K = kHi 2^64 + kLo
+    const unsigned __int128 prod = static_cast<unsigned __int128>(m) * kLo +
+                                   (static_cast<unsigned __int128>(m * kHi) << 64);
+    const uint64_t t = static_cast<uint64_t>(prod >> shift);
+    return (b & 0x80000000u) ? 0ull - t : t;
+}
+
+// cos and sin of position * frequency, times `factor`.  The nearest quarter
+// turn is taken off in integers, so that the rest, at most an eighth of a
+// turn, keeps 24 significant bits as fp32.
+PK_DEV float2 rotation(int64_t position, uint64_t turns, float factor) {
+    const uint64_t a = static_cast<uint64_t>(position) * turns;
+    const uint32_t quarter = static_cast<uint32_t>((a + (1ull << 61)) >> 62);
+    const int64_t rest = static_cast<int64_t>(a - (static_cast<uint64_t>(quarter) << 62));
+    float s, c;
+    sincospif(static_cast<float>(rest) * 0x1p-63f, &s, &c);     // rest 2^-63 half turns
+    if (quarter & 1) {
+        const float t = c;
+        c = -s;
+        s = t;
+    }
+    if (quarter & 2) {
+        c = -c;
+        s = -s;
+    }
+    return make_float2(c * factor, s * factor);
+}
+
+// 16-byte load of data that the same call may write elsewhere (a rotation in
+// place): no read-only path, no place in L1.
+PK_DEV uint4 ld_stream(const void *p) {
+    uint4 r;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");
+    return r;
+}
+
+PK_DEV uint4 pack8(const float f[8]) {
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                      pack_bf16x2(f[6], f[7]));
+}
+
+// A head's D elements are handled in units of two 8-element vectors: of the
+// first `rot` elements, unit j < rot / 16 has those at 8 j and rot / 2 + 8 j
+// (in the half layout each other's partners), of the others those at
+// rot + 8 (j - rot / 16) and half of the rest further on.  Neighbouring
+// lanes then touch neighbouring vectors in either layout.
+PK_DEV int2 unit_offsets(int j, int rot, int D) {
+    const int n = rot >> 4;
+    if (j < n) return make_int2(8 * j, (rot >> 1) + 8 * j);
+    const int a = rot + 8 * (j - n);
+    return make_int2(a, a + ((D - rot) >> 1));
+}
+
+// Rotate unit j < rot / 16: `a` and `b` are its two vectors, cs the token's
+// (cos, sin) of pair 0 .. rot / 2 - 1.
+template <bool kInterleaved>
+PK_DEV void rotate_unit(float (&a)[8], float (&b)[8], const float2 *cs, int j, int rot) {
+    if constexpr (kInterleaved) {
+        // Pairs lie in neighbouring elements: four in each vector.
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 ca = cs[4 * j + i], cb = cs[(rot >> 2) + 4 * j + i];
+            const float a0 = a[2 * i], a1 = a[2 * i + 1], b0 = b[2 * i], b1 = b[2 * i + 1];
+            a[2 * i] = a0 * ca.x - a1 * ca.y;
+            a[2 * i + 1] = a1 * ca.x + a0 * ca.y;
+            b[2 * i] = b0 * cb.x - b1 * cb.y;
+            b[2 * i + 1] = b1 * cb.x + b0 * cb.y;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float2 c = cs[8 * j + i];
+            const float x = a[i], y = b[i];
+            a[i] = x * c.x - y * c.y;
+            b[i] = y * c.x + x * c.y;
+        }
+    }
+}
+
+// Host-side checks that both rotary appends share: sizes, token strides (in
+// elements, whole 16-byte vectors) and the rotation's own arguments.
+inline int check_rope_args(int64_t q_out_stride, int64_t q_stride, int64_t k_stride, int64_t v_stride, int rot_dim,
+                           float factor, int num_tokens, int num_heads, int num_kv_heads, int head_dim,
+                           int num_blocks, int block_size) {
+    if (num_tokens < 0 || num_heads < 0 || num_kv_heads <= 0 || num_blocks < 0 || block_size <= 0) return PK_ERR_SHAPE;
+    if (head_dim != 64 && head_dim != 128) return PK_ERR_UNSUPPORTED;
+    if (block_size != 8 && block_size != 16 && block_size != 32) return PK_ERR_UNSUPPORTED;
+    if (num_heads > 65535 || num_kv_heads > 32767) return PK_ERR_SHAPE;
+    if (rot_dim < 0 || rot_dim > head_dim) return PK_ERR_SHAPE;
+    if (rot_dim % 16) return PK_ERR_UNSUPPORTED;
+    if (!(factor >= 0x1p-20f && factor <= 0x1p20f)) return PK_ERR_SHAPE;
+    const int64_t q_row = static_cast<int64_t>(num_heads) * head_dim;
+    const int64_t kv_row = static_cast<int64_t>(num_kv_heads) * head_dim;
+    if (num_heads > 0 && (q_stride < q_row || q_out_stride < q_row)) return PK_ERR_SHAPE;
+    if (k_stride < kv_row || v_stride < kv_row) return PK_ERR_SHAPE;
+    if ((num_heads > 0 && (q_stride % 8 || q_out_stride % 8)) || k_stride % 8 || v_stride % 8)
+        return PK_ERR_ALIGNMENT;
+    return PK_OK;
+}
+
+}  // namespace pk
