@@ -720,9 +720,10 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             float ks[HP], lv[HP], ivs[HP];
 #pragma unroll
             for (int hd = 0; hd < HP; ++hd) {
-                const float k1 = misc->scales[st][row >> lgB][0][hd], v1 = misc->scales[st][row >> lgB][1][hd];
+                float k1 = misc->scales[st][row >> lgB][0][hd], v1 = misc->scales[st][row >> lgB][1][hd];
                 valid[hd] = in_page && scale_ok(k1) && scale_ok(v1);
                 if (in_page && !valid[hd]) set_error(p.err, PK_DEVERR_SCALE);
+                if (!valid[hd]) k1 = v1 = 1.f;         // a weight of zero times its scale stays zero
                 ks[hd] = k1;
                 const uint32_t b = __float_as_uint(v1);
                 lv[hd] = (b & 0x7fffffu) ? __log2f(v1) : static_cast<float>(static_cast<int>(b >> 23) - 127);
