@@ -9,9 +9,9 @@
 //   q * 2^k = h + l / 32, 2^k bringing the row's largest to [128, 256): two
 //     terms hold a bf16 value exactly down to 2^-13 of the row's largest, and
 //     what is smaller to 2^-22 of it.
-//   u = 2^(t - m) = h1 + h2 / 32 + h3 / 2^16, u <= 256: 9 bits or more of the
-//     largest weights, 13 of those below 4, and nothing above 2^-27 is lost
-//     (of a largest weight that is 16 or more: see the reference below).
+//   u = 2^(t - m) = h1 + h2 / 32 + h3 / 2^16, u <= 256: to 2^-10 of u, and
+//     nothing above 2^-25 is lost, of a largest weight that is 16 or more (see
+//     the reference below).  bf16 weights are to 2^-9.
 // The extra columns cost MMA time only, and a tile's MMAs take a tenth of the
 // time its bytes take from HBM.
 //
@@ -20,7 +20,7 @@
 // bounded waits are those of the bf16 kernel (decode_tc.cu, decode_split.cuh).
 //
 // Per 128-token tile, inside a CTA (256 threads):
-//   warp 0    producer: block-table entries one tile ahead (a lane per page),
+//   warp 0    producer: block-table entries four tiles ahead (a lane per page),
 //             one box of K and one of V per page and KV head -- B D contiguous
 //             bytes -- into a ring of six stages, and the pages' scales by
 //             cp.async beside them;
@@ -49,12 +49,14 @@ using namespace sm100;
 
 constexpr int kThreads = 256;
 constexpr int kStages = 6;
+constexpr int kAhead = 4;                                    // tiles whose table entries are on their way
 constexpr int kQBytes = 8192;                                // all query buffers
 constexpr int kQRing = 8;                                    // query scales kept, by segment
 constexpr uint64_t kWaitLimitNs = 1000000000ull;             // 1 s: far beyond any legal wait
 constexpr int kLenCache = 2048;                              // lengths kept in shared memory up to this batch
 constexpr float kLevel2 = 1.f / 32, kLevel3 = 1.f / 65536;   // what the terms of u stand for
 constexpr float kHeadroom = 8.f;                             // u <= 2^8: e4m3 holds 256
+constexpr float kNoReference = 3.0e38f;                      // minus the reference of a segment's start
 constexpr float kStart = 4.f;                                // the largest u when the reference moves: 2^4
 
 constexpr uint32_t kLayoutSw64 = 4;
@@ -132,6 +134,63 @@ SM100_DEV void tmem_ld32(uint32_t taddr, float (&v)[32]) {
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// Two floats in one 64-bit register and the packed fp32 instructions on them.
+SM100_DEV uint64_t f2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+SM100_DEV float2 unf2(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+SM100_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+SM100_DEV uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+SM100_DEV uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// The three terms of two weights u <= 256, two e4m3 bytes each.  u is first
+// rounded to fp16 (11 bits; steps of 2^-24 at the bottom), in which the
+// remainders after each term are exact.  The first, at most 8, is scaled by 32;
+// the second by 2048, and beyond 448 / 2048 its term stops at 448.
+SM100_DEV void split_weights(float u0, float u1, uint32_t &h1, uint32_t &h2, uint32_t &h3) {
+    asm("{\n\t.reg .b32 u, b, r;\n\t.reg .b16 a;\n\t"
+        "cvt.rn.f16x2.f32 u, %4, %3;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 a, u;\n\t"
+        "cvt.u32.u16 %0, a;\n\t"
+        "cvt.rn.f16x2.e4m3x2 b, a;\n\t"
+        "sub.rn.f16x2 r, u, b;\n\t"
+        "mul.rn.f16x2 r, r, %5;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 a, r;\n\t"
+        "cvt.u32.u16 %1, a;\n\t"
+        "cvt.rn.f16x2.e4m3x2 b, a;\n\t"
+        "sub.rn.f16x2 r, r, b;\n\t"
+        "mul.rn.f16x2 r, r, %6;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 a, r;\n\t"
+        "cvt.u32.u16 %2, a;\n\t}"
+        : "=r"(h1), "=r"(h2), "=r"(h3)
+        : "f"(u0), "f"(u1), "r"(0x50005000u), "r"(0x68006800u));
+}
+
+// Nearly 1 / v for a scale (relative error 2^-23).
+SM100_DEV float fast_rcp(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
 // The weights of the cut, as for the bf16 kernel's (decode_tc.cu).
 constexpr int64_t kTileCost = 400;
 constexpr int kTokCost = 1;
@@ -145,7 +204,6 @@ struct Shape {
     static_assert(NC >= 1 && NC <= kNPad, "query columns");
     static_assert(HP == 1 || (HP == 2 && D == 64 && NC <= 8), "head pairs: head dim 64, at most 8 columns each");
     static constexpr int CW = HP == 2 ? 8 : kNPad;          // columns per head in slots and lsum
-    static constexpr int NCOL = HP == 2 ? 8 + NC : NC;      // columns 0 .. NCOL - 1 may be in use
     static constexpr int HL = NC <= 8 ? 8 : 16;             // rows of h (and of l) in a query buffer
     static constexpr int NS = 2 * HL;                       // MMA N of S^T per head: h columns, then l columns
     static constexpr int PW = (HP == 2 || NC > 8) ? 16 : 8; // columns of one term of u
@@ -171,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const DecodeFp8Params p) {
     using C_ = Shape<D, NC, HP>;
-    constexpr int CW = C_::CW, NCOL = C_::NCOL, HL = C_::HL, NS = C_::NS, PW = C_::PW, NP = C_::NP;
+    constexpr int CW = C_::CW, HL = C_::HL, NS = C_::NS, PW = C_::PW, NP = C_::NP;
     constexpr uint32_t kLayout = D == 128 ? kLayoutSw128 : kLayoutSw64;
     constexpr uint32_t kAtom = 8 * D;                 // eight rows: the swizzle's atom
     constexpr uint32_t kIdescQK = idesc_e4m3(kTile, NS, 0, 0);   // A = K (K-major), B = Q (K-major)
@@ -324,10 +382,27 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             return (lane < (kTile >> lgB) && fp + lane < MB)
                        ? p.block_tables[static_cast<size_t>(ww.s) * MB + fp + lane] : -1;
         };
-        int phys_next = n_tiles > 0 ? fetch(w) : -1;
+        // Table entries are read kAhead tiles before their tile: a tile's bytes
+        // take less time than one read does, so one tile ahead would bound the
+        // copies by that read's latency.
+        int ahead_phys[kAhead];
+        Walk wf = w;
+        int fetched = 0;
+        auto fetch_next = [&]() -> int {
+            if (fetched >= n_tiles) return -1;
+            const int v = fetch(wf);
+            wf.next(lens);
+            ++fetched;
+            return v;
+        };
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x) ahead_phys[x] = fetch_next();
         for (int i = 0; i < n_tiles; ++i) {
             const int st = i % kStages;
-            const int phys = phys_next;
+            const int phys = ahead_phys[0];
+#pragma unroll
+            for (int x = 0; x + 1 < kAhead; ++x) ahead_phys[x] = ahead_phys[x + 1];
+            ahead_phys[kAhead - 1] = fetch_next();
             int got = 1;
             if (lane == 0)
                 got = mbar_wait(smem_u32(&misc->empty[st]), ((i / kStages) & 1) ^ 1, &misc->abort, lim);
@@ -393,7 +468,6 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             cp_async_arrive(smem_u32(&misc->sfull[st]));
             ++issued;
             w.next(lens);
-            if (i + 1 < n_tiles) phys_next = fetch(w);
         }
         cp_async_wait_all();
         // On abort, let this warp's copies land before the CTA can exit.
@@ -588,9 +662,15 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         const int row = quad * 32 + lane;
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quad * 32) << 16);
         // Columns: HP == 1, query column j; HP == 2, 0-7 the pair's first head's and 8-15 the second's.
-        float qf[NCOL], m_ref[NCOL], l_run[NCOL], m_prev[NCOL], l_prev[NCOL];
+        // They are kept in pairs, for the packed fp32 instructions: pair x holds
+        // columns col(x) and col(x) + 1 of head hd(x) (a single column's partner is unused).
+        constexpr int kPerHead = (NC + 1) / 2, kPairs = HP * kPerHead;
+        auto col = [](int x) { return (x / kPerHead) * 8 * (HP - 1) + 2 * (x % kPerHead); };
+        auto hd_of = [](int x) { return HP == 2 ? x / kPerHead : 0; };
+        uint64_t qf[kPairs], l_run[kPairs], l_prev[kPairs];
+        uint64_t neg_m[kPairs], neg_m_prev[kPairs];      // minus the references
 #pragma unroll
-        for (int j = 0; j < NCOL; ++j) qf[j] = m_ref[j] = l_run[j] = m_prev[j] = l_prev[j] = 0.f;
+        for (int x = 0; x < kPairs; ++x) qf[x] = l_run[x] = l_prev[x] = neg_m[x] = neg_m_prev[x] = 0;
         const int hr = HP == 2 ? row >> 6 : 0;          // head of the pair of this O^T row
         const int dd = HP == 2 ? (row & 63) : row;      // its element
         const bool row_ok = HP == 2 || row < D;
@@ -619,9 +699,13 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&misc->o_free[pend_seg & 1]));
 #pragma unroll
-            for (int j = 0; j < NCOL; ++j) {
-                const float v = warp_sum(l_prev[j]);
-                if (lane == 0) misc->lsum[quad][j] = v;
+            for (int x = 0; x < kPairs; ++x) {
+                const float2 lp = unf2(l_prev[x]);
+                const float v0 = warp_sum(lp.x), v1 = NC > 1 ? warp_sum(lp.y) : 0.f;
+                if (lane == 0) {
+                    misc->lsum[quad][col(x)] = v0;
+                    misc->lsum[quad][col(x) + 1] = v1;
+                }
             }
             named_bar_sync(1, 128);
             float l[NC], o[NC];
@@ -656,7 +740,11 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 }
                 if (row == 0) {
 #pragma unroll
-                    for (int j = 0; j < NCOL; ++j) sl->m[j] = m_prev[j];
+                    for (int x = 0; x < kPairs; ++x) {
+                        const float2 m = unf2(neg_m_prev[x]);
+                        sl->m[col(x)] = -m.x;
+                        sl->m[col(x) + 1] = -m.y;
+                    }
                     sl->s = pend_s;
                     sl->h = pend_h;
                     sl->start_tile = beg + pend_i0 - pend_t0;
@@ -690,29 +778,28 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 seg_t0 = mt.z;
                 seg_i0 = i;
 #pragma unroll
-                for (int j = 0; j < NCOL; ++j) {
-                    m_ref[j] = -INFINITY;
-                    l_run[j] = 0.f;
-                    if ((j % CW) < NC) qf[j] = misc->qscale[seg % kQRing][j] * p.scale_log2;
+                for (int x = 0; x < kPairs; ++x) {
+                    neg_m[x] = f2(kNoReference, kNoReference);
+                    l_run[x] = 0;
+                    const float *qs = &misc->qscale[seg % kQRing][col(x)];
+                    qf[x] = f2(qs[0] * p.scale_log2, NC > 1 ? qs[1] * p.scale_log2 : 0.f);
                 }
             }
             tc_fence_after();
             // Scores: h columns plus 1/32 of the l columns.
-            float sv[NCOL];
+            uint64_t t2[kPairs];
             const uint32_t saddr = lane_addr + C_::tS + sb * C_::SCols;
-            if constexpr (HP == 2 || NS == 32) {
-                float x[32];
-                tmem_ld32(saddr, x);
+            {
+                constexpr int kLoaded = HP * NS;
+                float x[kLoaded];
+                if constexpr (kLoaded == 32) tmem_ld32(saddr, x);
+                else tmem_ld16(saddr, x);
 #pragma unroll
-                for (int j = 0; j < NCOL; ++j) {
-                    if constexpr (HP == 2) sv[j] = fmaf(x[(j >> 3) * 16 + 8 + (j & 7)], kLevel2, x[(j >> 3) * 16 + (j & 7)]);
-                    else sv[j] = fmaf(x[16 + j], kLevel2, x[j]);
+                for (int y = 0; y < kPairs; ++y) {
+                    const int h = (HP == 2 ? hd_of(y) * NS : 0) + 2 * (y % kPerHead);
+                    t2[y] = fma2(f2(x[h + HL], NC > 1 ? x[h + HL + 1] : 0.f), f2(kLevel2, kLevel2),
+                                 f2(x[h], NC > 1 ? x[h + 1] : 0.f));
                 }
-            } else {
-                float x[16];
-                tmem_ld16(saddr, x);
-#pragma unroll
-                for (int j = 0; j < NCOL; ++j) sv[j] = fmaf(x[8 + j], kLevel2, x[j]);
             }
             // The token's scales; one that is out of range hides the token's head.
             const bool in_page = (misc->mask[st][row >> 5] >> (row & 31)) & 1u;
@@ -726,41 +813,69 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 if (!valid[hd]) k1 = v1 = 1.f;         // a weight of zero times its scale stays zero
                 ks[hd] = k1;
                 const uint32_t b = __float_as_uint(v1);
-                lv[hd] = (b & 0x7fffffu) ? __log2f(v1) : static_cast<float>(static_cast<int>(b >> 23) - 127);
-                ivs[hd] = 1.f / v1;
+                lv[hd] = static_cast<float>(static_cast<int>(b >> 23) - 127);
+                if (b & 0x7fffffu) lv[hd] = __log2f(v1);
+                ivs[hd] = fast_rcp(v1);
             }
-            float t2[NCOL];
-            bool need = false;
-            const int jpos = mt.z * kTile + row;          // this row's token position
 #pragma unroll
-            for (int j = 0; j < NCOL; ++j) {
-                const int hd = HP == 2 ? j >> 3 : 0;
-                if ((j % CW) >= NC) {                      // padding column of a head pair
-                    t2[j] = -INFINITY;
-                    continue;
-                }
-                // Query column j % CW is query token (j % CW) / G, which sees positions <= its own.
-                const bool see = valid[hd] && (!MQ || jpos <= qm.z + ((j % CW) >> lgG));
-                t2[j] = see ? fmaf(sv[j], qf[j] * ks[hd], lv[hd]) : -INFINITY;
-                need |= t2[j] > m_ref[j] + kHeadroom;
+            for (int x = 0; x < kPairs; ++x) {
+                const int hd = hd_of(x);
+                t2[x] = fma2(t2[x], mul2(qf[x], f2(ks[hd], ks[hd])), f2(lv[hd], lv[hd]));
             }
-            if (named_bar_or(1, 128, need)) {
+            const bool hide = !valid[0] || !valid[HP - 1];
+            const bool any_hidden = __any_sync(0xffffffffu, hide);
+            if (MQ || any_hidden) {
+                // Query column y of a head is query token y / G, which sees positions <= its own.
+                const int ahead = mt.z * kTile + row - qm.z;      // of the first query token
+#pragma unroll
+                for (int x = 0; x < kPairs; ++x) {
+                    float2 t = unf2(t2[x]);
+                    const int y = 2 * (x % kPerHead);
+                    if (!valid[hd_of(x)] || (MQ && ahead > (y >> lgG))) t.x = -INFINITY;
+                    if (!valid[hd_of(x)] || (MQ && ahead > ((y + 1) >> lgG))) t.y = -INFINITY;
+                    t2[x] = f2(t.x, t.y);
+                }
+            }
+            // Exponents t - m; a reference moves when one exceeds kHeadroom.
+            uint64_t d[kPairs];
+            float top = -INFINITY;
+#pragma unroll
+            for (int x = 0; x < kPairs; ++x) {
+                d[x] = add2(t2[x], neg_m[x]);
+                const float2 v = unf2(d[x]);
+                top = fmaxf(top, fmaxf(v.x, v.y));
+            }
+            if (named_bar_or(1, 128, top > kHeadroom)) {
                 // Rare: move the references to the running maxima less kStart.
 #pragma unroll
-                for (int j = 0; j < NCOL; ++j) {
-                    const float mx = warp_max_redux(t2[j]);
-                    if (lane == 0) misc->red[quad][j] = mx;
+                for (int x = 0; x < kPairs; ++x) {
+                    const float2 t = unf2(t2[x]);
+                    const float m0 = warp_max_redux(t.x), m1 = NC > 1 ? warp_max_redux(t.y) : m0;
+                    if (lane == 0) {
+                        misc->red[quad][col(x)] = m0;
+                        misc->red[quad][col(x) + 1] = m1;
+                    }
                 }
                 named_bar_sync(1, 128);
-                float a[NCOL];
+                float a[PW];
 #pragma unroll
-                for (int j = 0; j < NCOL; ++j) {
-                    const float t = fmaxf(fmaxf(misc->red[0][j], misc->red[1][j]),
-                                          fmaxf(misc->red[2][j], misc->red[3][j]));
-                    const float mn = fmaxf(m_ref[j], t - kStart);
-                    a[j] = m_ref[j] == -INFINITY ? 0.f : fast_exp2(m_ref[j] - mn);
-                    l_run[j] *= a[j];
-                    m_ref[j] = mn;
+                for (int j = 0; j < PW; ++j) a[j] = 1.f;
+#pragma unroll
+                for (int x = 0; x < kPairs; ++x) {
+                    const float2 nm = unf2(neg_m[x]);
+                    float n2[2] = {nm.x, nm.y};
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const int j = col(x) + y;
+                        const float t = fmaxf(fmaxf(misc->red[0][j], misc->red[1][j]),
+                                              fmaxf(misc->red[2][j], misc->red[3][j]));
+                        const float moved = fminf(n2[y], kStart - t);
+                        a[j] = fast_exp2(moved - n2[y]);
+                        n2[y] = moved;
+                    }
+                    neg_m[x] = f2(n2[0], n2[1]);
+                    l_run[x] = mul2(l_run[x], f2(a[col(x)], a[col(x) + 1]));
+                    d[x] = add2(t2[x], neg_m[x]);
                 }
                 if (!seg_first) {
                     // O through tile i-1, in TMEM (thread <-> head-dim row).
@@ -777,10 +892,7 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                         float o8[8];
                         tmem_ld<8>(oaddr + 8 * q, o8);
 #pragma unroll
-                        for (int x = 0; x < 8; ++x) {
-                            const int j = (8 * q + x) % PW;
-                            if (j < NCOL) o8[x] *= a[j < NCOL ? j : 0];
-                        }
+                        for (int x = 0; x < 8; ++x) o8[x] *= a[(8 * q + x) % PW];
                         tmem_st8(oaddr + 8 * q, o8);
                     }
                 }
@@ -791,25 +903,14 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
 #pragma unroll
             for (int x = 0; x < PW / 4; ++x) words[0][x] = words[1][x] = words[2][x] = 0;
 #pragma unroll
-            for (int j = 0; j < NCOL; j += 2) {
-                if ((j % CW) >= NC) continue;              // padding columns: weight 0
-                float u[2];
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const int jj = j + x < NCOL ? j + x : j;
-                    const bool used = j + x < NCOL && ((j + x) % CW) < NC;
-                    u[x] = used && t2[jj] != -INFINITY ? fast_exp2(t2[jj] - m_ref[jj]) : 0.f;
-                    if (used) l_run[jj] = fmaf(u[x], ivs[HP == 2 ? jj >> 3 : 0], l_run[jj]);
-                }
-                const uint32_t h1 = e4m3x2(u[0], u[1]);
-                float b0, b1;
-                e4m3x2_to_float(h1, b0, b1);
-                const float r0 = (u[0] - b0) * 32.f, r1 = (u[1] - b1) * 32.f;
-                const uint32_t h2 = e4m3x2(r0, r1);
-                e4m3x2_to_float(h2, b0, b1);
-                // Beyond 448 / 2048 the third term stops at 448: 2^-10 of u at most is left.
-                const uint32_t h3 = e4m3x2((r0 - b0) * 2048.f, (r1 - b1) * 2048.f);
-                const int sh = (j & 2) * 8;
+            for (int x = 0; x < kPairs; ++x) {
+                const float2 e = unf2(d[x]);
+                const float u0 = fast_exp2(e.x), u1 = NC > 1 ? fast_exp2(e.y) : 0.f;
+                const float iv = ivs[hd_of(x)];
+                l_run[x] = fma2(f2(u0, u1), f2(iv, iv), l_run[x]);
+                uint32_t h1, h2, h3;
+                split_weights(u0, u1, h1, h2, h3);
+                const int j = col(x), sh = (j & 2) * 8;
                 words[0][j >> 2] |= h1 << sh;
                 words[1][j >> 2] |= h2 << sh;
                 words[2][j >> 2] |= h3 << sh;
@@ -824,8 +925,7 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             // Rows of hidden tokens are zeroed once this tile's V has landed: the
             // MMA multiplies every V row by its weight, and theirs may hold stale
             // bytes or NaN.
-            const bool hide = !valid[0] || !valid[HP - 1];
-            if (__any_sync(0xffffffffu, hide) &&
+            if (any_hidden &&
                 !__all_sync(0xffffffffu, mbar_wait(smem_u32(&misc->vfull[st]), (i / kStages) & 1, &misc->never,
                                                    lim))) {
                 misc->abort = 1;
@@ -878,9 +978,9 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 pend_complete = seg_t0 == 0 && mt.z == mt.w - 1;
                 pend_cut_end = mt.z == mt.w - 1;
 #pragma unroll
-                for (int j = 0; j < NCOL; ++j) {
-                    m_prev[j] = m_ref[j];
-                    l_prev[j] = l_run[j];
+                for (int x = 0; x < kPairs; ++x) {
+                    neg_m_prev[x] = neg_m[x];
+                    l_prev[x] = l_run[x];
                 }
                 if (i == n_tiles - 1 && !finalize()) {
                     misc->abort = 1;
