@@ -48,12 +48,9 @@ namespace {
 using namespace sm100;
 
 constexpr int kThreads = 256;
-constexpr int kStages = 6;
 constexpr int kAhead = 4;                                    // tiles whose table entries are on their way
-constexpr int kQBytes = 8192;                                // all query buffers
 constexpr int kQRing = 8;                                    // query scales kept, by segment
 constexpr uint64_t kWaitLimitNs = 1000000000ull;             // 1 s: far beyond any legal wait
-constexpr int kLenCache = 2048;                              // lengths kept in shared memory up to this batch
 constexpr float kLevel2 = 1.f / 32, kLevel3 = 1.f / 65536;   // what the terms of u stand for
 constexpr float kHeadroom = 8.f;                             // u <= 2^8: e4m3 holds 256
 constexpr float kNoReference = 3.0e38f;                      // minus the reference of a segment's start
@@ -84,7 +81,8 @@ SM100_DEV void cp_async_arrive(uint32_t bar) {
 }
 SM100_DEV void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-struct Misc {
+template <int kStages, int kLenCache>
+struct MiscT {
     uint64_t full[kStages];       // K rows of a stage landed
     uint64_t vfull[kStages];      // V rows of a stage landed
     uint64_t sfull[kStages];      // its pages' scales landed
@@ -112,7 +110,7 @@ struct Misc {
     float qscale[kQRing][kNPad];   // by segment: what the stored query values of a column stand for
     float red[4][kNPad];
     float lsum[4][kNPad];
-    int lens[kLenCache];
+    int lens[kLenCache];          // the raw sequence lengths, when there are at most kLenCache
 };
 
 // 32 consecutive columns of this thread's TMEM lane.
@@ -206,30 +204,42 @@ struct Shape {
     static constexpr int CW = HP == 2 ? 8 : kNPad;          // columns per head in slots and lsum
     static constexpr int HL = NC <= 8 ? 8 : 16;             // rows of h (and of l) in a query buffer
     static constexpr int NS = 2 * HL;                       // MMA N of S^T per head: h columns, then l columns
-    static constexpr int PW = (HP == 2 || NC > 8) ? 16 : 8; // columns of one term of u
+    static constexpr int PW = HP * NC > 8 ? 16 : 8;         // columns of one term of u
+    static constexpr int PC = PW / HP;                      // of them, one head's
     static constexpr int NP = PW == 8 ? 32 : 48;            // MMA N of O^T: three terms (and padding to 16)
     static constexpr uint32_t HeadBytes = kTile * D;        // one head's rows of a tile
     static constexpr uint32_t StageBytes = 2 * HP * HeadBytes;
     static constexpr uint32_t VOff = HP * HeadBytes;
     static constexpr uint32_t QHeadBytes = NS * D;
     static constexpr uint32_t QBufBytes = HP * QHeadBytes;
-    static constexpr int QBufs = kQBytes / QBufBytes < 4 ? kQBytes / QBufBytes : 4;
+    // Two CTAs an SM where their shared memory and 128 registers a thread do:
+    // one CTA's warps wait for one another most of the time (a tile is a chain
+    // of copies, scores, weights and products), and a second one fills that.
+    static constexpr int CtasPerSm = NP == 32 ? 2 : 1;
+    static constexpr int Stages = CtasPerSm == 2 ? 3 * 32768 / StageBytes : 6;
+    static constexpr int LenCache = CtasPerSm == 2 ? 384 : 2048;
+    static constexpr int QBufs = 2;
     static constexpr uint32_t PBytes = kTile * NP;
     static constexpr uint32_t SCols = HP * NS;
     static constexpr uint32_t tS = 0, tO = 2 * SCols;
     static constexpr uint32_t TmemCols = tO + 2 * NP <= 128 ? 128 : 256;
-    static constexpr size_t SmemBytes = 1024 + kStages * StageBytes + kQBytes + 2 * PBytes + sizeof(Misc);
+    using Misc = MiscT<Stages, LenCache>;
+    static constexpr size_t SmemBytes = 1024 + Stages * StageBytes + QBufs * QBufBytes + 2 * PBytes + sizeof(Misc);
     static_assert(QBufs >= 2 && QBufs + 2 < kQRing, "query scales outlive their buffers");
     static_assert(tO + 2 * NP <= 256, "TMEM");
     static_assert(SmemBytes <= 227 * 1024, "shared memory");
+    static_assert(CtasPerSm * (SmemBytes + 1024) <= 228 * 1024, "CTAs per SM");
+    static_assert(CtasPerSm * TmemCols <= 512, "TMEM");
 };
 
 template <int D, int NC, bool MQ, int HP>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, Shape<D, NC, HP>::CtasPerSm)
 decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const DecodeFp8Params p) {
     using C_ = Shape<D, NC, HP>;
-    constexpr int CW = C_::CW, HL = C_::HL, NS = C_::NS, PW = C_::PW, NP = C_::NP;
+    using Misc = typename C_::Misc;
+    constexpr int kStages = C_::Stages, kLenCache = C_::LenCache;
+    constexpr int CW = C_::CW, HL = C_::HL, NS = C_::NS, PW = C_::PW, PC = C_::PC, NP = C_::NP;
     constexpr uint32_t kLayout = D == 128 ? kLayoutSw128 : kLayoutSw64;
     constexpr uint32_t kAtom = 8 * D;                 // eight rows: the swizzle's atom
     constexpr uint32_t kIdescQK = idesc_e4m3(kTile, NS, 0, 0);   // A = K (K-major), B = Q (K-major)
@@ -240,7 +250,7 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     uint8_t *smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
     uint8_t *stage_ptr = smem;
     uint8_t *q_ptr = smem + kStages * C_::StageBytes;
-    uint8_t *p_ptr = q_ptr + kQBytes;
+    uint8_t *p_ptr = q_ptr + C_::QBufs * C_::QBufBytes;
     Misc *misc = reinterpret_cast<Misc *>(p_ptr + 2 * C_::PBytes);
     const uint32_t stage_addr = smem_u32(stage_ptr);
     const uint32_t q_addr = smem_u32(q_ptr);
@@ -663,9 +673,11 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quad * 32) << 16);
         // Columns: HP == 1, query column j; HP == 2, 0-7 the pair's first head's and 8-15 the second's.
         // They are kept in pairs, for the packed fp32 instructions: pair x holds
-        // columns col(x) and col(x) + 1 of head hd(x) (a single column's partner is unused).
+        // columns col(x) and col(x) + 1 of head hd(x) (a single column's partner
+        // is unused), which are pc(x) and pc(x) + 1 of a term of u and of O^T.
         constexpr int kPerHead = (NC + 1) / 2, kPairs = HP * kPerHead;
         auto col = [](int x) { return (x / kPerHead) * 8 * (HP - 1) + 2 * (x % kPerHead); };
+        auto pc = [](int x) { return (x / kPerHead) * PC * (HP - 1) + 2 * (x % kPerHead); };
         auto hd_of = [](int x) { return HP == 2 ? x / kPerHead : 0; };
         uint64_t qf[kPairs], l_run[kPairs], l_prev[kPairs];
         uint64_t neg_m[kPairs], neg_m_prev[kPairs];      // minus the references
@@ -698,13 +710,34 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&misc->o_free[pend_seg & 1]));
+            {
+                // Denominators over the warp: halves of the columns are exchanged
+                // until a lane holds one column's sum (n - 1 + log2(32 / n) shuffles
+                // for n columns instead of 5 n).
+                constexpr int n = HP * NC;
+                float v[n];
 #pragma unroll
-            for (int x = 0; x < kPairs; ++x) {
-                const float2 lp = unf2(l_prev[x]);
-                const float v0 = warp_sum(lp.x), v1 = NC > 1 ? warp_sum(lp.y) : 0.f;
-                if (lane == 0) {
-                    misc->lsum[quad][col(x)] = v0;
-                    misc->lsum[quad][col(x) + 1] = v1;
+                for (int x = 0; x < kPairs; ++x) {
+                    const float2 lp = unf2(l_prev[x]);
+                    const int at = hd_of(x) * NC + 2 * (x % kPerHead);
+                    v[at] = lp.x;
+                    if constexpr (NC > 1) v[at + 1] = lp.y;
+                }
+                int off = 16;
+#pragma unroll
+                for (int m = n; m > 1; m >>= 1, off >>= 1) {
+                    const bool upper = lane & off;
+#pragma unroll
+                    for (int x = 0; x < m / 2; ++x) {
+                        const float mine = upper ? v[x + m / 2] : v[x], theirs = upper ? v[x] : v[x + m / 2];
+                        v[x] = mine + __shfl_xor_sync(0xffffffffu, theirs, off);
+                    }
+                }
+#pragma unroll
+                for (; off >= 1; off >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
+                if (lane % (32 / n) == 0) {
+                    const int at = lane / (32 / n);
+                    misc->lsum[quad][(HP == 2 ? at / NC * 8 : 0) + at % NC] = v[0];
                 }
             }
             named_bar_sync(1, 128);
@@ -713,7 +746,7 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             for (int cq = 0; cq < NC; ++cq) {
                 const int j = hr * CW + cq;
                 l[cq] = misc->lsum[0][j] + misc->lsum[1][j] + misc->lsum[2][j] + misc->lsum[3][j];
-                if constexpr (HP == 2) o[cq] = hr ? ov[8 + cq] : ov[cq];
+                if constexpr (HP == 2) o[cq] = hr ? ov[PC + cq] : ov[cq];
                 else o[cq] = ov[cq];
             }
             if (pend_complete) {
@@ -723,7 +756,7 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                         if ((cq >> lgG) >= pend_qn) continue;      // a padded query column
                         const size_t qrow = static_cast<size_t>(MQ ? pend_q0 : pend_s) + (cq >> lgG);
                         const int qh = (pend_h * HP + hr) * Gq + (cq & (Gq - 1));
-                        store_out(p, (qrow * H + qh) * D + dd, l[cq] != 0.f ? o[cq] / l[cq] : 0.f);
+                        store_out(p, (qrow * H + qh) * D + dd, l[cq] != 0.f ? __fdividef(o[cq], l[cq]) : 0.f);
                     }
                 }
             } else {
@@ -870,11 +903,11 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                         const float t = fmaxf(fmaxf(misc->red[0][j], misc->red[1][j]),
                                               fmaxf(misc->red[2][j], misc->red[3][j]));
                         const float moved = fminf(n2[y], kStart - t);
-                        a[j] = fast_exp2(moved - n2[y]);
+                        a[pc(x) + y] = fast_exp2(moved - n2[y]);
                         n2[y] = moved;
                     }
                     neg_m[x] = f2(n2[0], n2[1]);
-                    l_run[x] = mul2(l_run[x], f2(a[col(x)], a[col(x) + 1]));
+                    l_run[x] = mul2(l_run[x], f2(a[pc(x)], a[pc(x) + 1]));
                     d[x] = add2(t2[x], neg_m[x]);
                 }
                 if (!seg_first) {
@@ -910,7 +943,7 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 l_run[x] = fma2(f2(u0, u1), f2(iv, iv), l_run[x]);
                 uint32_t h1, h2, h3;
                 split_weights(u0, u1, h1, h2, h3);
-                const int j = col(x), sh = (j & 2) * 8;
+                const int j = pc(x), sh = (j & 2) * 8;
                 words[0][j >> 2] |= h1 << sh;
                 words[1][j >> 2] |= h2 << sh;
                 words[2][j >> 2] |= h3 << sh;
@@ -1032,7 +1065,8 @@ bool encode_piece_map(CUtensorMap *m, const void *base, const DecodeFp8Params &p
 }
 
 template <int D, int NC, int HP>
-cudaError_t launch_shape(const DecodeFp8Params &p, int C, cudaStream_t stream) {
+cudaError_t launch_shape(const DecodeFp8Params &p, int sms, cudaStream_t stream) {
+    const int C = std::min(sms * Shape<D, NC, HP>::CtasPerSm, static_cast<int>(kMaxCtas));
     CUtensorMap mk, mv;
     if (!encode_piece_map(&mk, p.k8, p) || !encode_piece_map(&mv, p.v8, p)) return cudaErrorInvalidValue;
     auto *kernel = p.cu_q_lens ? decode_fp8_tc_kernel<D, NC, true, HP> : decode_fp8_tc_kernel<D, NC, false, HP>;
@@ -1069,7 +1103,7 @@ cudaError_t launch_dim(const DecodeFp8Params &p, int C, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_decode_fp8_tensor_core(const DecodeFp8Params &p, cudaStream_t stream) {
-    const int C = std::min(sm_count(), static_cast<int>(kMaxCtas));
+    const int C = sm_count();
     if (C <= 0) return cudaErrorNoDevice;
     // MMA columns: the group's query heads times the query tokens per sequence.
     switch ((p.num_heads / p.num_kv_heads) * (p.cu_q_lens ? p.q_len : 1)) {
