@@ -10,7 +10,7 @@
 //     terms hold a bf16 value exactly down to 2^-13 of the row's largest, and
 //     what is smaller to 2^-22 of it.
 //   u = 2^(t - m) = h1 + h2 / 32 + h3 / 2^16, u <= 256: to 2^-10 of u, and
-//     nothing above 2^-25 is lost, of a largest weight that is 16 or more (see
+//     nothing above 2^-25 is lost, of a largest weight that is 1 or more (see
 //     the reference below).  bf16 weights are to 2^-9.
 // The extra columns cost MMA time only, and a tile's MMAs take a tenth of the
 // time its bytes take from HBM.
@@ -47,14 +47,13 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kThreads = 256;
 constexpr int kAhead = 4;                                    // tiles whose table entries are on their way
 constexpr int kQRing = 8;                                    // query scales kept, by segment
 constexpr uint64_t kWaitLimitNs = 1000000000ull;             // 1 s: far beyond any legal wait
 constexpr float kLevel2 = 1.f / 32, kLevel3 = 1.f / 65536;   // what the terms of u stand for
 constexpr float kHeadroom = 8.f;                             // u <= 2^8: e4m3 holds 256
 constexpr float kNoReference = 3.0e38f;                      // minus the reference of a segment's start
-constexpr float kStart = 4.f;                                // the largest u when the reference moves: 2^4
+constexpr float kStart = 0.f;                                // the largest u when the reference moves: 2^0
 
 constexpr uint32_t kLayoutSw64 = 4;
 
@@ -81,7 +80,7 @@ SM100_DEV void cp_async_arrive(uint32_t bar) {
 }
 SM100_DEV void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-template <int kStages, int kLenCache>
+template <int kThreads, int kStages, int kLenCache>
 struct MiscT {
     uint64_t full[kStages];       // K rows of a stage landed
     uint64_t vfull[kStages];      // V rows of a stage landed
@@ -109,7 +108,8 @@ struct MiscT {
     float scales[kStages][16][2][2];   // [page][K, V][head of the pair]
     float qscale[kQRing][kNPad];   // by segment: what the stored query values of a column stand for
     float red[4][kNPad];
-    float lsum[4][kNPad];
+    float lsum[2][4][kNPad];       // a segment's denominators by warp (segment parity)
+    float mref[2][kNPad];          // its references
     int lens[kLenCache];          // the raw sequence lengths, when there are at most kLenCache
 };
 
@@ -217,13 +217,19 @@ struct Shape {
     // of copies, scores, weights and products), and a second one fills that.
     static constexpr int CtasPerSm = NP == 32 ? 2 : 1;
     static constexpr int Stages = CtasPerSm == 2 ? 3 * 32768 / StageBytes : 6;
-    static constexpr int LenCache = CtasPerSm == 2 ? 384 : 2048;
+    static constexpr int LenCache = CtasPerSm == 2 ? 256 : 2048;
     static constexpr int QBufs = 2;
+    // The one CTA of an SM splits its work over more warps instead: two groups
+    // of softmax warps, eight columns each, and a producer each for K and V.
+    static constexpr int Groups = CtasPerSm == 2 ? 1 : 2;
+    static constexpr int GPairs = Groups == 2 ? 4 : (HP == 2 ? NC + NC % 2 : (NC + 1) / 2);   // pairs of columns of a group
+    static constexpr int QueryWarp = 2 + 4 * Groups;        // the first of two
+    static constexpr int Threads = 32 * (QueryWarp + 2 + (Groups - 1));
     static constexpr uint32_t PBytes = kTile * NP;
     static constexpr uint32_t SCols = HP * NS;
     static constexpr uint32_t tS = 0, tO = 2 * SCols;
     static constexpr uint32_t TmemCols = tO + 2 * NP <= 128 ? 128 : 256;
-    using Misc = MiscT<Stages, LenCache>;
+    using Misc = MiscT<Threads, Stages, LenCache>;
     static constexpr size_t SmemBytes = 1024 + Stages * StageBytes + QBufs * QBufBytes + 2 * PBytes + sizeof(Misc);
     static_assert(QBufs >= 2 && QBufs + 2 < kQRing, "query scales outlive their buffers");
     static_assert(tO + 2 * NP <= 256, "TMEM");
@@ -233,12 +239,12 @@ struct Shape {
 };
 
 template <int D, int NC, bool MQ, int HP>
-__global__ void __launch_bounds__(kThreads, Shape<D, NC, HP>::CtasPerSm)
+__global__ void __launch_bounds__(Shape<D, NC, HP>::Threads, Shape<D, NC, HP>::CtasPerSm)
 decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const DecodeFp8Params p) {
     using C_ = Shape<D, NC, HP>;
     using Misc = typename C_::Misc;
-    constexpr int kStages = C_::Stages, kLenCache = C_::LenCache;
+    constexpr int kThreads = C_::Threads, kStages = C_::Stages, kLenCache = C_::LenCache, kGroups = C_::Groups;
     constexpr int CW = C_::CW, HL = C_::HL, NS = C_::NS, PW = C_::PW, PC = C_::PC, NP = C_::NP;
     constexpr uint32_t kLayout = D == 128 ? kLayoutSw128 : kLayoutSw64;
     constexpr uint32_t kAtom = 8 * D;                 // eight rows: the swizzle's atom
@@ -270,7 +276,7 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         for (int i = 0; i < kStages; ++i) {
             mbar_init(smem_u32(&misc->full[i]), 1);
             mbar_init(smem_u32(&misc->vfull[i]), 1);
-            mbar_init(smem_u32(&misc->sfull[i]), 32);
+            mbar_init(smem_u32(&misc->sfull[i]), 32 * kGroups);   // the lanes of every producer
             mbar_init(smem_u32(&misc->empty[i]), 1);
         }
         for (int i = 0; i < C_::QBufs; ++i) {
@@ -279,9 +285,9 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&misc->s_full[i]), 1);
-            mbar_init(smem_u32(&misc->p_full[i]), 4);
+            mbar_init(smem_u32(&misc->p_full[i]), 4 * kGroups);
             mbar_init(smem_u32(&misc->o_full[i]), 1);
-            mbar_init(smem_u32(&misc->o_free[i]), 4);
+            mbar_init(smem_u32(&misc->o_free[i]), 4 * kGroups);
         }
         mbar_init(smem_u32(&misc->drain), 1);
         misc->abort = 0;
@@ -382,9 +388,13 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         }
     };
 
-    if (warp == 0) {
+    if (warp == 0 || warp == C_::QueryWarp + 2) {
         // ================= producer =================
+        // K and V, or (two groups) warp 0 K and the last warp V.
+        const bool do_k = warp == 0, do_v = kGroups == 1 || warp != 0;
         Walk w = w0;
+        int2 qr = make_int2(0, 0);
+        int qr_of = -1;
         const int MB = p.max_blocks_per_seq;
         int issued = 0;
         auto fetch = [&](const Walk &ww) -> int {
@@ -445,34 +455,38 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             const uint32_t full = smem_u32(&misc->full[st]);
             const uint32_t vfull = smem_u32(&misc->vfull[st]);
             const uint32_t sbase = stage_addr + st * C_::StageBytes;
-            if (lane == 0) {
+            if constexpr (MQ) {
+                if (w.s != qr_of) qr = query_rows(qr_of = w.s);
+            }
+            if (lane == 0 && do_v) mbar_arrive_expect_tx(vfull, nok * (HP * D) << lgB);
+            if (lane == 0 && do_k) {
                 misc->mask[st][0] = m0;
                 misc->mask[st][1] = m1;
                 misc->mask[st][2] = m2;
                 misc->mask[st][3] = m3;
                 misc->meta[st] = make_int4(w.s, w.h, w.t, w.nt);
-                if constexpr (MQ) {
-                    const int2 qr = query_rows(w.s);
-                    misc->qmeta[st] = make_int4(qr.x, qr.y, w.L - qr.y, 0);
-                }
+                if constexpr (MQ) misc->qmeta[st] = make_int4(qr.x, qr.y, w.L - qr.y, 0);
                 mbar_arrive_expect_tx(full, nok * (HP * D) << lgB);
-                mbar_arrive_expect_tx(vfull, nok * (HP * D) << lgB);
             }
             __syncwarp();
             if (ok) {
                 // The (block, head) piece: B rows of D bytes, at the page's place in each head's tile.
                 const int piece = phys * p.num_kv_heads + w.h * HP;
                 const uint32_t at = sbase + static_cast<uint32_t>(r0) * D;
+                if (do_k) {
 #pragma unroll
-                for (int hd = 0; hd < HP; ++hd)
-                    tma_load_3d(at + hd * C_::HeadBytes, &tm_k, full, 0, 0, piece + hd);
+                    for (int hd = 0; hd < HP; ++hd)
+                        tma_load_3d(at + hd * C_::HeadBytes, &tm_k, full, 0, 0, piece + hd);
+                }
+                if (do_v) {
 #pragma unroll
-                for (int hd = 0; hd < HP; ++hd)
-                    tma_load_3d(at + C_::VOff + hd * C_::HeadBytes, &tm_v, vfull, 0, 0, piece + hd);
+                    for (int hd = 0; hd < HP; ++hd)
+                        tma_load_3d(at + C_::VOff + hd * C_::HeadBytes, &tm_v, vfull, 0, 0, piece + hd);
+                }
 #pragma unroll
                 for (int hd = 0; hd < HP; ++hd) {
-                    cp_async4(smem_u32(&misc->scales[st][lane][0][hd]), p.k_scales + piece + hd);
-                    cp_async4(smem_u32(&misc->scales[st][lane][1][hd]), p.v_scales + piece + hd);
+                    if (do_k) cp_async4(smem_u32(&misc->scales[st][lane][0][hd]), p.k_scales + piece + hd);
+                    if (do_v) cp_async4(smem_u32(&misc->scales[st][lane][1][hd]), p.v_scales + piece + hd);
                 }
             }
             cp_async_arrive(smem_u32(&misc->sfull[st]));
@@ -483,8 +497,8 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         // On abort, let this warp's copies land before the CTA can exit.
         if (misc->abort && lane == 0) {
             for (int i = max(0, issued - kStages); i < issued; ++i) {
-                mbar_wait(smem_u32(&misc->full[i % kStages]), (i / kStages) & 1, &misc->never, lim);
-                mbar_wait(smem_u32(&misc->vfull[i % kStages]), (i / kStages) & 1, &misc->never, lim);
+                if (do_k) mbar_wait(smem_u32(&misc->full[i % kStages]), (i / kStages) & 1, &misc->never, lim);
+                if (do_v) mbar_wait(smem_u32(&misc->vfull[i % kStages]), (i / kStages) & 1, &misc->never, lim);
             }
         }
     } else if (warp == 1) {
@@ -571,15 +585,15 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             mbar_wait(smem_u32(&misc->drain), 0, &misc->never, lim);
         }
         __syncwarp();
-    } else if (warp >= 6) {
+    } else if (warp >= C_::QueryWarp) {
         // ================= queries =================
-        // Warp 6 takes the even segments, warp 7 the odd ones.
+        // One warp takes the even segments, the other the odd ones.
         constexpr int kE = D / 32;                    // elements of a row a lane holds
         Walk w = w0;
         int i = 0;
         for (int sg = 0; i < n_tiles; ++sg) {
             const int left = min(w.nt - w.t, n_tiles - i);
-            if ((sg & 1) == warp - 6) {
+            if ((sg & 1) == warp - C_::QueryWarp) {
                 const int2 qr = query_rows(w.s);
                 uint32_t raw[HP][NC][kE / 2];
 #pragma unroll
@@ -667,22 +681,30 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             w.next(lens);
         }
     } else {
-        // ================= softmax (warps 2-5): thread <-> tile row =================
+        // ================= softmax: thread <-> tile row =================
+        // Group g has columns 8 g to 8 g + 7 (two groups), or all of them.
+        const int grp = kGroups == 2 ? (warp - 2) >> 2 : 0;
+        const uint32_t bar = 1 + grp;                   // its named barrier
         const int quad = warp & 3;
         const int row = quad * 32 + lane;
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quad * 32) << 16);
         // Columns: HP == 1, query column j; HP == 2, 0-7 the pair's first head's and 8-15 the second's.
         // They are kept in pairs, for the packed fp32 instructions: pair x holds
-        // columns col(x) and col(x) + 1 of head hd(x) (a single column's partner
-        // is unused), which are pc(x) and pc(x) + 1 of a term of u and of O^T.
-        constexpr int kPerHead = (NC + 1) / 2, kPairs = HP * kPerHead;
-        auto col = [](int x) { return (x / kPerHead) * 8 * (HP - 1) + 2 * (x % kPerHead); };
-        auto pc = [](int x) { return (x / kPerHead) * PC * (HP - 1) + 2 * (x % kPerHead); };
-        auto hd_of = [](int x) { return HP == 2 ? x / kPerHead : 0; };
-        uint64_t qf[kPairs], l_run[kPairs], l_prev[kPairs];
-        uint64_t neg_m[kPairs], neg_m_prev[kPairs];      // minus the references
+        // columns col(x) and col(x) + 1 of head hd_of(x) (a single column's
+        // partner is unused), which are pc(x) and pc(x) + 1 of a term of u and
+        // of O^T.  With two groups col(x) = pc(x), and the head is the group's.
+        constexpr int kPairs = C_::GPairs, kPerHead = kGroups == 2 ? 4 : (NC + 1) / 2;
+        auto local = [](int x) { return x / kPerHead * PC + 2 * (x % kPerHead); };     // pc(x) less 8 grp
+        auto col = [&](int x) { return kGroups == 2 ? 8 * grp + 2 * x : x / kPerHead * 8 + 2 * (x % kPerHead); };
+        auto hd_of = [](int x) { return kGroups == 1 ? x / kPerHead : 0; };   // index into this group's heads
+        constexpr int kHeads = HP == 2 && kGroups == 1 ? 2 : 1;               // heads a group has
+        const int hd0 = HP == 2 && kGroups == 2 ? grp : 0;                    // its first head
+        constexpr int kCols = kGroups == 2 ? 8 : HP * NC;                     // its columns
+        constexpr int kGW = kGroups == 2 ? 8 : PW;                            // and with padding, in a term of u
+        uint64_t qf[kPairs], l_run[kPairs];
+        uint64_t neg_m[kPairs];                          // minus the references
 #pragma unroll
-        for (int x = 0; x < kPairs; ++x) qf[x] = l_run[x] = l_prev[x] = neg_m[x] = neg_m_prev[x] = 0;
+        for (int x = 0; x < kPairs; ++x) qf[x] = l_run[x] = neg_m[x] = 0;
         const int hr = HP == 2 ? row >> 6 : 0;          // head of the pair of this O^T row
         const int dd = HP == 2 ? (row & 63) : row;      // its element
         const bool row_ok = HP == 2 || row < D;
@@ -697,87 +719,58 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 return false;
             tc_fence_after();
             // The three terms, smallest first.
-            float ov[PW];
+            float ov[kGW];
             {
-                const uint32_t oaddr = lane_addr + C_::tO + (pend_seg & 1) * NP;
-                float o1[PW], o2[PW], o3[PW];
-                tmem_ld<PW>(oaddr, o1);
-                tmem_ld<PW>(oaddr + PW, o2);
-                tmem_ld<PW>(oaddr + 2 * PW, o3);
+                const uint32_t oaddr = lane_addr + C_::tO + (pend_seg & 1) * NP + 8 * grp;
+                float o1[kGW], o2[kGW], o3[kGW];
+                tmem_ld<kGW>(oaddr, o1);
+                tmem_ld<kGW>(oaddr + PW, o2);
+                tmem_ld<kGW>(oaddr + 2 * PW, o3);
 #pragma unroll
-                for (int j = 0; j < PW; ++j) ov[j] = fmaf(o3[j], kLevel3, fmaf(o2[j], kLevel2, o1[j]));
+                for (int j = 0; j < kGW; ++j) ov[j] = fmaf(o3[j], kLevel3, fmaf(o2[j], kLevel2, o1[j]));
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&misc->o_free[pend_seg & 1]));
-            {
-                // Denominators over the warp: halves of the columns are exchanged
-                // until a lane holds one column's sum (n - 1 + log2(32 / n) shuffles
-                // for n columns instead of 5 n).
-                constexpr int n = HP * NC;
-                float v[n];
+            // This row's columns: of one head, first_col .. first_col + kMine - 1.
+            constexpr int kMine = kGroups == 2 ? 8 : NC;
+            const int first_col = kGroups == 2 ? 8 * grp : hr * 8;
+            const bool mine = row_ok && (HP == 1 || kGroups == 1 || hr == grp);
+            float l[kMine], o[kMine];
+            const float (*ls)[kNPad] = misc->lsum[pend_seg & 1];
 #pragma unroll
-                for (int x = 0; x < kPairs; ++x) {
-                    const float2 lp = unf2(l_prev[x]);
-                    const int at = hd_of(x) * NC + 2 * (x % kPerHead);
-                    v[at] = lp.x;
-                    if constexpr (NC > 1) v[at + 1] = lp.y;
-                }
-                int off = 16;
-#pragma unroll
-                for (int m = n; m > 1; m >>= 1, off >>= 1) {
-                    const bool upper = lane & off;
-#pragma unroll
-                    for (int x = 0; x < m / 2; ++x) {
-                        const float mine = upper ? v[x + m / 2] : v[x], theirs = upper ? v[x] : v[x + m / 2];
-                        v[x] = mine + __shfl_xor_sync(0xffffffffu, theirs, off);
-                    }
-                }
-#pragma unroll
-                for (; off >= 1; off >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
-                if (lane % (32 / n) == 0) {
-                    const int at = lane / (32 / n);
-                    misc->lsum[quad][(HP == 2 ? at / NC * 8 : 0) + at % NC] = v[0];
-                }
-            }
-            named_bar_sync(1, 128);
-            float l[NC], o[NC];
-#pragma unroll
-            for (int cq = 0; cq < NC; ++cq) {
-                const int j = hr * CW + cq;
-                l[cq] = misc->lsum[0][j] + misc->lsum[1][j] + misc->lsum[2][j] + misc->lsum[3][j];
-                if constexpr (HP == 2) o[cq] = hr ? ov[PC + cq] : ov[cq];
-                else o[cq] = ov[cq];
+            for (int x = 0; x < kMine; ++x) {
+                const int j = first_col + x;
+                l[x] = ls[0][j] + ls[1][j] + ls[2][j] + ls[3][j];
+                if constexpr (kHeads == 2) o[x] = hr ? ov[PC + x] : ov[x];
+                else o[x] = ov[x];
             }
             if (pend_complete) {
-                if (row_ok) {
+                if (mine) {
 #pragma unroll
-                    for (int cq = 0; cq < NC; ++cq) {
-                        if ((cq >> lgG) >= pend_qn) continue;      // a padded query column
+                    for (int x = 0; x < kMine; ++x) {
+                        const int cq = (HP == 1 ? first_col : 0) + x;       // query column of the head
+                        if ((cq >> lgG) >= pend_qn) continue;               // a padded one
                         const size_t qrow = static_cast<size_t>(MQ ? pend_q0 : pend_s) + (cq >> lgG);
                         const int qh = (pend_h * HP + hr) * Gq + (cq & (Gq - 1));
-                        store_out(p, (qrow * H + qh) * D + dd, l[cq] != 0.f ? __fdividef(o[cq], l[cq]) : 0.f);
+                        store_out(p, (qrow * H + qh) * D + dd, l[x] != 0.f ? __fdividef(o[x], l[x]) : 0.f);
                     }
                 }
             } else {
                 // A cut part: slot 0 if the segment is this CTA's first, 1 if not.
                 const int slot_idx = pend_i0 == 0 ? 0 : 1;
                 Slot *sl = slots + 2 * c + slot_idx;
-                if (row_ok) {
+                if (mine) {
 #pragma unroll
-                    for (int cq = 0; cq < NC; ++cq) sl->o[(hr * CW + cq) * 128 + row] = o[cq];
-                }
-                if (dd == 0 && row_ok) {
-#pragma unroll
-                    for (int cq = 0; cq < NC; ++cq) sl->l[hr * CW + cq] = l[cq];
-                }
-                if (row == 0) {
-#pragma unroll
-                    for (int x = 0; x < kPairs; ++x) {
-                        const float2 m = unf2(neg_m_prev[x]);
-                        sl->m[col(x)] = -m.x;
-                        sl->m[col(x) + 1] = -m.y;
+                    for (int x = 0; x < kMine; ++x) {
+                        sl->o[(first_col + x) * 128 + row] = o[x];
+                        if (dd == 0) {
+                            sl->l[first_col + x] = l[x];
+                            sl->m[first_col + x] = misc->mref[pend_seg & 1][first_col + x];
+                        }
                     }
+                }
+                if (row == 0 && grp == 0) {
                     sl->s = pend_s;
                     sl->h = pend_h;
                     sl->start_tile = beg + pend_i0 - pend_t0;
@@ -791,6 +784,46 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             }
             pending = false;
             return true;
+        };
+        // A finished segment's denominators and references, for finalize (which
+        // follows at least one barrier of the group later).
+        auto close_segment = [&]() {
+            // Sums over the warp: halves of the columns are exchanged until a
+            // lane holds one column's (n - 1 + log2(32 / n) shuffles for n
+            // columns instead of 5 n).
+            constexpr int n = kCols;
+            float v[n];
+#pragma unroll
+            for (int x = 0; x < kPairs; ++x) {
+                const float2 lp = unf2(l_run[x]);
+                const int at = kGroups == 2 ? 2 * x : hd_of(x) * NC + 2 * (x % kPerHead);
+                v[at] = lp.x;
+                if constexpr (NC > 1) v[at + 1] = lp.y;
+            }
+            int off = 16;
+#pragma unroll
+            for (int m = n; m > 1; m >>= 1, off >>= 1) {
+                const bool upper = lane & off;
+#pragma unroll
+                for (int x = 0; x < m / 2; ++x) {
+                    const float keep = upper ? v[x + m / 2] : v[x], give = upper ? v[x] : v[x + m / 2];
+                    v[x] = keep + __shfl_xor_sync(0xffffffffu, give, off);
+                }
+            }
+#pragma unroll
+            for (; off >= 1; off >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
+            if (lane % (32 / n) == 0) {
+                const int at = lane / (32 / n);
+                misc->lsum[seg & 1][quad][kGroups == 2 ? 8 * grp + at : (HP == 2 ? at / NC * 8 : 0) + at % NC] = v[0];
+            }
+            if (row == 0) {
+#pragma unroll
+                for (int x = 0; x < kPairs; ++x) {
+                    const float2 m = unf2(neg_m[x]);
+                    misc->mref[seg & 1][col(x)] = -m.x;
+                    if constexpr (NC > 1) misc->mref[seg & 1][col(x) + 1] = -m.y;
+                }
+            }
         };
         for (int i = 0; i < n_tiles; ++i) {
             const int st = i % kStages;
@@ -823,24 +856,37 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             uint64_t t2[kPairs];
             const uint32_t saddr = lane_addr + C_::tS + sb * C_::SCols;
             {
-                constexpr int kLoaded = HP * NS;
-                float x[kLoaded];
-                if constexpr (kLoaded == 32) tmem_ld32(saddr, x);
-                else tmem_ld16(saddr, x);
+                // h and l columns of this group.
+                constexpr int kWide = kHeads * 16;
+                float x[kWide];
+                if constexpr (kGroups == 2 && HP == 1) {
+                    float h8[8], l8[8];
+                    tmem_ld<8>(saddr + 8 * grp, h8);
+                    tmem_ld<8>(saddr + HL + 8 * grp, l8);
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) {
+                        x[y] = h8[y];
+                        x[8 + y] = l8[y];
+                    }
+                } else if constexpr (kWide == 32) {
+                    tmem_ld32(saddr, x);
+                } else {
+                    tmem_ld16(saddr + hd0 * NS, x);
+                }
 #pragma unroll
                 for (int y = 0; y < kPairs; ++y) {
-                    const int h = (HP == 2 ? hd_of(y) * NS : 0) + 2 * (y % kPerHead);
-                    t2[y] = fma2(f2(x[h + HL], NC > 1 ? x[h + HL + 1] : 0.f), f2(kLevel2, kLevel2),
+                    const int h = hd_of(y) * 16 + 2 * (y % kPerHead);
+                    t2[y] = fma2(f2(x[h + 8], NC > 1 ? x[h + 9] : 0.f), f2(kLevel2, kLevel2),
                                  f2(x[h], NC > 1 ? x[h + 1] : 0.f));
                 }
             }
             // The token's scales; one that is out of range hides the token's head.
             const bool in_page = (misc->mask[st][row >> 5] >> (row & 31)) & 1u;
-            bool valid[HP];
-            float ks[HP], lv[HP], ivs[HP];
+            bool valid[kHeads];
+            float ks[kHeads], lv[kHeads], ivs[kHeads];
 #pragma unroll
-            for (int hd = 0; hd < HP; ++hd) {
-                float k1 = misc->scales[st][row >> lgB][0][hd], v1 = misc->scales[st][row >> lgB][1][hd];
+            for (int hd = 0; hd < kHeads; ++hd) {
+                float k1 = misc->scales[st][row >> lgB][0][hd0 + hd], v1 = misc->scales[st][row >> lgB][1][hd0 + hd];
                 valid[hd] = in_page && scale_ok(k1) && scale_ok(v1);
                 if (in_page && !valid[hd]) set_error(p.err, PK_DEVERR_SCALE);
                 if (!valid[hd]) k1 = v1 = 1.f;         // a weight of zero times its scale stays zero
@@ -855,7 +901,7 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 const int hd = hd_of(x);
                 t2[x] = fma2(t2[x], mul2(qf[x], f2(ks[hd], ks[hd])), f2(lv[hd], lv[hd]));
             }
-            const bool hide = !valid[0] || !valid[HP - 1];
+            const bool hide = !valid[0] || !valid[kHeads - 1];
             const bool any_hidden = __any_sync(0xffffffffu, hide);
             if (MQ || any_hidden) {
                 // Query column y of a head is query token y / G, which sees positions <= its own.
@@ -863,7 +909,7 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
 #pragma unroll
                 for (int x = 0; x < kPairs; ++x) {
                     float2 t = unf2(t2[x]);
-                    const int y = 2 * (x % kPerHead);
+                    const int y = (HP == 1 ? 8 * grp : 0) + 2 * (x % kPerHead);
                     if (!valid[hd_of(x)] || (MQ && ahead > (y >> lgG))) t.x = -INFINITY;
                     if (!valid[hd_of(x)] || (MQ && ahead > ((y + 1) >> lgG))) t.y = -INFINITY;
                     t2[x] = f2(t.x, t.y);
@@ -878,7 +924,7 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 const float2 v = unf2(d[x]);
                 top = fmaxf(top, fmaxf(v.x, v.y));
             }
-            if (named_bar_or(1, 128, top > kHeadroom)) {
+            if (named_bar_or(bar, 128, top > kHeadroom)) {
                 // Rare: move the references to the running maxima less kStart.
 #pragma unroll
                 for (int x = 0; x < kPairs; ++x) {
@@ -889,10 +935,10 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                         misc->red[quad][col(x) + 1] = m1;
                     }
                 }
-                named_bar_sync(1, 128);
-                float a[PW];
+                named_bar_sync(bar, 128);
+                float a[kGW];
 #pragma unroll
-                for (int j = 0; j < PW; ++j) a[j] = 1.f;
+                for (int j = 0; j < kGW; ++j) a[j] = 1.f;
 #pragma unroll
                 for (int x = 0; x < kPairs; ++x) {
                     const float2 nm = unf2(neg_m[x]);
@@ -903,11 +949,11 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                         const float t = fmaxf(fmaxf(misc->red[0][j], misc->red[1][j]),
                                               fmaxf(misc->red[2][j], misc->red[3][j]));
                         const float moved = fminf(n2[y], kStart - t);
-                        a[pc(x) + y] = fast_exp2(moved - n2[y]);
+                        a[local(x) + y] = fast_exp2(moved - n2[y]);
                         n2[y] = moved;
                     }
                     neg_m[x] = f2(n2[0], n2[1]);
-                    l_run[x] = mul2(l_run[x], f2(a[pc(x)], a[pc(x) + 1]));
+                    l_run[x] = mul2(l_run[x], f2(a[local(x)], a[local(x) + 1]));
                     d[x] = add2(t2[x], neg_m[x]);
                 }
                 if (!seg_first) {
@@ -919,22 +965,22 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t oaddr = lane_addr + C_::tO + (seg & 1) * NP;
+                    const uint32_t oaddr = lane_addr + C_::tO + (seg & 1) * NP + 8 * grp;
 #pragma unroll
-                    for (int q = 0; q < 3 * PW / 8; ++q) {
-                        float o8[8];
-                        tmem_ld<8>(oaddr + 8 * q, o8);
+                    for (int term = 0; term < 3; ++term) {
+                        float o8[kGW];
+                        tmem_ld<kGW>(oaddr + term * PW, o8);
 #pragma unroll
-                        for (int x = 0; x < 8; ++x) o8[x] *= a[(8 * q + x) % PW];
-                        tmem_st8(oaddr + 8 * q, o8);
+                        for (int x = 0; x < kGW; ++x) o8[x] *= a[x];
+                        static_assert(kGW == 8, "one store");
+                        tmem_st8(oaddr + term * PW, o8);
                     }
                 }
                 // red[] is rewritten only in a later rare path, after the next vote.
             }
-            // Weights in their three terms: words[term][4 columns].
-            uint32_t words[3][PW / 4];
-#pragma unroll
-            for (int x = 0; x < PW / 4; ++x) words[0][x] = words[1][x] = words[2][x] = 0;
+            // Weights in their three terms: words[term][4 columns of the group].
+            static_assert(kGW == 8, "two words a term");
+            uint32_t words[3][2] = {};
 #pragma unroll
             for (int x = 0; x < kPairs; ++x) {
                 const float2 e = unf2(d[x]);
@@ -943,7 +989,7 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 l_run[x] = fma2(f2(u0, u1), f2(iv, iv), l_run[x]);
                 uint32_t h1, h2, h3;
                 split_weights(u0, u1, h1, h2, h3);
-                const int j = pc(x), sh = (j & 2) * 8;
+                const int j = local(x), sh = (j & 2) * 8;
                 words[0][j >> 2] |= h1 << sh;
                 words[1][j >> 2] |= h2 << sh;
                 words[2][j >> 2] |= h3 << sh;
@@ -965,12 +1011,12 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 set_error(p.err, PK_DEVERR_TIMEOUT);
                 break;
             }
-            if (hide) {
+            if (hide && (HP == 2 || grp == 0)) {
 #pragma unroll
-                for (int hd = 0; hd < HP; ++hd) {
+                for (int hd = 0; hd < kHeads; ++hd) {
                     if (valid[hd]) continue;
                     uint4 *vrow = reinterpret_cast<uint4 *>(stage_ptr + st * C_::StageBytes + C_::VOff +
-                                                            hd * C_::HeadBytes + row * D);
+                                                            (hd0 + hd) * C_::HeadBytes + row * D);
 #pragma unroll
                     for (int x = 0; x < D / 16; ++x) vrow[x] = make_uint4(0, 0, 0, 0);
                 }
@@ -984,8 +1030,7 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             } else {
 #pragma unroll
                 for (int x = 0; x < 3; ++x)
-                    *reinterpret_cast<uint4 *>(prow + 128 * x) =
-                        make_uint4(words[x][0], words[x][1], words[x][PW / 4 - 2], words[x][PW / 4 - 1]);
+                    *reinterpret_cast<uint2 *>(prow + 128 * x + 8 * grp) = make_uint2(words[x][0], words[x][1]);
             }
             fence_proxy_async_smem();
             tc_fence_before();
@@ -1010,11 +1055,8 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 pend_i0 = seg_i0;
                 pend_complete = seg_t0 == 0 && mt.z == mt.w - 1;
                 pend_cut_end = mt.z == mt.w - 1;
-#pragma unroll
-                for (int x = 0; x < kPairs; ++x) {
-                    neg_m_prev[x] = neg_m[x];
-                    l_prev[x] = l_run[x];
-                }
+                close_segment();
+                if (i == n_tiles - 1) named_bar_sync(bar, 128);
                 if (i == n_tiles - 1 && !finalize()) {
                     misc->abort = 1;
                     set_error(p.err, PK_DEVERR_TIMEOUT);
@@ -1078,7 +1120,7 @@ cudaError_t launch_shape(const DecodeFp8Params &p, int sms, cudaStream_t stream)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(C);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(Shape<D, NC, HP>::Threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attr;
