@@ -182,6 +182,21 @@ SM100_DEV void split_weights(float u0, float u1, uint32_t &h1, uint32_t &h2, uin
         : "f"(u0), "f"(u1), "r"(0x50005000u), "r"(0x68006800u));
 }
 
+// The two terms of two query values below 256, which fp16 holds exactly down
+// to 2^-14 (and to 2^-25 below): h, and 32 times what is left.
+SM100_DEV void split_query(float q0, float q1, uint32_t &h, uint32_t &l) {
+    asm("{\n\t.reg .b32 u, b;\n\t.reg .b16 a;\n\t"
+        "cvt.rn.f16x2.f32 u, %3, %2;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 a, u;\n\t"
+        "cvt.u32.u16 %0, a;\n\t"
+        "cvt.rn.f16x2.e4m3x2 b, a;\n\t"
+        "sub.rn.f16x2 u, u, b;\n\t"
+        "mul.rn.f16x2 u, u, %4;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 a, u;\n\t"
+        "cvt.u32.u16 %1, a;\n\t}"
+        : "=r"(h), "=r"(l) : "f"(q0), "f"(q1), "r"(0x50005000u));
+}
+
 // Nearly 1 / v for a scale (relative error 2^-23).
 SM100_DEV float fast_rcp(float v) {
     float r;
@@ -629,47 +644,49 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                     break;
                 }
                 uint8_t *buf = q_ptr + qb * C_::QBufBytes;
+                // Each row's power of two, then the terms: no branch in between, so
+                // that the rows' chains of conversions overlap.
+                float up[HP * NC], my_scale = 0.f;
 #pragma unroll
-                for (int hd = 0; hd < HP; ++hd) {
+                for (int y = 0; y < HP * NC; ++y) {
+                    // The row's largest magnitude: bf16 bits without the sign order as integers.
+                    uint32_t top = 0;
 #pragma unroll
-                    for (int cq = 0; cq < NC; ++cq) {
-                        // The row's largest magnitude: bf16 bits without the sign order as integers.
-                        uint32_t top = 0;
+                    for (int x = 0; x < kE / 2; ++x) {
+                        const uint32_t v = raw[y / NC][y % NC][x] & 0x7fff7fffu;
+                        top = max(top, max(v & 0xffffu, v >> 16));
+                    }
+                    top = __reduce_max_sync(0xffffffffu, top);
+                    // 2^k brings it to [128, 256); |k| <= 120 keeps 2^k and 2^-k normal.
+                    const bool finite = top < 0x7f80u;
+                    const int k = finite ? min(7 - (max(static_cast<int>(top >> 7), 1) - 127), 120) : 0;
+                    up[y] = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
+                    const float down = finite ? __uint_as_float(static_cast<uint32_t>(127 - k) << 23) : __int_as_float(0x7fffffff);
+                    my_scale = lane == y ? down : my_scale;
+                }
+                if (lane < HP * NC) misc->qscale[sg % kQRing][lane / NC * CW + lane % NC] = my_scale;
 #pragma unroll
-                        for (int x = 0; x < kE / 2; ++x) {
-                            const uint32_t v = raw[hd][cq][x] & 0x7fff7fffu;
-                            top = max(top, max(v & 0xffffu, v >> 16));
-                        }
-                        top = __reduce_max_sync(0xffffffffu, top);
-                        // 2^k brings it to [128, 256); |k| <= 120 keeps 2^k and 2^-k normal.
-                        const int k = min(7 - (max(static_cast<int>(top >> 7), 1) - 127), 120);
-                        const bool finite = top < 0x7f80u;
-                        const float up = __uint_as_float(static_cast<uint32_t>((finite ? k : 0) + 127) << 23);
-                        if (lane == 0)
-                            misc->qscale[sg % kQRing][hd * CW + cq] =
-                                finite ? __uint_as_float(static_cast<uint32_t>(127 - k) << 23) : __int_as_float(0x7fffffff);
-                        uint32_t hi = 0, lo = 0;
+                for (int y = 0; y < HP * NC; ++y) {
+                    const int hd = y / NC, cq = y % NC;
+                    uint32_t hi = 0, lo = 0;
 #pragma unroll
-                        for (int x = 0; x < kE / 2; ++x) {
-                            const float a = bf16_lo(raw[hd][cq][x]) * up, b = bf16_hi(raw[hd][cq][x]) * up;
-                            const uint32_t h2 = e4m3x2(a, b);
-                            float ha, hb;
-                            e4m3x2_to_float(h2, ha, hb);
-                            hi |= h2 << (16 * x);
-                            lo |= e4m3x2((a - ha) * 32.f, (b - hb) * 32.f) << (16 * x);
-                        }
-                        // K-major, no swizzle: 8 rows of 16 bytes side by side, 128 bytes
-                        // to the next 16 of the row, 8 D to the next 8 rows.
-                        const int byte = lane * kE;
-                        uint8_t *dst = buf + hd * C_::QHeadBytes + (cq >> 3) * 8 * D + (byte >> 4) * 128 + (cq & 7) * 16 +
-                                       (byte & 15);
-                        if constexpr (kE == 4) {
-                            *reinterpret_cast<uint32_t *>(dst) = hi;
-                            *reinterpret_cast<uint32_t *>(dst + HL * D) = lo;
-                        } else {
-                            *reinterpret_cast<uint16_t *>(dst) = static_cast<uint16_t>(hi);
-                            *reinterpret_cast<uint16_t *>(dst + HL * D) = static_cast<uint16_t>(lo);
-                        }
+                    for (int x = 0; x < kE / 2; ++x) {
+                        uint32_t h2, l2;
+                        split_query(bf16_lo(raw[hd][cq][x]) * up[y], bf16_hi(raw[hd][cq][x]) * up[y], h2, l2);
+                        hi |= h2 << (16 * x);
+                        lo |= l2 << (16 * x);
+                    }
+                    // K-major, no swizzle: 8 rows of 16 bytes side by side, 128 bytes
+                    // to the next 16 of the row, 8 D to the next 8 rows.
+                    const int byte = lane * kE;
+                    uint8_t *dst = buf + hd * C_::QHeadBytes + (cq >> 3) * 8 * D + (byte >> 4) * 128 + (cq & 7) * 16 +
+                                   (byte & 15);
+                    if constexpr (kE == 4) {
+                        *reinterpret_cast<uint32_t *>(dst) = hi;
+                        *reinterpret_cast<uint32_t *>(dst + HL * D) = lo;
+                    } else {
+                        *reinterpret_cast<uint16_t *>(dst) = static_cast<uint16_t>(hi);
+                        *reinterpret_cast<uint16_t *>(dst + HL * D) = static_cast<uint16_t>(lo);
                     }
                 }
                 fence_proxy_async_smem();
@@ -747,13 +764,27 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             }
             if (pend_complete) {
                 if (mine) {
+                    // Query column cq: token cq / G of the sequence, head cq % G of the KV head.
+                    const int cq0 = HP == 1 ? first_col : 0;
+                    const size_t base = (static_cast<size_t>(MQ ? pend_q0 : pend_s) * H + (pend_h * HP + hr) * Gq) * D + dd;
+                    const size_t row_step = static_cast<size_t>(H) * D;
+                    const int used = MQ ? min(NC, pend_qn << lgG) - cq0 : NC - cq0;     // the rest are padding
 #pragma unroll
-                    for (int x = 0; x < kMine; ++x) {
-                        const int cq = (HP == 1 ? first_col : 0) + x;       // query column of the head
-                        if ((cq >> lgG) >= pend_qn) continue;               // a padded one
-                        const size_t qrow = static_cast<size_t>(MQ ? pend_q0 : pend_s) + (cq >> lgG);
-                        const int qh = (pend_h * HP + hr) * Gq + (cq & (Gq - 1));
-                        store_out(p, (qrow * H + qh) * D + dd, l[x] != 0.f ? __fdividef(o[x], l[x]) : 0.f);
+                    for (int x = 0; x < kMine; ++x) o[x] = l[x] != 0.f ? __fdividef(o[x], l[x]) : 0.f;
+                    auto at = [&](int x) -> size_t {
+                        const int cq = cq0 + x;
+                        return MQ ? base + (cq >> lgG) * row_step + (cq & (Gq - 1)) * D : base + cq * D;
+                    };
+                    if (p.out_fp32) {
+                        float *out = static_cast<float *>(p.out);
+#pragma unroll
+                        for (int x = 0; x < kMine; ++x)
+                            if (x < used) out[at(x)] = o[x];
+                    } else {
+                        uint16_t *out = static_cast<uint16_t *>(p.out);
+#pragma unroll
+                        for (int x = 0; x < kMine; ++x)
+                            if (x < used) out[at(x)] = static_cast<uint16_t>(pack_bf16x2(o[x], 0.f));
                     }
                 }
             } else {
