@@ -80,6 +80,15 @@ SM100_DEV void cp_async_arrive(uint32_t bar) {
 }
 SM100_DEV void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
+// mbar_wait with its loop out of line: the kernel's warps run different code
+// side by side, so its size is instruction-cache traffic.
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int *abort, uint64_t limit_ns) {
+    return mbar_wait(bar, parity, abort, limit_ns);
+}
+SM100_DEV bool wait_for(uint32_t bar, uint32_t parity, volatile int *abort, uint64_t limit_ns) {
+    return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort, limit_ns);
+}
+
 template <int kThreads, int kStages, int kLenCache>
 struct MiscT {
     uint64_t full[kStages];       // K rows of a stage landed
@@ -340,6 +349,7 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     };
     bool ahead = cached;
     if (cached) {
+#pragma unroll 1
         for (int s = threadIdx.x; s < N; s += kThreads) misc->lens[s] = ld_cg(p.seq_lens + s);
         __syncthreads();
     } else {
@@ -351,8 +361,10 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         ahead = false;
         wait_prev();
         int changed = 0;
+#pragma unroll 1
         for (int s = threadIdx.x; s < N; s += kThreads) changed |= ld_cg(p.seq_lens + s) != misc->lens[s];
         if (!__syncthreads_or(changed)) break;
+#pragma unroll 1
         for (int s = threadIdx.x; s < N; s += kThreads) misc->lens[s] = ld_cg(p.seq_lens + s);
         __syncthreads();
     }
@@ -362,6 +374,7 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     // Lengths outside [0, cap] are reported, and empty sequences get zeros,
     // by CTA s % C.
     if (odd || MQ) {
+#pragma unroll 1
         for (int s = c; s < N; s += C) {
             const int raw = lens.raw(s);
             if ((raw < 0 || raw > cap) && threadIdx.x == 0) set_error(p.err, PK_DEVERR_SEQ_LEN);
@@ -372,10 +385,12 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 const bool bad = r0 < 0 || r1 < r0 || r1 > p.total_q || r1 - r0 > p.q_len;
                 if ((bad || r1 - r0 > L) && threadIdx.x == 0) set_error(p.err, PK_DEVERR_SEQ_LEN);
                 if (L != 0 || bad) continue;
+#pragma unroll 1
                 for (int64_t i = threadIdx.x; i < static_cast<int64_t>(r1 - r0) * H * D; i += kThreads)
                     store_out(p, static_cast<size_t>(r0) * H * D + i, 0.f);
             } else {
                 if (L != 0) continue;
+#pragma unroll 1
                 for (int i = threadIdx.x; i < H * D; i += kThreads) store_out(p, static_cast<size_t>(s) * H * D + i, 0.f);
             }
         }
@@ -430,17 +445,21 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             ++fetched;
             return v;
         };
+        int phys = -1;
 #pragma unroll
-        for (int x = 0; x < kAhead; ++x) ahead_phys[x] = fetch_next();
-        for (int i = 0; i < n_tiles; ++i) {
-            const int st = i % kStages;
-            const int phys = ahead_phys[0];
+        for (int x = 0; x < kAhead; ++x) ahead_phys[x] = -1;
+        // Rounds before 0 only start the reads.
+#pragma unroll 1
+        for (int i = -kAhead; i < n_tiles; ++i) {
+            phys = ahead_phys[0];
 #pragma unroll
             for (int x = 0; x + 1 < kAhead; ++x) ahead_phys[x] = ahead_phys[x + 1];
             ahead_phys[kAhead - 1] = fetch_next();
+            if (i < 0) continue;
+            const int st = i % kStages;
             int got = 1;
             if (lane == 0)
-                got = mbar_wait(smem_u32(&misc->empty[st]), ((i / kStages) & 1) ^ 1, &misc->abort, lim);
+                got = wait_for(smem_u32(&misc->empty[st]), ((i / kStages) & 1) ^ 1, &misc->abort, lim);
             if (!__shfl_sync(0xffffffffu, got, 0)) {      // one decision for the whole warp
                 if (lane == 0) {
                     misc->abort = 1;
@@ -512,8 +531,8 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         // On abort, let this warp's copies land before the CTA can exit.
         if (misc->abort && lane == 0) {
             for (int i = max(0, issued - kStages); i < issued; ++i) {
-                if (do_k) mbar_wait(smem_u32(&misc->full[i % kStages]), (i / kStages) & 1, &misc->never, lim);
-                if (do_v) mbar_wait(smem_u32(&misc->vfull[i % kStages]), (i / kStages) & 1, &misc->never, lim);
+                if (do_k) wait_for(smem_u32(&misc->full[i % kStages]), (i / kStages) & 1, &misc->never, lim);
+                if (do_v) wait_for(smem_u32(&misc->vfull[i % kStages]), (i / kStages) & 1, &misc->never, lim);
             }
         }
     } else if (warp == 1) {
@@ -545,7 +564,7 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
 #pragma unroll
                     for (int kk = 0; kk < D / 32; ++kk) {
                         const uint64_t a = smem_desc(kbase + hd * C_::HeadBytes + kk * 32, 16, kAtom, kLayout);
-                        const uint64_t b = smem_desc(qbase + hd * C_::QHeadBytes + kk * 256, 128, 8 * D, kLayoutNone);
+                        const uint64_t b = smem_desc(qbase + hd * C_::QHeadBytes + kk * 32, 16, kAtom, kLayout);
                         mma_e4m3(tmem + C_::tS + (i & 1) * C_::SCols + hd * NS, a, b, kIdescQK, kk > 0 ? 1u : 0u);
                     }
                 }
@@ -597,45 +616,38 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             }
             // Let every issued MMA finish before the CTA can release TMEM.
             mma_commit(smem_u32(&misc->drain));
-            mbar_wait(smem_u32(&misc->drain), 0, &misc->never, lim);
+            wait_for(smem_u32(&misc->drain), 0, &misc->never, lim);
         }
         __syncwarp();
     } else if (warp >= C_::QueryWarp) {
         // ================= queries =================
         // One warp takes the even segments, the other the odd ones.
-        constexpr int kE = D / 32;                    // elements of a row a lane holds
+        // A row is D / 8 lanes of 8 elements; a warp does kRows rows at once.
+        constexpr int kLanes = D / 8, kRows = 32 / kLanes, kIters = (HP * NC + kRows - 1) / kRows;
+        const int part = lane % kLanes, sub = lane / kLanes;
         Walk w = w0;
         int i = 0;
+#pragma unroll 1
         for (int sg = 0; i < n_tiles; ++sg) {
             const int left = min(w.nt - w.t, n_tiles - i);
             if ((sg & 1) == warp - C_::QueryWarp) {
                 const int2 qr = query_rows(w.s);
-                uint32_t raw[HP][NC][kE / 2];
+                uint4 raw[kIters];
 #pragma unroll
-                for (int hd = 0; hd < HP; ++hd) {
-#pragma unroll
-                    for (int cq = 0; cq < NC; ++cq) {
-                        // Column cq: query token cq / G, query head cq % G of the KV head.
-                        const int r = cq >> lgG;
-#pragma unroll
-                        for (int x = 0; x < kE / 2; ++x) raw[hd][cq][x] = 0;
-                        if (r < qr.y) {
-                            const size_t head = static_cast<size_t>(qr.x + r) * H + (w.h * HP + hd) * Gq + (cq & (Gq - 1));
-                            const uint16_t *src = p.q + head * D + lane * kE;
-                            if constexpr (kE == 4) {
-                                const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src));
-                                raw[hd][cq][0] = v.x;
-                                raw[hd][cq][1] = v.y;
-                            } else {
-                                raw[hd][cq][0] = __ldg(reinterpret_cast<const uint32_t *>(src));
-                            }
-                        }
+                for (int y = 0; y < kIters; ++y) {
+                    // Row x of the buffer: query column x % NC of head x / NC of the
+                    // pair; column cq: query token cq / G, query head cq % G.
+                    const int x = y * kRows + sub, cq = x % NC;
+                    raw[y] = make_uint4(0, 0, 0, 0);
+                    if (x < HP * NC && (cq >> lgG) < qr.y) {
+                        const size_t head = static_cast<size_t>(qr.x + (cq >> lgG)) * H + (w.h * HP + x / NC) * Gq + (cq & (Gq - 1));
+                        raw[y] = __ldg(reinterpret_cast<const uint4 *>(p.q + head * D + part * 8));
                     }
                 }
                 const int qb = sg % C_::QBufs;
                 int got = 1;
                 if (lane == 0)
-                    got = mbar_wait(smem_u32(&misc->qempty[qb]), ((sg / C_::QBufs) & 1) ^ 1, &misc->abort, lim);
+                    got = wait_for(smem_u32(&misc->qempty[qb]), ((sg / C_::QBufs) & 1) ^ 1, &misc->abort, lim);
                 if (!__shfl_sync(0xffffffffu, got, 0)) {
                     if (lane == 0) {
                         misc->abort = 1;
@@ -644,49 +656,41 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                     break;
                 }
                 uint8_t *buf = q_ptr + qb * C_::QBufBytes;
-                // Each row's power of two, then the terms: no branch in between, so
-                // that the rows' chains of conversions overlap.
-                float up[HP * NC], my_scale = 0.f;
 #pragma unroll
-                for (int y = 0; y < HP * NC; ++y) {
+                for (int y = 0; y < kIters; ++y) {
+                    const int x = y * kRows + sub, hd = x / NC, cq = x % NC;
                     // The row's largest magnitude: bf16 bits without the sign order as integers.
                     uint32_t top = 0;
+                    const uint32_t words[4] = {raw[y].x, raw[y].y, raw[y].z, raw[y].w};
 #pragma unroll
-                    for (int x = 0; x < kE / 2; ++x) {
-                        const uint32_t v = raw[y / NC][y % NC][x] & 0x7fff7fffu;
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t v = words[e] & 0x7fff7fffu;
                         top = max(top, max(v & 0xffffu, v >> 16));
                     }
-                    top = __reduce_max_sync(0xffffffffu, top);
+#pragma unroll
+                    for (int o = kLanes / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
                     // 2^k brings it to [128, 256); |k| <= 120 keeps 2^k and 2^-k normal.
                     const bool finite = top < 0x7f80u;
                     const int k = finite ? min(7 - (max(static_cast<int>(top >> 7), 1) - 127), 120) : 0;
-                    up[y] = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
-                    const float down = finite ? __uint_as_float(static_cast<uint32_t>(127 - k) << 23) : __int_as_float(0x7fffffff);
-                    my_scale = lane == y ? down : my_scale;
-                }
-                if (lane < HP * NC) misc->qscale[sg % kQRing][lane / NC * CW + lane % NC] = my_scale;
+                    const float up = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
+                    if (part == 0 && x < HP * NC)
+                        misc->qscale[sg % kQRing][hd * CW + cq] =
+                            finite ? __uint_as_float(static_cast<uint32_t>(127 - k) << 23) : __int_as_float(0x7fffffff);
+                    uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll
-                for (int y = 0; y < HP * NC; ++y) {
-                    const int hd = y / NC, cq = y % NC;
-                    uint32_t hi = 0, lo = 0;
-#pragma unroll
-                    for (int x = 0; x < kE / 2; ++x) {
+                    for (int e = 0; e < 4; ++e) {
                         uint32_t h2, l2;
-                        split_query(bf16_lo(raw[hd][cq][x]) * up[y], bf16_hi(raw[hd][cq][x]) * up[y], h2, l2);
-                        hi |= h2 << (16 * x);
-                        lo |= l2 << (16 * x);
+                        split_query(bf16_lo(words[e]) * up, bf16_hi(words[e]) * up, h2, l2);
+                        hi[e >> 1] |= h2 << (16 * (e & 1));
+                        lo[e >> 1] |= l2 << (16 * (e & 1));
                     }
-                    // K-major, no swizzle: 8 rows of 16 bytes side by side, 128 bytes
-                    // to the next 16 of the row, 8 D to the next 8 rows.
-                    const int byte = lane * kE;
-                    uint8_t *dst = buf + hd * C_::QHeadBytes + (cq >> 3) * 8 * D + (byte >> 4) * 128 + (cq & 7) * 16 +
-                                   (byte & 15);
-                    if constexpr (kE == 4) {
-                        *reinterpret_cast<uint32_t *>(dst) = hi;
-                        *reinterpret_cast<uint32_t *>(dst + HL * D) = lo;
-                    } else {
-                        *reinterpret_cast<uint16_t *>(dst) = static_cast<uint16_t>(hi);
-                        *reinterpret_cast<uint16_t *>(dst + HL * D) = static_cast<uint16_t>(lo);
+                    // K-major rows of D bytes, swizzled as TMA swizzles K: the 16-byte
+                    // piece of a row is exchanged by the row (128 bytes: row % 8; 64: row / 2 % 4).
+                    const int r = cq, piece = (part >> 1) ^ (D == 128 ? r & 7 : (r >> 1) & 3);
+                    uint8_t *dst = buf + hd * C_::QHeadBytes + r * D + piece * 16 + (part & 1) * 8;
+                    if (x < HP * NC) {
+                        *reinterpret_cast<uint2 *>(dst) = make_uint2(hi[0], hi[1]);
+                        *reinterpret_cast<uint2 *>(dst + HL * D) = make_uint2(lo[0], lo[1]);
                     }
                 }
                 fence_proxy_async_smem();
@@ -731,7 +735,7 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         bool pend_complete = false, pend_cut_end = false;
         auto finalize = [&]() -> bool {
             // P.V of the segment's last tile (pend_i) complete.
-            if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&misc->o_full[pend_i & 1]), (pend_i >> 1) & 1,
+            if (!__all_sync(0xffffffffu, wait_for(smem_u32(&misc->o_full[pend_i & 1]), (pend_i >> 1) & 1,
                                                    &misc->never, lim)))
                 return false;
             tc_fence_after();
@@ -856,217 +860,224 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 }
             }
         };
-        for (int i = 0; i < n_tiles; ++i) {
-            const int st = i % kStages;
-            const int sb = i & 1;
-            if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&misc->s_full[sb]), (i >> 1) & 1, &misc->never, lim) &&
-                                             mbar_wait(smem_u32(&misc->sfull[st]), (i / kStages) & 1, &misc->never, lim))) {
-                misc->abort = 1;
-                set_error(p.err, PK_DEVERR_TIMEOUT);
-                break;
-            }
-            const int4 mt = misc->meta[st];   // (s, h, t, nt), written with the stage
-            int4 qm = make_int4(mt.x, 1, 0, 0);
-            if constexpr (MQ) qm = misc->qmeta[st];  // (first query row, query tokens, first query position)
-            const bool seg_first = (i == 0) || (mt.z == 0);
-            const bool seg_last = (i == n_tiles - 1) || (mt.z == mt.w - 1);
-            if (seg_first) {
-                ++seg;
-                seg_t0 = mt.z;
-                seg_i0 = i;
-#pragma unroll
-                for (int x = 0; x < kPairs; ++x) {
-                    neg_m[x] = f2(kNoReference, kNoReference);
-                    l_run[x] = 0;
-                    const float *qs = &misc->qscale[seg % kQRing][col(x)];
-                    qf[x] = f2(qs[0] * p.scale_log2, NC > 1 ? qs[1] * p.scale_log2 : 0.f);
+        // Round n_tiles only reads out the last segment.
+#pragma unroll 1
+        for (int i = 0; i <= n_tiles; ++i) {
+            int4 mt = make_int4(0, 0, 0, 0);             // (s, h, t, nt), written with the stage
+            int4 qm = make_int4(0, 1, 0, 0);             // (first query row, query tokens, first query position)
+            bool seg_last = false;
+            if (i == n_tiles) named_bar_sync(bar, 128);
+            if (i < n_tiles) {
+                const int st = i % kStages;
+                const int sb = i & 1;
+                if (!__all_sync(0xffffffffu, wait_for(smem_u32(&misc->s_full[sb]), (i >> 1) & 1, &misc->never, lim) &&
+                                                 wait_for(smem_u32(&misc->sfull[st]), (i / kStages) & 1, &misc->never, lim))) {
+                    misc->abort = 1;
+                    set_error(p.err, PK_DEVERR_TIMEOUT);
+                    break;
                 }
-            }
-            tc_fence_after();
-            // Scores: h columns plus 1/32 of the l columns.
-            uint64_t t2[kPairs];
-            const uint32_t saddr = lane_addr + C_::tS + sb * C_::SCols;
-            {
-                // h and l columns of this group.
-                constexpr int kWide = kHeads * 16;
-                float x[kWide];
-                if constexpr (kGroups == 2 && HP == 1) {
-                    float h8[8], l8[8];
-                    tmem_ld<8>(saddr + 8 * grp, h8);
-                    tmem_ld<8>(saddr + HL + 8 * grp, l8);
+                mt = misc->meta[st];
+                if constexpr (MQ) qm = misc->qmeta[st];
+                const bool seg_first = (i == 0) || (mt.z == 0);
+                seg_last = (i == n_tiles - 1) || (mt.z == mt.w - 1);
+                if (seg_first) {
+                    ++seg;
+                    seg_t0 = mt.z;
+                    seg_i0 = i;
 #pragma unroll
-                    for (int y = 0; y < 8; ++y) {
-                        x[y] = h8[y];
-                        x[8 + y] = l8[y];
-                    }
-                } else if constexpr (kWide == 32) {
-                    tmem_ld32(saddr, x);
-                } else {
-                    tmem_ld16(saddr + hd0 * NS, x);
-                }
-#pragma unroll
-                for (int y = 0; y < kPairs; ++y) {
-                    const int h = hd_of(y) * 16 + 2 * (y % kPerHead);
-                    t2[y] = fma2(f2(x[h + 8], NC > 1 ? x[h + 9] : 0.f), f2(kLevel2, kLevel2),
-                                 f2(x[h], NC > 1 ? x[h + 1] : 0.f));
-                }
-            }
-            // The token's scales; one that is out of range hides the token's head.
-            const bool in_page = (misc->mask[st][row >> 5] >> (row & 31)) & 1u;
-            bool valid[kHeads];
-            float ks[kHeads], lv[kHeads], ivs[kHeads];
-#pragma unroll
-            for (int hd = 0; hd < kHeads; ++hd) {
-                float k1 = misc->scales[st][row >> lgB][0][hd0 + hd], v1 = misc->scales[st][row >> lgB][1][hd0 + hd];
-                valid[hd] = in_page && scale_ok(k1) && scale_ok(v1);
-                if (in_page && !valid[hd]) set_error(p.err, PK_DEVERR_SCALE);
-                if (!valid[hd]) k1 = v1 = 1.f;         // a weight of zero times its scale stays zero
-                ks[hd] = k1;
-                const uint32_t b = __float_as_uint(v1);
-                lv[hd] = static_cast<float>(static_cast<int>(b >> 23) - 127);
-                if (b & 0x7fffffu) lv[hd] = __log2f(v1);
-                ivs[hd] = fast_rcp(v1);
-            }
-#pragma unroll
-            for (int x = 0; x < kPairs; ++x) {
-                const int hd = hd_of(x);
-                t2[x] = fma2(t2[x], mul2(qf[x], f2(ks[hd], ks[hd])), f2(lv[hd], lv[hd]));
-            }
-            const bool hide = !valid[0] || !valid[kHeads - 1];
-            const bool any_hidden = __any_sync(0xffffffffu, hide);
-            if (MQ || any_hidden) {
-                // Query column y of a head is query token y / G, which sees positions <= its own.
-                const int ahead = mt.z * kTile + row - qm.z;      // of the first query token
-#pragma unroll
-                for (int x = 0; x < kPairs; ++x) {
-                    float2 t = unf2(t2[x]);
-                    const int y = (HP == 1 ? 8 * grp : 0) + 2 * (x % kPerHead);
-                    if (!valid[hd_of(x)] || (MQ && ahead > (y >> lgG))) t.x = -INFINITY;
-                    if (!valid[hd_of(x)] || (MQ && ahead > ((y + 1) >> lgG))) t.y = -INFINITY;
-                    t2[x] = f2(t.x, t.y);
-                }
-            }
-            // Exponents t - m; a reference moves when one exceeds kHeadroom.
-            uint64_t d[kPairs];
-            float top = -INFINITY;
-#pragma unroll
-            for (int x = 0; x < kPairs; ++x) {
-                d[x] = add2(t2[x], neg_m[x]);
-                const float2 v = unf2(d[x]);
-                top = fmaxf(top, fmaxf(v.x, v.y));
-            }
-            if (named_bar_or(bar, 128, top > kHeadroom)) {
-                // Rare: move the references to the running maxima less kStart.
-#pragma unroll
-                for (int x = 0; x < kPairs; ++x) {
-                    const float2 t = unf2(t2[x]);
-                    const float m0 = warp_max_redux(t.x), m1 = NC > 1 ? warp_max_redux(t.y) : m0;
-                    if (lane == 0) {
-                        misc->red[quad][col(x)] = m0;
-                        misc->red[quad][col(x) + 1] = m1;
+                    for (int x = 0; x < kPairs; ++x) {
+                        neg_m[x] = f2(kNoReference, kNoReference);
+                        l_run[x] = 0;
+                        const float *qs = &misc->qscale[seg % kQRing][col(x)];
+                        qf[x] = f2(qs[0] * p.scale_log2, NC > 1 ? qs[1] * p.scale_log2 : 0.f);
                     }
                 }
-                named_bar_sync(bar, 128);
-                float a[kGW];
+                tc_fence_after();
+                // Scores: h columns plus 1/32 of the l columns.
+                uint64_t t2[kPairs];
+                const uint32_t saddr = lane_addr + C_::tS + sb * C_::SCols;
+                {
+                    // h and l columns of this group.
+                    constexpr int kWide = kHeads * 16;
+                    float x[kWide];
+                    if constexpr (kGroups == 2 && HP == 1) {
+                        float h8[8], l8[8];
+                        tmem_ld<8>(saddr + 8 * grp, h8);
+                        tmem_ld<8>(saddr + HL + 8 * grp, l8);
 #pragma unroll
-                for (int j = 0; j < kGW; ++j) a[j] = 1.f;
-#pragma unroll
-                for (int x = 0; x < kPairs; ++x) {
-                    const float2 nm = unf2(neg_m[x]);
-                    float n2[2] = {nm.x, nm.y};
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const int j = col(x) + y;
-                        const float t = fmaxf(fmaxf(misc->red[0][j], misc->red[1][j]),
-                                              fmaxf(misc->red[2][j], misc->red[3][j]));
-                        const float moved = fminf(n2[y], kStart - t);
-                        a[local(x) + y] = fast_exp2(moved - n2[y]);
-                        n2[y] = moved;
+                        for (int y = 0; y < 8; ++y) {
+                            x[y] = h8[y];
+                            x[8 + y] = l8[y];
+                        }
+                    } else if constexpr (kWide == 32) {
+                        tmem_ld32(saddr, x);
+                    } else {
+                        tmem_ld16(saddr + hd0 * NS, x);
                     }
-                    neg_m[x] = f2(n2[0], n2[1]);
-                    l_run[x] = mul2(l_run[x], f2(a[local(x)], a[local(x) + 1]));
-                    d[x] = add2(t2[x], neg_m[x]);
-                }
-                if (!seg_first) {
-                    // O through tile i-1, in TMEM (thread <-> head-dim row).
-                    if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&misc->o_full[(i - 1) & 1]), ((i - 1) >> 1) & 1,
-                                                           &misc->never, lim))) {
-                        misc->abort = 1;
-                        set_error(p.err, PK_DEVERR_TIMEOUT);
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t oaddr = lane_addr + C_::tO + (seg & 1) * NP + 8 * grp;
 #pragma unroll
-                    for (int term = 0; term < 3; ++term) {
-                        float o8[kGW];
-                        tmem_ld<kGW>(oaddr + term * PW, o8);
-#pragma unroll
-                        for (int x = 0; x < kGW; ++x) o8[x] *= a[x];
-                        static_assert(kGW == 8, "one store");
-                        tmem_st8(oaddr + term * PW, o8);
+                    for (int y = 0; y < kPairs; ++y) {
+                        const int h = hd_of(y) * 16 + 2 * (y % kPerHead);
+                        t2[y] = fma2(f2(x[h + 8], NC > 1 ? x[h + 9] : 0.f), f2(kLevel2, kLevel2),
+                                     f2(x[h], NC > 1 ? x[h + 1] : 0.f));
                     }
                 }
-                // red[] is rewritten only in a later rare path, after the next vote.
-            }
-            // Weights in their three terms: words[term][4 columns of the group].
-            static_assert(kGW == 8, "two words a term");
-            uint32_t words[3][2] = {};
-#pragma unroll
-            for (int x = 0; x < kPairs; ++x) {
-                const float2 e = unf2(d[x]);
-                const float u0 = fast_exp2(e.x), u1 = NC > 1 ? fast_exp2(e.y) : 0.f;
-                const float iv = ivs[hd_of(x)];
-                l_run[x] = fma2(f2(u0, u1), f2(iv, iv), l_run[x]);
-                uint32_t h1, h2, h3;
-                split_weights(u0, u1, h1, h2, h3);
-                const int j = local(x), sh = (j & 2) * 8;
-                words[0][j >> 2] |= h1 << sh;
-                words[1][j >> 2] |= h2 << sh;
-                words[2][j >> 2] |= h3 << sh;
-            }
-            // P buffer sb is free once P.V of tile i-2 is done.
-            if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&misc->o_full[sb]), ((i >> 1) & 1) ^ 1, &misc->never,
-                                                   lim))) {
-                misc->abort = 1;
-                set_error(p.err, PK_DEVERR_TIMEOUT);
-                break;
-            }
-            // Rows of hidden tokens are zeroed once this tile's V has landed: the
-            // MMA multiplies every V row by its weight, and theirs may hold stale
-            // bytes or NaN.
-            if (any_hidden &&
-                !__all_sync(0xffffffffu, mbar_wait(smem_u32(&misc->vfull[st]), (i / kStages) & 1, &misc->never,
-                                                   lim))) {
-                misc->abort = 1;
-                set_error(p.err, PK_DEVERR_TIMEOUT);
-                break;
-            }
-            if (hide && (HP == 2 || grp == 0)) {
+                // The token's scales; one that is out of range hides the token's head.
+                const bool in_page = (misc->mask[st][row >> 5] >> (row & 31)) & 1u;
+                bool valid[kHeads];
+                float ks[kHeads], lv[kHeads], ivs[kHeads];
 #pragma unroll
                 for (int hd = 0; hd < kHeads; ++hd) {
-                    if (valid[hd]) continue;
-                    uint4 *vrow = reinterpret_cast<uint4 *>(stage_ptr + st * C_::StageBytes + C_::VOff +
-                                                            (hd0 + hd) * C_::HeadBytes + row * D);
-#pragma unroll
-                    for (int x = 0; x < D / 16; ++x) vrow[x] = make_uint4(0, 0, 0, 0);
+                    float k1 = misc->scales[st][row >> lgB][0][hd0 + hd], v1 = misc->scales[st][row >> lgB][1][hd0 + hd];
+                    valid[hd] = in_page && scale_ok(k1) && scale_ok(v1);
+                    if (in_page && !valid[hd]) set_error(p.err, PK_DEVERR_SCALE);
+                    if (!valid[hd]) k1 = v1 = 1.f;         // a weight of zero times its scale stays zero
+                    ks[hd] = k1;
+                    const uint32_t b = __float_as_uint(v1);
+                    lv[hd] = static_cast<float>(static_cast<int>(b >> 23) - 127);
+                    if (b & 0x7fffffu) lv[hd] = __log2f(v1);
+                    ivs[hd] = fast_rcp(v1);
                 }
-            }
-            // MN-major, no swizzle: 16 columns side by side, 8 tokens 16 bytes
-            // apart, 128 bytes to the next 16 columns, 8 NP to the next 8 tokens.
-            uint8_t *prow = p_ptr + sb * C_::PBytes + (row >> 3) * (8 * NP) + (row & 7) * 16;
-            if constexpr (PW == 8) {
-                *reinterpret_cast<uint4 *>(prow) = make_uint4(words[0][0], words[0][1], words[1][0], words[1][1]);
-                *reinterpret_cast<uint4 *>(prow + 128) = make_uint4(words[2][0], words[2][1], 0, 0);
-            } else {
 #pragma unroll
-                for (int x = 0; x < 3; ++x)
-                    *reinterpret_cast<uint2 *>(prow + 128 * x + 8 * grp) = make_uint2(words[x][0], words[x][1]);
+                for (int x = 0; x < kPairs; ++x) {
+                    const int hd = hd_of(x);
+                    t2[x] = fma2(t2[x], mul2(qf[x], f2(ks[hd], ks[hd])), f2(lv[hd], lv[hd]));
+                }
+                const bool hide = !valid[0] || !valid[kHeads - 1];
+                const bool any_hidden = __any_sync(0xffffffffu, hide);
+                if (MQ || any_hidden) {
+                    // Query column y of a head is query token y / G, which sees positions <= its own.
+                    const int ahead = mt.z * kTile + row - qm.z;      // of the first query token
+#pragma unroll
+                    for (int x = 0; x < kPairs; ++x) {
+                        float2 t = unf2(t2[x]);
+                        const int y = (HP == 1 ? 8 * grp : 0) + 2 * (x % kPerHead);
+                        if (!valid[hd_of(x)] || (MQ && ahead > (y >> lgG))) t.x = -INFINITY;
+                        if (!valid[hd_of(x)] || (MQ && ahead > ((y + 1) >> lgG))) t.y = -INFINITY;
+                        t2[x] = f2(t.x, t.y);
+                    }
+                }
+                // Exponents t - m; a reference moves when one exceeds kHeadroom.
+                uint64_t d[kPairs];
+                float top = -INFINITY;
+#pragma unroll
+                for (int x = 0; x < kPairs; ++x) {
+                    d[x] = add2(t2[x], neg_m[x]);
+                    const float2 v = unf2(d[x]);
+                    top = fmaxf(top, fmaxf(v.x, v.y));
+                }
+                if (named_bar_or(bar, 128, top > kHeadroom)) {
+                    // Rare: move the references to the running maxima less kStart.
+#pragma unroll
+                    for (int x = 0; x < kPairs; ++x) {
+                        const float2 t = unf2(t2[x]);
+                        const float m0 = warp_max_redux(t.x), m1 = NC > 1 ? warp_max_redux(t.y) : m0;
+                        if (lane == 0) {
+                            misc->red[quad][col(x)] = m0;
+                            misc->red[quad][col(x) + 1] = m1;
+                        }
+                    }
+                    named_bar_sync(bar, 128);
+                    float a[kGW];
+#pragma unroll
+                    for (int j = 0; j < kGW; ++j) a[j] = 1.f;
+#pragma unroll
+                    for (int x = 0; x < kPairs; ++x) {
+                        const float2 nm = unf2(neg_m[x]);
+                        float n2[2] = {nm.x, nm.y};
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const int j = col(x) + y;
+                            const float t = fmaxf(fmaxf(misc->red[0][j], misc->red[1][j]),
+                                                  fmaxf(misc->red[2][j], misc->red[3][j]));
+                            const float moved = fminf(n2[y], kStart - t);
+                            a[local(x) + y] = fast_exp2(moved - n2[y]);
+                            n2[y] = moved;
+                        }
+                        neg_m[x] = f2(n2[0], n2[1]);
+                        l_run[x] = mul2(l_run[x], f2(a[local(x)], a[local(x) + 1]));
+                        d[x] = add2(t2[x], neg_m[x]);
+                    }
+                    if (!seg_first) {
+                        // O through tile i-1, in TMEM (thread <-> head-dim row).
+                        if (!__all_sync(0xffffffffu, wait_for(smem_u32(&misc->o_full[(i - 1) & 1]), ((i - 1) >> 1) & 1,
+                                                               &misc->never, lim))) {
+                            misc->abort = 1;
+                            set_error(p.err, PK_DEVERR_TIMEOUT);
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t oaddr = lane_addr + C_::tO + (seg & 1) * NP + 8 * grp;
+#pragma unroll
+                        for (int term = 0; term < 3; ++term) {
+                            float o8[kGW];
+                            tmem_ld<kGW>(oaddr + term * PW, o8);
+#pragma unroll
+                            for (int x = 0; x < kGW; ++x) o8[x] *= a[x];
+                            static_assert(kGW == 8, "one store");
+                            tmem_st8(oaddr + term * PW, o8);
+                        }
+                    }
+                    // red[] is rewritten only in a later rare path, after the next vote.
+                }
+                // Weights in their three terms: words[term][4 columns of the group].
+                static_assert(kGW == 8, "two words a term");
+                uint32_t words[3][2] = {};
+#pragma unroll
+                for (int x = 0; x < kPairs; ++x) {
+                    const float2 e = unf2(d[x]);
+                    const float u0 = fast_exp2(e.x), u1 = NC > 1 ? fast_exp2(e.y) : 0.f;
+                    const float iv = ivs[hd_of(x)];
+                    l_run[x] = fma2(f2(u0, u1), f2(iv, iv), l_run[x]);
+                    uint32_t h1, h2, h3;
+                    split_weights(u0, u1, h1, h2, h3);
+                    const int j = local(x), sh = (j & 2) * 8;
+                    words[0][j >> 2] |= h1 << sh;
+                    words[1][j >> 2] |= h2 << sh;
+                    words[2][j >> 2] |= h3 << sh;
+                }
+                // P buffer sb is free once P.V of tile i-2 is done.
+                if (!__all_sync(0xffffffffu, wait_for(smem_u32(&misc->o_full[sb]), ((i >> 1) & 1) ^ 1, &misc->never,
+                                                       lim))) {
+                    misc->abort = 1;
+                    set_error(p.err, PK_DEVERR_TIMEOUT);
+                    break;
+                }
+                // Rows of hidden tokens are zeroed once this tile's V has landed: the
+                // MMA multiplies every V row by its weight, and theirs may hold stale
+                // bytes or NaN.
+                if (any_hidden &&
+                    !__all_sync(0xffffffffu, wait_for(smem_u32(&misc->vfull[st]), (i / kStages) & 1, &misc->never,
+                                                       lim))) {
+                    misc->abort = 1;
+                    set_error(p.err, PK_DEVERR_TIMEOUT);
+                    break;
+                }
+                if (hide && (HP == 2 || grp == 0)) {
+#pragma unroll
+                    for (int hd = 0; hd < kHeads; ++hd) {
+                        if (valid[hd]) continue;
+                        uint4 *vrow = reinterpret_cast<uint4 *>(stage_ptr + st * C_::StageBytes + C_::VOff +
+                                                                (hd0 + hd) * C_::HeadBytes + row * D);
+#pragma unroll
+                        for (int x = 0; x < D / 16; ++x) vrow[x] = make_uint4(0, 0, 0, 0);
+                    }
+                }
+                // MN-major, no swizzle: 16 columns side by side, 8 tokens 16 bytes
+                // apart, 128 bytes to the next 16 columns, 8 NP to the next 8 tokens.
+                uint8_t *prow = p_ptr + sb * C_::PBytes + (row >> 3) * (8 * NP) + (row & 7) * 16;
+                if constexpr (PW == 8) {
+                    *reinterpret_cast<uint4 *>(prow) = make_uint4(words[0][0], words[0][1], words[1][0], words[1][1]);
+                    *reinterpret_cast<uint4 *>(prow + 128) = make_uint4(words[2][0], words[2][1], 0, 0);
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 3; ++x)
+                        *reinterpret_cast<uint2 *>(prow + 128 * x + 8 * grp) = make_uint2(words[x][0], words[x][1]);
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&misc->p_full[sb]));
             }
-            fence_proxy_async_smem();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&misc->p_full[sb]));
 
             // The previous segment's read-out, one tile late.
             if (pending && !finalize()) {
@@ -1087,12 +1098,6 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 pend_complete = seg_t0 == 0 && mt.z == mt.w - 1;
                 pend_cut_end = mt.z == mt.w - 1;
                 close_segment();
-                if (i == n_tiles - 1) named_bar_sync(bar, 128);
-                if (i == n_tiles - 1 && !finalize()) {
-                    misc->abort = 1;
-                    set_error(p.err, PK_DEVERR_TIMEOUT);
-                    break;
-                }
             }
         }
         tc_fence_before();

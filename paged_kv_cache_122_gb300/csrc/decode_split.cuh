@@ -62,6 +62,7 @@ struct Walk {
         t = 0;
         if (++h < nh) return;
         h = 0;
+#pragma unroll 1
         do {
             if (++s >= ns) return;
             load(len);
@@ -93,6 +94,7 @@ __device__ __forceinline__ int64_t plan_range(const LenSrc lens, MiscT *misc, in
     const int cap = lens.cap;
     int64_t mine = 0, mine_w = 0;
     int bad = 0;
+#pragma unroll 1
     for (int s = s_lo; s < s_hi; ++s) {
         const int raw = lens.raw(s);
         bad |= raw <= 0 || raw > cap;
@@ -104,6 +106,7 @@ __device__ __forceinline__ int64_t plan_range(const LenSrc lens, MiscT *misc, in
     int64_t T, W;
     const int64_t my_off = block_exclusive_scan<kThreadsT>(mine, misc->scan, &T);
     const int64_t my_off_w = block_exclusive_scan<kThreadsT>(mine_w, misc->scan_w, &W);
+#pragma unroll 1
     for (int k = 0; k < 2; ++k) {
         const int64_t P = static_cast<int64_t>(c + k) * W / C;
         if (P >= W) {
@@ -112,7 +115,8 @@ __device__ __forceinline__ int64_t plan_range(const LenSrc lens, MiscT *misc, in
         }
         if (my_off_w <= P && P < my_off_w + mine_w) {
             int64_t acc_t = my_off, acc_w = my_off_w;
-            for (int s = s_lo; s < s_hi; ++s) {
+        #pragma unroll 1
+    for (int s = s_lo; s < s_hi; ++s) {
                 const int L = lens(s);
                 const int64_t nt = (L + kTile - 1) / kTile;
                 const int64_t segc = seg_total(nt, L);
@@ -141,7 +145,8 @@ __device__ __forceinline__ int64_t plan_range(const LenSrc lens, MiscT *misc, in
     if (misc->bnd[1] > b0) {
         int64_t acc = my_off, acc_w = my_off_w;
         if (acc <= b0 && b0 < acc + mine) {
-            for (int s = s_lo; s < s_hi; ++s) {
+        #pragma unroll 1
+    for (int s = s_lo; s < s_hi; ++s) {
                 const int L = lens(s);
                 const int64_t nt = (L + kTile - 1) / kTile;
                 const int64_t w = nt * Hkv;
