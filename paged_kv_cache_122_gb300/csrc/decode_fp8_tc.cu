@@ -1110,6 +1110,146 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     }
 }
 
+// Merge of cut segments.  CTA (c, y) combines query columns 2 y and 2 y + 1 of
+// the segment that was cut at the start of CTA c's range and ends in it, from
+// every CTA it spans; thread r handles O^T row r.  Two parts are one round
+// trip.  A segment of a long context spans dozens of CTAs (at one sequence of
+// 131,072 tokens, 38): their headers are read side by side by the threads, the
+// weights follow in shared memory, and the rows are added with kMergeAhead
+// reads on their way -- part after part, the chain of reads took longer than
+// the attention.  The order of the sum is the parts' order in any case.
+constexpr int kMergeAhead = 8;
+
+template <int D, int NC, int HP>
+__global__ void __launch_bounds__(128)
+decode_fp8_merge_kernel(const DecodeParams p, int C) {
+    constexpr int CW = HP == 2 ? 8 : kNPad;
+    constexpr int kCols = NC < 2 ? 1 : 2;                   // columns per head of this CTA
+    constexpr int kAll = HP * kCols;
+    __shared__ int part_slot[kTcMaxCtas];                   // slot of a part, -1 for an empty range
+    __shared__ float part_m[kTcMaxCtas][kAll], part_l[kTcMaxCtas][kAll], den_all[kAll];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const Slot *slots = static_cast<const Slot *>(p.tc_slots);
+    const int c = blockIdx.x, y = blockIdx.y;
+    const int row = threadIdx.x;
+    const int hr = HP == 2 ? row >> 6 : 0;
+    const int dd = HP == 2 ? (row & 63) : row;
+    const bool row_ok = HP == 2 || row < D;
+    const int orow = row_ok ? row : 0;
+    const int j0 = hr * CW + 2 * y;                         // this row's first column in the slots
+    const Slot *mine = slots + 2 * c;
+    // Everything two parts need is read at once, before the flag is known.
+    const Slot *q0 = slots + 2 * (c > 0 ? c - 1 : c);
+    const Slot *q1 = q0 + 1;
+    const int flag = mine->flag;
+    const int s = mine->s, h = mine->h;
+    const int64_t start = mine->start_tile, T = mine->total_tiles;
+    const int ca = mine->first_cta;
+    const int64_t beg_prev = q0->range_beg;
+    float mm[kCols], ml[kCols], mo[kCols], am[kCols], al[kCols], ao[kCols], bm[kCols], bl[kCols], bo[kCols];
+#pragma unroll
+    for (int x = 0; x < kCols; ++x) {
+        const int j = j0 + x;
+        mm[x] = mine->m[j];
+        ml[x] = mine->l[j];
+        mo[x] = mine->o[j * 128 + orow];
+        am[x] = q0->m[j];
+        al[x] = q0->l[j];
+        ao[x] = q0->o[j * 128 + orow];
+        bm[x] = q1->m[j];
+        bl[x] = q1->l[j];
+        bo[x] = q1->o[j * 128 + orow];
+    }
+    if (flag != 1) return;                                  // the same for the whole CTA
+    float num[kCols], den[kCols];
+    if (ca == c - 1) {
+        const bool first_of_prev = beg_prev >= start;
+#pragma unroll
+        for (int x = 0; x < kCols; ++x) {
+            const float pm = first_of_prev ? am[x] : bm[x];
+            const float pl = first_of_prev ? al[x] : bl[x];
+            const float po = first_of_prev ? ao[x] : bo[x];
+            const float M = fmaxf(pm, mm[x]);
+            const float a0 = fast_exp2(pm - M), a1 = fast_exp2(mm[x] - M);
+            den[x] = a0 * pl + a1 * ml[x];
+            num[x] = a0 * po + a1 * mo[x];
+        }
+    } else {
+        const int parts = c - ca + 1;
+#pragma unroll 1
+        for (int i = threadIdx.x; i < parts; i += 128) {
+            const int cc = ca + i;
+            const int64_t b0 = slots[2 * cc].range_beg, b1 = cc + 1 < C ? slots[2 * (cc + 1)].range_beg : T;
+            const int at = 2 * cc + (b0 >= start ? 0 : 1);
+            part_slot[i] = b0 == b1 ? -1 : at;
+#pragma unroll
+            for (int x = 0; x < kAll; ++x) {
+                const int j = x / kCols * CW + 2 * y + x % kCols;
+                part_m[i][x] = b0 == b1 ? -INFINITY : slots[at].m[j];
+                part_l[i][x] = b0 == b1 ? 0.f : slots[at].l[j];
+            }
+        }
+        __syncthreads();
+        // One warp a column: the largest reference, the weights, the denominator.
+        const int x = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        if (x < kAll) {
+            float M = -INFINITY, sum = 0.f;
+            for (int i = lane; i < parts; i += 32) M = fmaxf(M, part_m[i][x]);
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+            for (int i = lane; i < parts; i += 32) {
+                const float a = rescale(part_m[i][x], M);
+                part_m[i][x] = a;
+                sum = fmaf(a, part_l[i][x], sum);
+            }
+            sum = warp_sum(sum);
+            if (lane == 0) den_all[x] = sum;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) {
+            num[k] = 0.f;
+            den[k] = den_all[hr * kCols + k];
+        }
+        for (int i0 = 0; i0 < parts; i0 += kMergeAhead) {
+            float o[kMergeAhead][kCols];
+#pragma unroll
+            for (int i = 0; i < kMergeAhead; ++i) {
+                const int at = i0 + i < parts ? part_slot[i0 + i] : -1;
+#pragma unroll
+                for (int k = 0; k < kCols; ++k) o[i][k] = at >= 0 ? slots[at].o[(j0 + k) * 128 + orow] : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < kMergeAhead; ++i) {
+                if (i0 + i < parts) {
+#pragma unroll
+                    for (int k = 0; k < kCols; ++k) num[k] = fmaf(part_m[i0 + i][hr * kCols + k], o[i][k], num[k]);
+                }
+            }
+        }
+    }
+    if (!row_ok) return;
+    // Column cq: query token cq / G of the sequence, query head cq % G of this
+    // row's KV head; a sequence whose rows are not within the queries given has none.
+    const int Gq = p.num_heads / p.num_kv_heads, lgG = __ffs(Gq) - 1;
+    int row0 = s, qn = 1;
+    if (p.cu_q_lens) {
+        row0 = p.cu_q_lens[s];
+        const int row1 = p.cu_q_lens[s + 1];
+        qn = row1 - row0;
+        if (row0 < 0 || qn < 0 || row1 > p.total_q || qn > p.q_len) return;
+    }
+#pragma unroll
+    for (int x = 0; x < kCols; ++x) {
+        const int cq = 2 * y + x;
+        if ((cq >> lgG) >= qn) continue;
+        const int qh = (h * HP + hr) * Gq + (cq & (Gq - 1));
+        store_out(p, (static_cast<size_t>(row0 + (cq >> lgG)) * p.num_heads + qh) * D + dd,
+                  den[x] != 0.f ? num[x] / den[x] : 0.f);
+    }
+}
+
 // ---------------------------------------------------------------- host side
 PFN_cuTensorMapEncodeTiled_v12000 get_encoder() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
@@ -1164,9 +1304,10 @@ cudaError_t launch_shape(const DecodeFp8Params &p, int sms, cudaStream_t stream)
     e = cudaLaunchKernelEx(&cfg, kernel, mk, mv, p);
     if (e != cudaSuccess) return e;
     if (!p.tc_slots) return cudaSuccess;   // no sequence longer than one tile: nothing is cut
+    cfg.gridDim = dim3(C, (NC + 1) / 2);
     cfg.blockDim = dim3(128);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, decode_tc_merge_kernel<D, NC, HP, true>, static_cast<const DecodeParams &>(p), C);
+    return cudaLaunchKernelEx(&cfg, decode_fp8_merge_kernel<D, NC, HP>, static_cast<const DecodeParams &>(p), C);
 }
 
 template <int NC>

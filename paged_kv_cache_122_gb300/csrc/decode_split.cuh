@@ -196,10 +196,7 @@ __device__ __forceinline__ void store_out(const DecodeParams &p, size_t idx, flo
 // One CTA per decode CTA c: if c's first segment was cut at its start and
 // ends in c, combine the parts of that segment from every CTA it spans.
 // Thread r handles O^T row r (as the decode kernel's TMEM lanes).
-// kStrict: a denominator that is not a number gives that as the output instead
-// of zero, and a sequence whose query rows are not within p.total_q, or more
-// than p.q_len, is left out.
-template <int D, int NC, int HP, bool kStrict = false>
+template <int D, int NC, int HP>
 __global__ void __launch_bounds__(128)
 decode_tc_merge_kernel(const DecodeParams p, int C) {
     constexpr int CW = HP == 2 ? 8 : kNPad;
@@ -291,15 +288,12 @@ decode_tc_merge_kernel(const DecodeParams p, int C) {
     const int Gq = p.num_heads / p.num_kv_heads, lgG = __ffs(Gq) - 1;
     const int q0row = p.cu_q_lens ? p.cu_q_lens[s] : s;
     const int qn = p.cu_q_lens ? p.cu_q_lens[s + 1] - q0row : 1;
-    if constexpr (kStrict) {
-        if (p.cu_q_lens && (q0row < 0 || qn < 0 || p.cu_q_lens[s + 1] > p.total_q || qn > p.q_len)) return;
-    }
 #pragma unroll
     for (int cq = 0; cq < NC; ++cq) {
         if ((cq >> lgG) >= qn) continue;
         const int qh = (h * HP + hr) * Gq + (cq & (Gq - 1));
         store_out(p, (static_cast<size_t>(q0row + (cq >> lgG)) * p.num_heads + qh) * D + dd,
-                  (kStrict ? den[cq] != 0.f : den[cq] > 0.f) ? num[cq] / den[cq] : 0.f);
+                  den[cq] > 0.f ? num[cq] / den[cq] : 0.f);
     }
 }
 
