@@ -338,8 +338,8 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         w.ns = N;
         w.s = misc->s0;
         w.load(lens);
-        w.h = static_cast<int>(misc->rem0 / w.nt);
-        w.t = static_cast<int>(misc->rem0 % w.nt);
+        w.h = static_cast<int>(quotient(misc->rem0, w.nt));
+        w.t = static_cast<int>(misc->rem0 - static_cast<int64_t>(w.h) * w.nt);
         return w;
     };
     auto wait_prev = [&]() {
@@ -457,14 +457,11 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             ahead_phys[kAhead - 1] = fetch_next();
             if (i < 0) continue;
             const int st = i % kStages;
-            int got = 1;
-            if (lane == 0)
-                got = wait_for(smem_u32(&misc->empty[st]), ((i / kStages) & 1) ^ 1, &misc->abort, lim);
-            if (!__shfl_sync(0xffffffffu, got, 0)) {      // one decision for the whole warp
-                if (lane == 0) {
-                    misc->abort = 1;
-                    set_error(p.err, PK_DEVERR_TIMEOUT);
-                }
+            // Every lane waits (a lane that waited alone would leave the warp split
+            // for what follows); one decision for the whole warp.
+            if (!__all_sync(0xffffffffu, wait_for(smem_u32(&misc->empty[st]), ((i / kStages) & 1) ^ 1, &misc->abort, lim))) {
+                misc->abort = 1;
+                set_error(p.err, PK_DEVERR_TIMEOUT);
                 break;
             }
             const int vlen = min(kTile, w.L - w.t * kTile);
@@ -632,36 +629,37 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             const int left = min(w.nt - w.t, n_tiles - i);
             if ((sg & 1) == warp - C_::QueryWarp) {
                 const int2 qr = query_rows(w.s);
+                // Row x of the buffer: query column x % NC of head x / NC of the pair;
+                // column cq: query token cq / G, query head cq % G.  For one token
+                // (NC == G) the rows are consecutive.
                 uint4 raw[kIters];
+                const uint16_t *rows = p.q + (static_cast<size_t>(qr.x) * H + w.h * HP * Gq) * D + part * 8;
 #pragma unroll
                 for (int y = 0; y < kIters; ++y) {
-                    // Row x of the buffer: query column x % NC of head x / NC of the
-                    // pair; column cq: query token cq / G, query head cq % G.
                     const int x = y * kRows + sub, cq = x % NC;
                     raw[y] = make_uint4(0, 0, 0, 0);
                     if (x < HP * NC && (cq >> lgG) < qr.y) {
-                        const size_t head = static_cast<size_t>(qr.x + (cq >> lgG)) * H + (w.h * HP + x / NC) * Gq + (cq & (Gq - 1));
-                        raw[y] = __ldg(reinterpret_cast<const uint4 *>(p.q + head * D + part * 8));
+                        const int at = MQ ? ((cq >> lgG) * H + x / NC * Gq + (cq & (Gq - 1))) * D : x * D;
+                        raw[y] = ldg_stream(rows + at);      // volatile: stays ahead of the wait
                     }
                 }
                 const int qb = sg % C_::QBufs;
-                int got = 1;
-                if (lane == 0)
-                    got = wait_for(smem_u32(&misc->qempty[qb]), ((sg / C_::QBufs) & 1) ^ 1, &misc->abort, lim);
-                if (!__shfl_sync(0xffffffffu, got, 0)) {
-                    if (lane == 0) {
-                        misc->abort = 1;
-                        set_error(p.err, PK_DEVERR_TIMEOUT);
-                    }
+                if (!__all_sync(0xffffffffu, wait_for(smem_u32(&misc->qempty[qb]), ((sg / C_::QBufs) & 1) ^ 1, &misc->abort, lim))) {
+                    misc->abort = 1;
+                    set_error(p.err, PK_DEVERR_TIMEOUT);
                     break;
                 }
                 uint8_t *buf = q_ptr + qb * C_::QBufBytes;
-#pragma unroll
+                // Not unrolled (the code of every warp's part shares the instruction
+                // cache): the rows move up in their registers instead.
+#pragma unroll 1
                 for (int y = 0; y < kIters; ++y) {
                     const int x = y * kRows + sub, hd = x / NC, cq = x % NC;
                     // The row's largest magnitude: bf16 bits without the sign order as integers.
                     uint32_t top = 0;
-                    const uint32_t words[4] = {raw[y].x, raw[y].y, raw[y].z, raw[y].w};
+                    const uint32_t words[4] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w};
+#pragma unroll
+                    for (int e = 0; e + 1 < kIters; ++e) raw[e] = raw[e + 1];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const uint32_t v = words[e] & 0x7fff7fffu;
@@ -756,65 +754,52 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             // This row's columns: of one head, first_col .. first_col + kMine - 1.
             constexpr int kMine = kGroups == 2 ? 8 : NC;
             const int first_col = kGroups == 2 ? 8 * grp : hr * 8;
-            const bool mine = row_ok && (HP == 1 || kGroups == 1 || hr == grp);
-            float l[kMine], o[kMine];
-            const float (*ls)[kNPad] = misc->lsum[pend_seg & 1];
+            if constexpr (kHeads == 2) {
 #pragma unroll
-            for (int x = 0; x < kMine; ++x) {
-                const int j = first_col + x;
-                l[x] = ls[0][j] + ls[1][j] + ls[2][j] + ls[3][j];
-                if constexpr (kHeads == 2) o[x] = hr ? ov[PC + x] : ov[x];
-                else o[x] = ov[x];
+                for (int x = 0; x < kMine; ++x) ov[x] = hr ? ov[PC + x] : ov[x];
             }
+            // Lane x sums column x's denominator for the warp.
+            float l = 0.f;
+            if (lane < kMine) {
+                const float *ls = &misc->lsum[pend_seg & 1][0][first_col + lane];
+                l = ls[0] + ls[kNPad] + ls[2 * kNPad] + ls[3 * kNPad];
+            }
+            // A cut part goes to slot 0 if the segment is this CTA's first, 1 if not.
+            Slot *sl = slots + 2 * c + (pend_i0 == 0 ? 0 : 1);
+            const bool mine = row_ok && (HP == 1 || kGroups == 1 || hr == grp);
             if (pend_complete) {
-                if (mine) {
-                    // Query column cq: token cq / G of the sequence, head cq % G of the KV head.
-                    const int cq0 = HP == 1 ? first_col : 0;
-                    const size_t base = (static_cast<size_t>(MQ ? pend_q0 : pend_s) * H + (pend_h * HP + hr) * Gq) * D + dd;
-                    const size_t row_step = static_cast<size_t>(H) * D;
-                    const int used = MQ ? min(NC, pend_qn << lgG) - cq0 : NC - cq0;     // the rest are padding
+                // Query column cq: token cq / G of the sequence, head cq % G of the KV head.
+                const int cq0 = HP == 1 ? first_col : 0;
+                const size_t base = (static_cast<size_t>(MQ ? pend_q0 : pend_s) * H + (pend_h * HP + hr) * Gq) * D + dd;
+                const int used = MQ ? min(NC, pend_qn << lgG) - cq0 : NC - cq0;     // the rest are padding
+                const float inv = l != 0.f ? __fdividef(1.f, l) : 0.f;
 #pragma unroll
-                    for (int x = 0; x < kMine; ++x) o[x] = l[x] != 0.f ? __fdividef(o[x], l[x]) : 0.f;
-                    auto at = [&](int x) -> size_t {
-                        const int cq = cq0 + x;
-                        return MQ ? base + (cq >> lgG) * row_step + (cq & (Gq - 1)) * D : base + cq * D;
-                    };
-                    if (p.out_fp32) {
-                        float *out = static_cast<float *>(p.out);
-#pragma unroll
-                        for (int x = 0; x < kMine; ++x)
-                            if (x < used) out[at(x)] = o[x];
-                    } else {
-                        uint16_t *out = static_cast<uint16_t *>(p.out);
-#pragma unroll
-                        for (int x = 0; x < kMine; ++x)
-                            if (x < used) out[at(x)] = static_cast<uint16_t>(pack_bf16x2(o[x], 0.f));
-                    }
+                for (int x = 0; x < kMine; ++x) {
+                    const float o = ov[x] * __shfl_sync(0xffffffffu, inv, x);
+                    const int cq = cq0 + x;
+                    const size_t at = MQ ? base + static_cast<size_t>(cq >> lgG) * H * D + (cq & (Gq - 1)) * D : base + cq * D;
+                    if (mine && x < used) store_out(p, at, o);
                 }
             } else {
-                // A cut part: slot 0 if the segment is this CTA's first, 1 if not.
-                const int slot_idx = pend_i0 == 0 ? 0 : 1;
-                Slot *sl = slots + 2 * c + slot_idx;
                 if (mine) {
 #pragma unroll
-                    for (int x = 0; x < kMine; ++x) {
-                        sl->o[(first_col + x) * 128 + row] = o[x];
-                        if (dd == 0) {
-                            sl->l[first_col + x] = l[x];
-                            sl->m[first_col + x] = misc->mref[pend_seg & 1][first_col + x];
-                        }
-                    }
+                    for (int x = 0; x < kMine; ++x) sl->o[(first_col + x) * 128 + row] = ov[x];
                 }
-                if (row == 0 && grp == 0) {
-                    sl->s = pend_s;
-                    sl->h = pend_h;
-                    sl->start_tile = beg + pend_i0 - pend_t0;
-                    sl->total_tiles = T;
-                    // Cut at its start and finished here: this CTA merges it.
-                    if (slot_idx == 0) {
-                        sl->flag = (pend_t0 > 0 && pend_cut_end) ? 1 : 0;
-                        sl->first_cta = misc->first_cta;
-                    }
+                // The warp with element 0 of the head's rows writes its columns' sums.
+                if ((quad == 0 || (HP == 2 && quad == 2)) && (HP == 1 || kGroups == 1 || hr == grp) && lane < kMine) {
+                    sl->l[first_col + lane] = l;
+                    sl->m[first_col + lane] = misc->mref[pend_seg & 1][first_col + lane];
+                }
+            }
+            if (!pend_complete && row == 0 && grp == 0) {
+                sl->s = pend_s;
+                sl->h = pend_h;
+                sl->start_tile = beg + pend_i0 - pend_t0;
+                sl->total_tiles = T;
+                // Cut at its start and finished here: this CTA merges it.
+                if (pend_i0 == 0) {
+                    sl->flag = (pend_t0 > 0 && pend_cut_end) ? 1 : 0;
+                    sl->first_cta = misc->first_cta;
                 }
             }
             pending = false;
@@ -1007,7 +992,7 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                         }
                         tc_fence_after();
                         const uint32_t oaddr = lane_addr + C_::tO + (seg & 1) * NP + 8 * grp;
-#pragma unroll
+#pragma unroll 1
                         for (int term = 0; term < 3; ++term) {
                             float o8[kGW];
                             tmem_ld<kGW>(oaddr + term * PW, o8);

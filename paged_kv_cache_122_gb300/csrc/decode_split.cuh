@@ -70,6 +70,10 @@ struct Walk {
     }
 };
 
+// 64-bit division, out of line: each copy of its code is as long as the rest
+// of the plan, and the warps' different loops share one instruction cache.
+__device__ __noinline__ int64_t quotient(int64_t a, int64_t b) { return a / b; }
+
 // This CTA's range of the flattened tile space.  Tile x, whose cost interval
 // starts at a_x (a segment's tile 0 at its start, tile t >= 1 at start +
 // seg_cost + full * t, full the cost of a full tile), belongs to CTA k when
@@ -108,7 +112,7 @@ __device__ __forceinline__ int64_t plan_range(const LenSrc lens, MiscT *misc, in
     const int64_t my_off_w = block_exclusive_scan<kThreadsT>(mine_w, misc->scan_w, &W);
 #pragma unroll 1
     for (int k = 0; k < 2; ++k) {
-        const int64_t P = static_cast<int64_t>(c + k) * W / C;
+        const int64_t P = quotient(static_cast<int64_t>(c + k) * W, C);
         if (P >= W) {
             if (threadIdx.x == 0) misc->bnd[k] = T;
             continue;
@@ -123,10 +127,10 @@ __device__ __forceinline__ int64_t plan_range(const LenSrc lens, MiscT *misc, in
                 const int64_t cw = segc * Hkv;
                 if (P < acc_w + cw) {
                     const int64_t q = P - acc_w;
-                    int64_t h = q / segc;
+                    int64_t h = quotient(q, segc);
                     const int64_t r = q - h * segc;
                     // The first tile of the segment that starts at or after r.
-                    int64_t t = r == 0 ? 0 : (r - seg_cost + full - 1) / full;
+                    int64_t t = r == 0 ? 0 : quotient(r - seg_cost + full - 1, full);
                     if (r > 0 && t < 1) t = 1;
                     if (t >= nt) {
                         ++h;
@@ -155,11 +159,11 @@ __device__ __forceinline__ int64_t plan_range(const LenSrc lens, MiscT *misc, in
                     misc->rem0 = b0 - acc;
                     // If the range starts inside a segment, the CTA where that
                     // segment starts (the owner of its tile 0's cost start).
-                    const int64_t h0 = (b0 - acc) / nt;
+                    const int64_t h0 = quotient(b0 - acc, nt);
                     const int64_t a = acc_w + h0 * seg_total(nt, L);
-                    int64_t k = W > 0 ? a * C / W : 0;
-                    while (k + 1 < C && (k + 1) * W / C <= a) ++k;
-                    while (k > 0 && k * W / C > a) --k;
+                    int64_t k = W > 0 ? quotient(a * C, W) : 0;
+                    while (k + 1 < C && quotient((k + 1) * W, C) <= a) ++k;
+                    while (k > 0 && quotient(k * W, C) > a) --k;
                     misc->first_cta = static_cast<int32_t>(k);
                     break;
                 }
