@@ -457,13 +457,7 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             ahead_phys[kAhead - 1] = fetch_next();
             if (i < 0) continue;
             const int st = i % kStages;
-            // Every lane waits (a lane that waited alone would leave the warp split
-            // for what follows); one decision for the whole warp.
-            if (!__all_sync(0xffffffffu, wait_for(smem_u32(&misc->empty[st]), ((i / kStages) & 1) ^ 1, &misc->abort, lim))) {
-                misc->abort = 1;
-                set_error(p.err, PK_DEVERR_TIMEOUT);
-                break;
-            }
+            // What the tile needs is worked out before the wait for its stage.
             const int vlen = min(kTile, w.L - w.t * kTile);
             const int pages = (vlen + B - 1) >> lgB;
             bool ok = false;
@@ -489,6 +483,14 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             if constexpr (MQ) {
                 if (w.s != qr_of) qr = query_rows(qr_of = w.s);
             }
+            const int piece = phys * p.num_kv_heads + w.h * HP;
+            // Every lane waits (a lane that waited alone would leave the warp split
+            // for what follows); one decision for the whole warp.
+            if (!__all_sync(0xffffffffu, wait_for(smem_u32(&misc->empty[st]), ((i / kStages) & 1) ^ 1, &misc->abort, lim))) {
+                misc->abort = 1;
+                set_error(p.err, PK_DEVERR_TIMEOUT);
+                break;
+            }
             if (lane == 0 && do_v) mbar_arrive_expect_tx(vfull, nok * (HP * D) << lgB);
             if (lane == 0 && do_k) {
                 misc->mask[st][0] = m0;
@@ -502,7 +504,6 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             __syncwarp();
             if (ok) {
                 // The (block, head) piece: B rows of D bytes, at the page's place in each head's tile.
-                const int piece = phys * p.num_kv_heads + w.h * HP;
                 const uint32_t at = sbase + static_cast<uint32_t>(r0) * D;
                 if (do_k) {
 #pragma unroll
