@@ -47,8 +47,9 @@ namespace {
 
 using namespace sm100;
 
+constexpr int kTables = 5;                                   // ring of their entries, above kAhead
 constexpr int kAhead = 4;                                    // tiles whose table entries are on their way
-constexpr int kQRing = 8;                                    // query scales kept, by segment
+constexpr int kQRing = 6;                                    // query scales kept, by segment
 constexpr uint64_t kWaitLimitNs = 1000000000ull;             // 1 s: far beyond any legal wait
 constexpr float kLevel2 = 1.f / 32, kLevel3 = 1.f / 65536;   // what the terms of u stand for
 constexpr float kHeadroom = 8.f;                             // u <= 2^8: e4m3 holds 256
@@ -78,6 +79,10 @@ SM100_DEV void cp_async4(uint32_t dst, const void *src) {
 SM100_DEV void cp_async_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
+SM100_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Until at most N of this thread's groups are on their way.
+template <int N>
+SM100_DEV void cp_async_wait_group() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 SM100_DEV void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // mbar_wait with its loop out of line: the kernel's warps run different code
@@ -89,7 +94,7 @@ SM100_DEV bool wait_for(uint32_t bar, uint32_t parity, volatile int *abort, uint
     return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort, limit_ns);
 }
 
-template <int kThreads, int kStages, int kLenCache>
+template <int kThreads, int kStages, int kLenCache, int kHeadsPerTile, int kProducers>
 struct MiscT {
     uint64_t full[kStages];       // K rows of a stage landed
     uint64_t vfull[kStages];      // V rows of a stage landed
@@ -114,8 +119,9 @@ struct MiscT {
     uint32_t mask[kStages][4];
     int4 meta[kStages];            // (sequence, KV head group, tile, tiles in segment) of a stage's tile
     int4 qmeta[kStages];           // (first query row, query tokens, first query position, 0) of it
-    float scales[kStages][16][2][2];   // [page][K, V][head of the pair]
+    float scales[kStages][16][2][kHeadsPerTile];   // [page][K, V][head]
     float qscale[kQRing][kNPad];   // by segment: what the stored query values of a column stand for
+    int table[kProducers][kTables][16];  // table entries of the tiles ahead, a ring a producer
     float red[4][kNPad];
     float lsum[2][4][kNPad];       // a segment's denominators by warp (segment parity)
     float mref[2][kNPad];          // its references
@@ -253,7 +259,7 @@ struct Shape {
     static constexpr uint32_t SCols = HP * NS;
     static constexpr uint32_t tS = 0, tO = 2 * SCols;
     static constexpr uint32_t TmemCols = tO + 2 * NP <= 128 ? 128 : 256;
-    using Misc = MiscT<Threads, Stages, LenCache>;
+    using Misc = MiscT<Threads, Stages, LenCache, HP, Groups>;
     static constexpr size_t SmemBytes = 1024 + Stages * StageBytes + QBufs * QBufBytes + 2 * PBytes + sizeof(Misc);
     static_assert(QBufs >= 2 && QBufs + 2 < kQRing, "query scales outlive their buffers");
     static_assert(tO + 2 * NP <= 256, "TMEM");
@@ -427,36 +433,30 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         int qr_of = -1;
         const int MB = p.max_blocks_per_seq;
         int issued = 0;
-        auto fetch = [&](const Walk &ww) -> int {
-            const int fp = ww.t * (kTile >> lgB);
-            return (lane < (kTile >> lgB) && fp + lane < MB)
-                       ? p.block_tables[static_cast<size_t>(ww.s) * MB + fp + lane] : -1;
-        };
-        // Table entries are read kAhead tiles before their tile: a tile's bytes
-        // take less time than one read does, so one tile ahead would bound the
-        // copies by that read's latency.
-        int ahead_phys[kAhead];
+        // Table entries (a lane per page) are read kAhead tiles before their tile:
+        // a tile's bytes take less time than one read does, so one tile ahead would
+        // bound the copies by that read's latency.  They go through shared memory
+        // (registers that move up would wait for the reads on their way), each
+        // lane reading what it copied itself.
+        int (*ring)[16] = misc->table[do_k ? 0 : kGroups - 1];
         Walk wf = w;
-        int fetched = 0;
-        auto fetch_next = [&]() -> int {
-            if (fetched >= n_tiles) return -1;
-            const int v = fetch(wf);
-            wf.next(lens);
-            ++fetched;
-            return v;
+        auto fetch_tile = [&](int i) {
+            if (i < n_tiles) {
+                const int fp = wf.t * (kTile >> lgB);
+                if (lane < (kTile >> lgB) && fp + lane < MB)
+                    cp_async4(smem_u32(&ring[i % kTables][lane]), p.block_tables + static_cast<size_t>(wf.s) * MB + fp + lane);
+                wf.next(lens);
+            }
+            cp_async_commit();
         };
-        int phys = -1;
-#pragma unroll
-        for (int x = 0; x < kAhead; ++x) ahead_phys[x] = -1;
-        // Rounds before 0 only start the reads.
 #pragma unroll 1
-        for (int i = -kAhead; i < n_tiles; ++i) {
-            phys = ahead_phys[0];
-#pragma unroll
-            for (int x = 0; x + 1 < kAhead; ++x) ahead_phys[x] = ahead_phys[x + 1];
-            ahead_phys[kAhead - 1] = fetch_next();
-            if (i < 0) continue;
+        for (int i = 0; i < kAhead; ++i) fetch_tile(i);
+#pragma unroll 1
+        for (int i = 0; i < n_tiles; ++i) {
             const int st = i % kStages;
+            fetch_tile(i + kAhead);
+            cp_async_wait_group<kAhead>();
+            const int phys = lane < 16 ? ring[i % kTables][lane] : -1;
             // What the tile needs is worked out before the wait for its stage.
             const int vlen = min(kTile, w.L - w.t * kTile);
             const int pages = (vlen + B - 1) >> lgB;
