@@ -116,7 +116,7 @@ struct MiscT {
     uint32_t tmem_base;
     int abort;
     int never;
-    uint32_t mask[kStages][4];
+    int2 held[kStages];            // (tokens, a bit for each page that was read) of a stage's tile
     int4 meta[kStages];            // (sequence, KV head group, tile, tiles in segment) of a stage's tile
     int4 qmeta[kStages];           // (first query row, query tokens, first query position, 0) of it
     float scales[kStages][16][2][kHeadsPerTile];   // [page][K, V][head]
@@ -250,16 +250,18 @@ struct Shape {
     static constexpr int LenCache = CtasPerSm == 2 ? 256 : 2048;
     static constexpr int QBufs = 2;
     // The one CTA of an SM splits its work over more warps instead: two groups
-    // of softmax warps, eight columns each, and a producer each for K and V.
+    // of softmax warps, eight columns each, and four producers (the even and
+    // the odd pages of K and of V: issuing a box takes a warp 70 to 100 cycles).
     static constexpr int Groups = CtasPerSm == 2 ? 1 : 2;
     static constexpr int GPairs = Groups == 2 ? 4 : (HP == 2 ? NC + NC % 2 : (NC + 1) / 2);   // pairs of columns of a group
     static constexpr int QueryWarp = 2 + 4 * Groups;        // the first of two
-    static constexpr int Threads = 32 * (QueryWarp + 2 + (Groups - 1));
+    static constexpr int Producers = CtasPerSm == 2 ? 1 : 4;   // warp 0 and those behind the query warps
+    static constexpr int Threads = 32 * (QueryWarp + 1 + Producers);
     static constexpr uint32_t PBytes = kTile * NP;
     static constexpr uint32_t SCols = HP * NS;
     static constexpr uint32_t tS = 0, tO = 2 * SCols;
     static constexpr uint32_t TmemCols = tO + 2 * NP <= 128 ? 128 : 256;
-    using Misc = MiscT<Threads, Stages, LenCache, HP, Groups>;
+    using Misc = MiscT<Threads, Stages, LenCache, HP, Producers>;
     static constexpr size_t SmemBytes = 1024 + Stages * StageBytes + QBufs * QBufBytes + 2 * PBytes + sizeof(Misc);
     static_assert(QBufs >= 2 && QBufs + 2 < kQRing, "query scales outlive their buffers");
     static_assert(tO + 2 * NP <= 256, "TMEM");
@@ -275,6 +277,7 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     using C_ = Shape<D, NC, HP>;
     using Misc = typename C_::Misc;
     constexpr int kThreads = C_::Threads, kStages = C_::Stages, kLenCache = C_::LenCache, kGroups = C_::Groups;
+    constexpr int kProducers = C_::Producers, kPerOperand = kProducers == 4 ? 2 : 1;
     constexpr int CW = C_::CW, HL = C_::HL, NS = C_::NS, PW = C_::PW, PC = C_::PC, NP = C_::NP;
     constexpr uint32_t kLayout = D == 128 ? kLayoutSw128 : kLayoutSw64;
     constexpr uint32_t kAtom = 8 * D;                 // eight rows: the swizzle's atom
@@ -304,9 +307,9 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(smem_u32(&misc->full[i]), 1);
-            mbar_init(smem_u32(&misc->vfull[i]), 1);
-            mbar_init(smem_u32(&misc->sfull[i]), 32 * kGroups);   // the lanes of every producer
+            mbar_init(smem_u32(&misc->full[i]), kPerOperand);
+            mbar_init(smem_u32(&misc->vfull[i]), kPerOperand);
+            mbar_init(smem_u32(&misc->sfull[i]), 32 * kProducers);   // the lanes of every producer
             mbar_init(smem_u32(&misc->empty[i]), 1);
         }
         for (int i = 0; i < C_::QBufs; ++i) {
@@ -424,10 +427,12 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         }
     };
 
-    if (warp == 0 || warp == C_::QueryWarp + 2) {
+    if (warp == 0 || warp >= C_::QueryWarp + 2) {
         // ================= producer =================
-        // K and V, or (two groups) warp 0 K and the last warp V.
-        const bool do_k = warp == 0, do_v = kGroups == 1 || warp != 0;
+        // One of K and V, or four: K and V of the even pages, K and V of the odd ones.
+        const int pi = warp == 0 ? 0 : warp - (C_::QueryWarp + 1);
+        const bool do_k = (pi & 1) == 0, do_v = kProducers == 1 || (pi & 1);
+        const bool my_page = kProducers == 1 || (lane & 1) == (pi >> 1);
         Walk w = w0;
         int2 qr = make_int2(0, 0);
         int qr_of = -1;
@@ -438,7 +443,7 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         // bound the copies by that read's latency.  They go through shared memory
         // (registers that move up would wait for the reads on their way), each
         // lane reading what it copied itself.
-        int (*ring)[16] = misc->table[do_k ? 0 : kGroups - 1];
+        int (*ring)[16] = misc->table[pi];
         Walk wf = w;
         auto fetch_tile = [&](int i) {
             if (i < n_tiles) {
@@ -463,20 +468,11 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             bool ok = false;
             if (lane < pages) {
                 ok = phys >= 0 && phys < p.num_blocks;
-                if (!ok) set_error(p.err, PK_DEVERR_BLOCK_ID);
+                if (!ok && pi == 0) set_error(p.err, PK_DEVERR_BLOCK_ID);
             }
-            uint32_t bits = 0;
-            const int r0 = lane << lgB;
-            if (ok) {
-                const int nrows = min(B, vlen - r0);
-                bits = (nrows >= 32 ? 0xffffffffu : ((1u << nrows) - 1u)) << (r0 & 31);
-            }
-            const int word = r0 >> 5;
-            const uint32_t m0 = __reduce_or_sync(0xffffffffu, word == 0 ? bits : 0u);
-            const uint32_t m1 = __reduce_or_sync(0xffffffffu, word == 1 ? bits : 0u);
-            const uint32_t m2 = __reduce_or_sync(0xffffffffu, word == 2 ? bits : 0u);
-            const uint32_t m3 = __reduce_or_sync(0xffffffffu, word == 3 ? bits : 0u);
-            const uint32_t nok = __popc(__ballot_sync(0xffffffffu, ok));
+            const uint32_t oks = __ballot_sync(0xffffffffu, ok);
+            ok = ok && my_page;
+            const uint32_t bytes = static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, ok))) * (HP * D) << lgB;
             const uint32_t full = smem_u32(&misc->full[st]);
             const uint32_t vfull = smem_u32(&misc->vfull[st]);
             const uint32_t sbase = stage_addr + st * C_::StageBytes;
@@ -491,20 +487,19 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 set_error(p.err, PK_DEVERR_TIMEOUT);
                 break;
             }
-            if (lane == 0 && do_v) mbar_arrive_expect_tx(vfull, nok * (HP * D) << lgB);
+            if (lane == 0 && do_v) mbar_arrive_expect_tx(vfull, bytes);
             if (lane == 0 && do_k) {
-                misc->mask[st][0] = m0;
-                misc->mask[st][1] = m1;
-                misc->mask[st][2] = m2;
-                misc->mask[st][3] = m3;
-                misc->meta[st] = make_int4(w.s, w.h, w.t, w.nt);
-                if constexpr (MQ) misc->qmeta[st] = make_int4(qr.x, qr.y, w.L - qr.y, 0);
-                mbar_arrive_expect_tx(full, nok * (HP * D) << lgB);
+                if (pi == 0) {
+                    misc->meta[st] = make_int4(w.s, w.h, w.t, w.nt);
+                    misc->held[st] = make_int2(vlen, static_cast<int>(oks));
+                    if constexpr (MQ) misc->qmeta[st] = make_int4(qr.x, qr.y, w.L - qr.y, 0);
+                }
+                mbar_arrive_expect_tx(full, bytes);
             }
             __syncwarp();
             if (ok) {
                 // The (block, head) piece: B rows of D bytes, at the page's place in each head's tile.
-                const uint32_t at = sbase + static_cast<uint32_t>(r0) * D;
+                const uint32_t at = sbase + (static_cast<uint32_t>(lane) << lgB) * D;
                 if (do_k) {
 #pragma unroll
                     for (int hd = 0; hd < HP; ++hd)
@@ -908,7 +903,8 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                     }
                 }
                 // The token's scales; one that is out of range hides the token's head.
-                const bool in_page = (misc->mask[st][row >> 5] >> (row & 31)) & 1u;
+                const int2 held = misc->held[st];
+                const bool in_page = row < held.x && ((held.y >> (row >> lgB)) & 1);
                 bool valid[kHeads];
                 float ks[kHeads], lv[kHeads], ivs[kHeads];
 #pragma unroll
