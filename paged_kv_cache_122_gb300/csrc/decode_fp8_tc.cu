@@ -49,6 +49,7 @@ using namespace sm100;
 
 constexpr int kTables = 5;                                   // ring of their entries, above kAhead
 constexpr int kAhead = 4;                                    // tiles whose table entries are on their way
+constexpr int kScores = 3;                                   // score buffers: two tiles ahead of the weights
 constexpr int kQRing = 6;                                    // query scales kept, by segment
 constexpr uint64_t kWaitLimitNs = 1000000000ull;             // 1 s: far beyond any legal wait
 constexpr float kLevel2 = 1.f / 32, kLevel3 = 1.f / 65536;   // what the terms of u stand for
@@ -102,7 +103,7 @@ struct MiscT {
     uint64_t empty[kStages];
     uint64_t qfull[kQRing];       // a segment's queries written (by buffer)
     uint64_t qempty[kQRing];
-    uint64_t s_full[2];
+    uint64_t s_full[kScores];     // scores of a tile complete
     uint64_t p_full[2];
     uint64_t o_full[2];       // P.V of a tile complete (per tile parity)
     uint64_t o_free[2];       // a segment's O buffer has been read out
@@ -259,11 +260,12 @@ struct Shape {
     static constexpr int Threads = 32 * (QueryWarp + 1 + Producers);
     static constexpr uint32_t PBytes = kTile * NP;
     static constexpr uint32_t SCols = HP * NS;
-    static constexpr uint32_t tS = 0, tO = 2 * SCols;
+    static constexpr uint32_t tS = 0, tO = kScores * SCols;
     static constexpr uint32_t TmemCols = tO + 2 * NP <= 128 ? 128 : 256;
     using Misc = MiscT<Threads, Stages, LenCache, HP, Producers>;
     static constexpr size_t SmemBytes = 1024 + Stages * StageBytes + QBufs * QBufBytes + 2 * PBytes + sizeof(Misc);
-    static_assert(QBufs >= 2 && QBufs + 2 < kQRing, "query scales outlive their buffers");
+    // The queries run at most QBufs segments ahead of the scores, and those kScores - 1 tiles of the weights.
+    static_assert(QBufs >= 2 && QBufs + kScores - 1 < kQRing, "query scales outlive their buffers");
     static_assert(tO + 2 * NP <= 256, "TMEM");
     static_assert(SmemBytes <= 227 * 1024, "shared memory");
     static_assert(CtasPerSm * (SmemBytes + 1024) <= 228 * 1024, "CTAs per SM");
@@ -316,8 +318,8 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             mbar_init(smem_u32(&misc->qfull[i]), 1);
             mbar_init(smem_u32(&misc->qempty[i]), 1);
         }
+        for (int i = 0; i < kScores; ++i) mbar_init(smem_u32(&misc->s_full[i]), 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&misc->s_full[i]), 1);
             mbar_init(smem_u32(&misc->p_full[i]), 4 * kGroups);
             mbar_init(smem_u32(&misc->o_full[i]), 1);
             mbar_init(smem_u32(&misc->o_free[i]), 4 * kGroups);
@@ -558,10 +560,10 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                     for (int kk = 0; kk < D / 32; ++kk) {
                         const uint64_t a = smem_desc(kbase + hd * C_::HeadBytes + kk * 32, 16, kAtom, kLayout);
                         const uint64_t b = smem_desc(qbase + hd * C_::QHeadBytes + kk * 32, 16, kAtom, kLayout);
-                        mma_e4m3(tmem + C_::tS + (i & 1) * C_::SCols + hd * NS, a, b, kIdescQK, kk > 0 ? 1u : 0u);
+                        mma_e4m3(tmem + C_::tS + (i % kScores) * C_::SCols + hd * NS, a, b, kIdescQK, kk > 0 ? 1u : 0u);
                     }
                 }
-                mma_commit(smem_u32(&misc->s_full[i & 1]));
+                mma_commit(smem_u32(&misc->s_full[i % kScores]));
                 if (last) mma_commit(smem_u32(&misc->qempty[sg % C_::QBufs]));
             };
             // Event loop, as in decode_tc_kernel; the scores of a segment's
@@ -583,7 +585,7 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                         prog = true;
                     }
                 }
-                if (nq < n_tiles && nq <= np + 1 &&
+                if (nq < n_tiles && nq < np + kScores &&
                     mbar_test_wait(smem_u32(&misc->full[nq % kStages]), (nq / kStages) & 1)) {
                     const int4 mt = misc->meta[nq % kStages];
                     const bool first = nq == 0 || mt.z == 0;
@@ -851,7 +853,7 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             if (i < n_tiles) {
                 const int st = i % kStages;
                 const int sb = i & 1;
-                if (!__all_sync(0xffffffffu, wait_for(smem_u32(&misc->s_full[sb]), (i >> 1) & 1, &misc->never, lim) &&
+                if (!__all_sync(0xffffffffu, wait_for(smem_u32(&misc->s_full[i % kScores]), (i / kScores) & 1, &misc->never, lim) &&
                                                  wait_for(smem_u32(&misc->sfull[st]), (i / kStages) & 1, &misc->never, lim))) {
                     misc->abort = 1;
                     set_error(p.err, PK_DEVERR_TIMEOUT);
@@ -876,7 +878,7 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 tc_fence_after();
                 // Scores: h columns plus 1/32 of the l columns.
                 uint64_t t2[kPairs];
-                const uint32_t saddr = lane_addr + C_::tS + sb * C_::SCols;
+                const uint32_t saddr = lane_addr + C_::tS + (i % kScores) * C_::SCols;
                 {
                     // h and l columns of this group.
                     constexpr int kWide = kHeads * 16;
