@@ -73,6 +73,13 @@ SM100_DEV void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint3
         : "memory");
 }
 
+// True in one lane of the (converged) warp.
+SM100_DEV bool elect_one() {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
+}
+
 SM100_DEV void cp_async4(uint32_t dst, const void *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -532,87 +539,110 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         }
     } else if (warp == 1) {
         // ================= MMA issuer =================
-        if (lane == 0) {
-            int pv_seg = -1, qk_seg = -1;
-            auto pv = [&](int j, bool first, int sg) {
-                const int pb = j & 1;
-                tc_fence_after();
-                const uint32_t vbase = stage_addr + (j % kStages) * C_::StageBytes + C_::VOff;
-                const uint32_t pbase = p_addr + pb * C_::PBytes;
+        // The whole warp runs the loop and one lane issues: what an MMA takes then
+        // stays in uniform registers (one lane alone took 100 cycles an MMA, and
+        // this warp bounded the tile).
+        const bool leader = elect_one();
+        const uint64_t k_desc = smem_desc(stage_addr, 16, kAtom, kLayout);
+        // Head dim 64: the second 64 rows of O^T come from the pair's second head
+        // (HP == 2) or are not used.
+        const uint64_t v_desc = smem_desc(stage_addr + C_::VOff, HP == 2 ? C_::HeadBytes : kAtom, kAtom, kLayout);
+        const uint64_t q_desc = smem_desc(q_addr, 16, kAtom, kLayout);
+        const uint64_t p_desc = smem_desc(p_addr, 8 * NP, 128, kLayoutNone);
+        int pv_seg = -1, qk_seg = -1;
+        auto pv = [&](int j, int st, bool first, int sg) {
+            const int pb = j & 1;
+            tc_fence_after();
+            if (leader) {
 #pragma unroll
                 for (int kk = 0; kk < kTile / 32; ++kk) {
-                    // Tokens 32 kk .. 32 kk + 31: four 8-row atoms of V.  Head dim 64: the second
-                    // 64 rows of O^T come from the pair's second head (HP == 2) or are not used.
-                    const uint64_t a = smem_desc(vbase + kk * 4 * kAtom, HP == 2 ? C_::HeadBytes : kAtom, kAtom, kLayout);
-                    const uint64_t b = smem_desc(pbase + kk * 32 * NP, 8 * NP, 128, kLayoutNone);
-                    mma_e4m3(tmem + C_::tO + (sg & 1) * NP, a, b, kIdescPV, (first && kk == 0) ? 0u : 1u);
+                    // Tokens 32 kk .. 32 kk + 31: four 8-row atoms of V.
+                    mma_e4m3(tmem + C_::tO + (sg & 1) * NP, v_desc + ((st * C_::StageBytes + kk * 4 * kAtom) >> 4),
+                             p_desc + ((pb * C_::PBytes + kk * 32 * NP) >> 4), kIdescPV, (first && kk == 0) ? 0u : 1u);
                 }
                 mma_commit(smem_u32(&misc->o_full[pb]));
-                mma_commit(smem_u32(&misc->empty[j % kStages]));
-            };
-            auto qk = [&](int i, int sg, bool last) {
-                tc_fence_after();
-                const uint32_t kbase = stage_addr + (i % kStages) * C_::StageBytes;
-                const uint32_t qbase = q_addr + (sg % C_::QBufs) * C_::QBufBytes;
+                mma_commit(smem_u32(&misc->empty[st]));
+            }
+            __syncwarp();
+        };
+        auto qk = [&](int sb, int st, int sg, bool last) {
+            const uint32_t qb = sg % C_::QBufs;
+            tc_fence_after();
+            if (leader) {
 #pragma unroll
                 for (int hd = 0; hd < HP; ++hd) {
 #pragma unroll
                     for (int kk = 0; kk < D / 32; ++kk) {
-                        const uint64_t a = smem_desc(kbase + hd * C_::HeadBytes + kk * 32, 16, kAtom, kLayout);
-                        const uint64_t b = smem_desc(qbase + hd * C_::QHeadBytes + kk * 32, 16, kAtom, kLayout);
-                        mma_e4m3(tmem + C_::tS + (i % kScores) * C_::SCols + hd * NS, a, b, kIdescQK, kk > 0 ? 1u : 0u);
+                        mma_e4m3(tmem + C_::tS + sb * C_::SCols + hd * NS,
+                                 k_desc + ((st * C_::StageBytes + hd * C_::HeadBytes + kk * 32) >> 4),
+                                 q_desc + ((qb * C_::QBufBytes + hd * C_::QHeadBytes + kk * 32) >> 4), kIdescQK, kk > 0 ? 1u : 0u);
                     }
                 }
-                mma_commit(smem_u32(&misc->s_full[i % kScores]));
-                if (last) mma_commit(smem_u32(&misc->qempty[sg % C_::QBufs]));
-            };
-            // Event loop, as in decode_tc_kernel; the scores of a segment's
-            // first tile also wait for its queries.
-            int nq = 0, np = 0;
-            uint64_t t_idle = 0;
-            uint32_t spins = 0;
-            while (np < n_tiles) {
-                bool prog = false;
-                if (np < nq && mbar_test_wait(smem_u32(&misc->p_full[np & 1]), (np >> 1) & 1) &&
-                    mbar_test_wait(smem_u32(&misc->vfull[np % kStages]), (np / kStages) & 1)) {
-                    const bool first = np == 0 || misc->meta[np % kStages].z == 0;
-                    const int sg = pv_seg + (first ? 1 : 0);
-                    // A new segment's O buffer must have been read out (segment sg - 2).
-                    if (!first || mbar_test_wait(smem_u32(&misc->o_free[sg & 1]), ((sg >> 1) & 1) ^ 1)) {
-                        pv(np, first, sg);
-                        pv_seg = sg;
-                        ++np;
-                        prog = true;
+                mma_commit(smem_u32(&misc->s_full[sb]));
+                if (last) mma_commit(smem_u32(&misc->qempty[qb]));
+            }
+            __syncwarp();
+        };
+        auto done = [&](uint64_t &bar, uint32_t parity) -> bool {
+            return __all_sync(0xffffffffu, mbar_test_wait(smem_u32(&bar), parity));
+        };
+        // Event loop, as in decode_tc_kernel; the scores of a segment's first tile
+        // also wait for its queries.
+        int nq = 0, np = 0;
+        int st_q = 0, st_p = 0, sb = 0;                  // stages of tiles nq and np, score buffer of nq
+        uint32_t ph_q = 0, ph_p = 0;                     // and the parities of their rounds
+        uint64_t t_idle = 0;
+        uint32_t spins = 0;
+#pragma unroll 1
+        while (np < n_tiles) {
+            bool prog = false;
+            if (np < nq && done(misc->p_full[np & 1], (np >> 1) & 1) && done(misc->vfull[st_p], ph_p)) {
+                const bool first = np == 0 || misc->meta[st_p].z == 0;
+                const int sg = pv_seg + (first ? 1 : 0);
+                // A new segment's O buffer must have been read out (segment sg - 2).
+                if (!first || done(misc->o_free[sg & 1], ((sg >> 1) & 1) ^ 1)) {
+                    pv(np, st_p, first, sg);
+                    pv_seg = sg;
+                    ++np;
+                    if (++st_p == kStages) {
+                        st_p = 0;
+                        ph_p ^= 1;
                     }
-                }
-                if (nq < n_tiles && nq < np + kScores &&
-                    mbar_test_wait(smem_u32(&misc->full[nq % kStages]), (nq / kStages) & 1)) {
-                    const int4 mt = misc->meta[nq % kStages];
-                    const bool first = nq == 0 || mt.z == 0;
-                    const int sg = qk_seg + (first ? 1 : 0);
-                    if (!first || mbar_test_wait(smem_u32(&misc->qfull[sg % C_::QBufs]), (sg / C_::QBufs) & 1)) {
-                        qk(nq, sg, nq == n_tiles - 1 || mt.z == mt.w - 1);
-                        qk_seg = sg;
-                        ++nq;
-                        prog = true;
-                    }
-                }
-                if (prog) {
-                    spins = 0;
-                } else if ((++spins & 255u) == 0) {
-                    const uint64_t now = globaltimer_ns();
-                    if (spins == 256) t_idle = now;
-                    else if (misc->abort || now - t_idle > lim) {
-                        misc->abort = 1;
-                        set_error(p.err, PK_DEVERR_TIMEOUT);
-                        break;
-                    }
+                    prog = true;
                 }
             }
-            // Let every issued MMA finish before the CTA can release TMEM.
-            mma_commit(smem_u32(&misc->drain));
-            wait_for(smem_u32(&misc->drain), 0, &misc->never, lim);
+            if (nq < n_tiles && nq < np + kScores && done(misc->full[st_q], ph_q)) {
+                const int4 mt = misc->meta[st_q];
+                const bool first = nq == 0 || mt.z == 0;
+                const int sg = qk_seg + (first ? 1 : 0);
+                if (!first || done(misc->qfull[sg % C_::QBufs], (sg / C_::QBufs) & 1)) {
+                    qk(sb, st_q, sg, nq == n_tiles - 1 || mt.z == mt.w - 1);
+                    qk_seg = sg;
+                    ++nq;
+                    if (++st_q == kStages) {
+                        st_q = 0;
+                        ph_q ^= 1;
+                    }
+                    if (++sb == kScores) sb = 0;
+                    prog = true;
+                }
+            }
+            if (prog) {
+                spins = 0;
+            } else if ((++spins & 255u) == 0) {
+                const uint64_t now = globaltimer_ns();
+                if (spins == 256) t_idle = now;
+                else if (__any_sync(0xffffffffu, misc->abort || now - t_idle > lim)) {
+                    misc->abort = 1;
+                    set_error(p.err, PK_DEVERR_TIMEOUT);
+                    break;
+                }
+            }
         }
+        // Let every issued MMA finish before the CTA can release TMEM.
+        if (leader) mma_commit(smem_u32(&misc->drain));
+        __syncwarp();
+        wait_for(smem_u32(&misc->drain), 0, &misc->never, lim);
         __syncwarp();
     } else if (warp >= C_::QueryWarp) {
         // ================= queries =================
