@@ -231,7 +231,7 @@ SM100_DEV float fast_rcp(float v) {
 constexpr int64_t kTileCost = 400;
 constexpr int kTokCost = 1;
 template <int NUSED, int HP>
-constexpr int64_t seg_cost() { return (NUSED > 8 ? 200 : 56) / HP; }
+constexpr int64_t seg_cost() { return NUSED > 8 ? 780 : 20 * NUSED; }
 
 // What follows from (head dim, query columns per KV head, KV heads per tile).
 template <int D, int NC, int HP>
