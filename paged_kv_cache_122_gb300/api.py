@@ -22,12 +22,32 @@ def _ptr(t: Optional[torch.Tensor]):
     return ctypes.c_void_p(t.data_ptr()) if t is not None and t.numel() > 0 else ctypes.c_void_p(0)
 
 
+def _at(t: Optional[torch.Tensor]) -> int:
+    return t.data_ptr() if t is not None else 0
+
+
+def _raw_stream(device: torch.device, stream=None) -> int:
+    """The cudaStream_t of ``stream``, or of the device's current stream.  (Asked
+    for as a number: a Stream object costs 2 us, half a launch.)"""
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device.index)
+
+
 def _stream(device: torch.device, stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    return ctypes.c_void_p(s.cuda_stream)
+    return ctypes.c_void_p(_raw_stream(device, stream))
+
+
+def _on(device: torch.device, fn, *args) -> int:
+    """``fn(*args)`` with ``device`` current."""
+    if torch._C._cuda_getDevice() == device.index:
+        return fn(*args)
+    with torch.cuda.device(device):
+        return fn(*args)
 
 
 def _need(t: torch.Tensor, name: str, dtype, ndim: int, device=None):
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == ndim and t.is_cuda
+            and (device is None or t.device == device) and t.is_contiguous()):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -57,8 +77,7 @@ def workspace_for(device: torch.device, nbytes: int, stream=None) -> Optional[to
     """A cached scratch buffer of at least ``nbytes`` for ``device`` and stream."""
     if nbytes == 0:
         return None
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    key = (device, s.cuda_stream)
+    key = (device, _raw_stream(device, stream))
     ws = _WORKSPACES.get(key)
     if ws is None or ws.numel() < nbytes:
         ws = new_workspace(nbytes, device)
@@ -230,15 +249,15 @@ reshape_and_cache = pk_reshape_and_cache
 def _need_rows(t: torch.Tensor, name: str, device):
     """[tokens, heads, D] bf16 rows whose heads are dense; the tokens may be any
     stride apart (a slice of a fused projection).  Returns that stride."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must have 3 dims, got shape {tuple(t.shape)}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (this library has no CPU path)")
-    if t.device != device:
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.dim() == 3 and t.device == device):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dtype != torch.bfloat16:
+            raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+        if t.dim() != 3:
+            raise ValueError(f"{name} must have 3 dims, got shape {tuple(t.shape)}")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor (this library has no CPU path)")
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     T, heads, D = t.shape
     s0, s1, s2 = t.stride()
@@ -304,11 +323,9 @@ def pk_rope_and_cache(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tenso
         _need(positions, "positions", torch.int64, 1, dev)
         if positions.shape[0] != T:
             raise ValueError("positions must have one entry per token")
-    with torch.cuda.device(dev):
-        st = load().pk_rope_and_cache(
-            _ptr(q_out), _ptr(q), _ptr(k), _ptr(v), *strides, _ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping),
-            _ptr(positions), _ptr(inv_freq), rot, int(interleaved), float(factor), T, H, Hkv, D, P, B,
-            _stream(dev, stream))
+    st = _on(dev, load().pk_rope_and_cache, _at(q_out), _at(q), k.data_ptr(), v.data_ptr(), *strides,
+             k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), _at(positions), _at(inv_freq), rot,
+             int(interleaved), factor, T, H, Hkv, D, P, B, _raw_stream(dev, stream))
     check("pk_rope_and_cache", st)
     if stream is not None and q_out is not None and not given:
         q_out.record_stream(stream)

@@ -8,13 +8,14 @@ unprefixed names are the same calls.
 """
 from __future__ import annotations
 
+import functools
 from typing import Optional, Tuple
 
 import torch
 
 from . import _native
 from ._native import check, load
-from .api import _need, _ptr, _rope_args, _stream, new_workspace, workspace_for
+from .api import _at, _need, _on, _raw_stream, _rope_args, new_workspace, workspace_for
 
 FP8 = torch.float8_e4m3fn
 
@@ -33,11 +34,12 @@ def _need_cache(k_cache, v_cache, k_scales, v_scales, dev):
     _need(v_cache, "v_cache", FP8, 4, dev)
     _need(k_scales, "k_scales", torch.float32, 2, dev)
     _need(v_scales, "v_scales", torch.float32, 2, dev)
-    P, Hkv, _, _ = k_cache.shape
-    if v_cache.shape != k_cache.shape:
+    shape = k_cache.shape
+    if v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must have the same shape")
-    if tuple(k_scales.shape) != (P, Hkv) or tuple(v_scales.shape) != (P, Hkv):
-        raise ValueError(f"scales must be [num_blocks, num_kv_heads] = {(P, Hkv)}")
+    if k_scales.shape != shape[:2] or v_scales.shape != shape[:2]:
+        raise ValueError(f"scales must be [num_blocks, num_kv_heads] = {tuple(shape[:2])}")
+    return shape
 
 
 def pk_rope_and_cache_fp8(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
@@ -53,13 +55,12 @@ def pk_rope_and_cache_fp8(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.T
     the append; the positions are those in the block table unless given.  The
     other arguments are those of ``rope_and_cache``.  See the C header."""
     dev = k_cache.device
-    _need_cache(k_cache, v_cache, k_scales, v_scales, dev)
+    P, Hc, B, Dc = _need_cache(k_cache, v_cache, k_scales, v_scales, dev)
     _need(block_tables, "block_tables", torch.int32, 2, dev)
     _need(seq_lens, "seq_lens", torch.int32, 1, dev)
     given = q_out is not None
     q_out, H, rot, strides = _rope_args(q, k, v, inv_freq, q_out, dev)
     T, Hkv, D = k.shape
-    P, Hc, B, Dc = k_cache.shape
     N, MB = block_tables.shape
     if (Hc, Dc) != (Hkv, D):
         raise ValueError("k / v / cache shapes disagree")
@@ -79,12 +80,10 @@ def pk_rope_and_cache_fp8(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.T
         _need(positions, "positions", torch.int64, 1, dev)
         if positions.shape[0] != T:
             raise ValueError("positions must have one entry per token")
-    with torch.cuda.device(dev):
-        st = load().pk_rope_and_cache_fp8(
-            _ptr(q_out), _ptr(q), _ptr(k), _ptr(v), *strides, _ptr(k_cache), _ptr(v_cache), _ptr(k_scales),
-            _ptr(v_scales), _ptr(block_tables), MB, _ptr(seq_lens), _ptr(cu_q_lens), int(max_q_len), N,
-            _ptr(positions), _ptr(inv_freq), rot, int(interleaved), float(factor), T, H, Hkv, D, P, B,
-            _stream(dev, stream))
+    st = _on(dev, load().pk_rope_and_cache_fp8, _at(q_out), _at(q), k.data_ptr(), v.data_ptr(), *strides,
+             k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+             block_tables.data_ptr(), MB, seq_lens.data_ptr(), _at(cu_q_lens), max_q_len, N, _at(positions),
+             _at(inv_freq), rot, int(interleaved), factor, T, H, Hkv, D, P, B, _raw_stream(dev, stream))
     check("pk_rope_and_cache_fp8", st)
     if stream is not None and q_out is not None and not given:
         q_out.record_stream(stream)
@@ -94,6 +93,7 @@ def pk_rope_and_cache_fp8(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.T
 rope_and_cache_fp8 = pk_rope_and_cache_fp8
 
 
+@functools.lru_cache(maxsize=256)
 def pk_decode_fp8_workspace_bytes(num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int,
                                   max_seq_len: int) -> int:
     return int(load().pk_decode_fp8_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, max_seq_len))
@@ -104,7 +104,7 @@ def _workspace(dev, nbytes: int, stream) -> Optional[torch.Tensor]:
     the graph's own pool, so that two graphs never share one."""
     if nbytes == 0:
         return None
-    if torch.cuda.is_current_stream_capturing():
+    if torch._C._cuda_isCurrentStreamCapturing():
         return new_workspace(nbytes, dev)
     return workspace_for(dev, nbytes, stream)
 
@@ -113,11 +113,10 @@ def _attend(name, out, q, cu_q_lens, max_q_len, k_cache, v_cache, k_scales, v_sc
             out_dtype, max_seq_len, workspace, stream):
     dev = q.device
     _need(q, "q", torch.bfloat16, 3)
-    _need_cache(k_cache, v_cache, k_scales, v_scales, dev)
+    P, Hkv, B, Dk = _need_cache(k_cache, v_cache, k_scales, v_scales, dev)
     _need(block_tables, "block_tables", torch.int32, 2, dev)
     _need(seq_lens, "seq_lens", torch.int32, 1, dev)
-    T, H, D = q.shape
-    P, Hkv, B, Dk = k_cache.shape
+    T, H, D = shape = q.shape
     N, MB = block_tables.shape
     if Dk != D:
         raise ValueError("k_cache / v_cache / q shapes disagree")
@@ -132,32 +131,34 @@ def _attend(name, out, q, cu_q_lens, max_q_len, k_cache, v_cache, k_scales, v_sc
             raise ValueError("cu_q_lens must have one entry more than sequences")
     given = out is not None
     if not given:
-        out = torch.empty((T, H, D), dtype=out_dtype, device=dev)
-    if out.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError("out must be bf16 or fp32")
-    _need(out, "out", out.dtype, 3, dev)
-    if tuple(out.shape) != (T, H, D):
+        out = torch.empty(shape, dtype=out_dtype, device=dev)
+    elif out.shape != shape:
         raise ValueError("out must have q's shape")
+    if out.dtype is torch.bfloat16:
+        dtype = _native.PK_BF16
+    elif out.dtype is torch.float32:
+        dtype = _native.PK_FP32
+    else:
+        raise TypeError("out must be bf16 or fp32")
+    if given:
+        _need(out, "out", out.dtype, 3, dev)
     if max_seq_len is None:
         max_seq_len = MB * B
-    lib = load()
-    with torch.cuda.device(dev):
-        nbytes = lib.pk_decode_fp8_workspace_bytes(N, H, Hkv, D, int(max_seq_len))
-        if workspace is None:
-            workspace = _workspace(dev, nbytes, stream)
-        elif workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-        elif workspace.numel() * workspace.element_size() < nbytes:
-            raise ValueError("workspace too small")
-        dtype = _native.PK_FP32 if out.dtype == torch.float32 else _native.PK_BF16
-        tail = (_ptr(k_cache), _ptr(v_cache), _ptr(k_scales), _ptr(v_scales), _ptr(block_tables), MB, _ptr(seq_lens),
-                int(max_seq_len), N, H, Hkv, D, P, B, float(scale), _ptr(workspace),
-                0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(dev, stream))
-        if cu_q_lens is None:
-            st = lib.pk_paged_attention_decode_fp8(_ptr(out), dtype, _ptr(q), *tail)
-        else:
-            st = lib.pk_paged_attention_multi_query_fp8(_ptr(out), dtype, _ptr(q), T, _ptr(cu_q_lens), int(max_q_len),
-                                                        *tail)
+    nbytes = pk_decode_fp8_workspace_bytes(N, H, Hkv, D, max_seq_len)
+    if workspace is None:
+        workspace = _workspace(dev, nbytes, stream)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    elif workspace.numel() * workspace.element_size() < nbytes:
+        raise ValueError("workspace too small")
+    tail = (k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(),
+            MB, seq_lens.data_ptr(), max_seq_len, N, H, Hkv, D, P, B, scale, _at(workspace),
+            0 if workspace is None else workspace.nbytes, _raw_stream(dev, stream))
+    if cu_q_lens is None:
+        st = _on(dev, load().pk_paged_attention_decode_fp8, out.data_ptr(), dtype, q.data_ptr(), *tail)
+    else:
+        st = _on(dev, load().pk_paged_attention_multi_query_fp8, out.data_ptr(), dtype, q.data_ptr(), T,
+                 cu_q_lens.data_ptr(), max_q_len, *tail)
     check(name, st)
     if stream is not None and not given:
         out.record_stream(stream)
@@ -204,24 +205,23 @@ def pk_gather_kv_fp8(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scales: tor
     """Write the sequences' K and V rows as bf16 to rows cu_seq_lens[s] + j of
     out_k and out_v ([rows, Hkv, D]).  See the C header."""
     dev = k_cache.device
-    _need_cache(k_cache, v_cache, k_scales, v_scales, dev)
+    P, Hkv, B, D = _need_cache(k_cache, v_cache, k_scales, v_scales, dev)
     _need(block_tables, "block_tables", torch.int32, 2, dev)
     _need(seq_lens, "seq_lens", torch.int32, 1, dev)
     _need(cu_seq_lens, "cu_seq_lens", torch.int64, 1, dev)
     _need(out_k, "out_k", torch.bfloat16, 3, dev)
     _need(out_v, "out_v", torch.bfloat16, 3, dev)
-    P, Hkv, B, D = k_cache.shape
     N, MB = block_tables.shape
     if seq_lens.shape[0] != N or cu_seq_lens.shape[0] != N:
         raise ValueError("seq_lens / cu_seq_lens do not match the block tables' batch")
-    if out_k.shape != out_v.shape or tuple(out_k.shape[1:]) != (Hkv, D):
+    rows, heads, width = out_k.shape
+    if out_k.shape != out_v.shape or (heads, width) != (Hkv, D):
         raise ValueError("out_k and out_v must be [rows, num_kv_heads, head_dim]")
     if max_seq_len is None:
         max_seq_len = MB * B
-    with torch.cuda.device(dev):
-        st = load().pk_gather_kv_fp8(_ptr(out_k), _ptr(out_v), _ptr(k_cache), _ptr(v_cache), _ptr(k_scales),
-                                     _ptr(v_scales), _ptr(block_tables), MB, _ptr(seq_lens), _ptr(cu_seq_lens),
-                                     out_k.shape[0], int(max_seq_len), N, Hkv, D, P, B, _stream(dev, stream))
+    st = _on(dev, load().pk_gather_kv_fp8, out_k.data_ptr(), out_v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+             k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(), MB, seq_lens.data_ptr(),
+             cu_seq_lens.data_ptr(), rows, max_seq_len, N, Hkv, D, P, B, _raw_stream(dev, stream))
     check("pk_gather_kv_fp8", st)
 
 
@@ -233,15 +233,13 @@ def pk_copy_blocks_fp8(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scales: t
     """Copy whole blocks and their scales for every (src, dst) row of an int64
     [n, 2] tensor.  See the C header."""
     dev = k_cache.device
-    _need_cache(k_cache, v_cache, k_scales, v_scales, dev)
+    P, Hkv, B, D = _need_cache(k_cache, v_cache, k_scales, v_scales, dev)
     _need(src_dst_pairs, "src_dst_pairs", torch.int64, 2, dev)
-    if src_dst_pairs.shape[1] != 2:
+    n, two = src_dst_pairs.shape
+    if two != 2:
         raise ValueError("src_dst_pairs must be [n, 2]")
-    P, Hkv, B, D = k_cache.shape
-    with torch.cuda.device(dev):
-        st = load().pk_copy_blocks_fp8(_ptr(k_cache), _ptr(v_cache), _ptr(k_scales), _ptr(v_scales),
-                                       _ptr(src_dst_pairs), src_dst_pairs.shape[0], Hkv, D, P, B,
-                                       _stream(dev, stream))
+    st = _on(dev, load().pk_copy_blocks_fp8, k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(),
+             v_scales.data_ptr(), src_dst_pairs.data_ptr(), n, Hkv, D, P, B, _raw_stream(dev, stream))
     check("pk_copy_blocks_fp8", st)
 
 
@@ -273,9 +271,8 @@ def pk_swap_blocks_fp8(dst, src, pairs: torch.Tensor, stream=None) -> None:
     if src[0].shape[1:] != dst[0].shape[1:]:
         raise ValueError("pool shapes disagree")
     P_src, Hkv, B, D = src[0].shape
-    with torch.cuda.device(dev):
-        st = load().pk_swap_blocks_fp8(*(_ptr(t) for t in dst), *(_ptr(t) for t in src), _ptr(pairs), pairs.shape[0],
-                                       Hkv, D, B, P_src, dst[0].shape[0], _stream(dev, stream))
+    st = _on(dev, load().pk_swap_blocks_fp8, *(t.data_ptr() for t in dst), *(t.data_ptr() for t in src),
+             pairs.data_ptr(), pairs.shape[0], Hkv, D, B, P_src, dst[0].shape[0], _raw_stream(dev, stream))
     check("pk_swap_blocks_fp8", st)
 
 
