@@ -25,7 +25,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBatch = 4;          // q units (2 x 16 bytes) a thread has in flight
+constexpr int kCtasPerSm = 4;
+constexpr int kBatch = 3;          // q units (2 x 16 bytes) a thread has in flight
 constexpr int kQueryUnits = 2048;  // most q units of a CTA: 8 a thread
 
 struct AppendParams {
@@ -39,6 +40,7 @@ struct AppendParams {
     const float *inv_freq;
     int rot, num_heads, num_kv_heads, max_blocks_per_seq, num_seqs, total_q, max_q_len, num_blocks;
     int cells_per_seq;       // > 0: cell x belongs to sequence x / cells_per_seq; 0: found by search
+    int kv_ctas;             // CTAs (blockIdx.y) of a cell for K and V, kWarps heads each
     int q_heads_per_cta;
     float factor;
     unsigned int *err;
@@ -103,7 +105,7 @@ __device__ __forceinline__ uint2 quantise8(const float (&f)[8], float inv) {
 }
 
 template <int D, int B, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
 rope_and_cache_fp8_kernel(const AppendParams p) {
     constexpr int kUnits = D / 16;                 // units (two 8-element vectors) a row
     constexpr int kRows = 32 / kUnits;             // rows a warp handles at once
@@ -159,9 +161,9 @@ rope_and_cache_fp8_kernel(const AppendParams p) {
         __syncthreads();
     };
 
-    if (blockIdx.y > 0) {
+    if (blockIdx.y >= p.kv_ctas) {
         // ---- queries: heads h0 .. h0 + nh - 1 of the cell's tokens ---------
-        const int h0 = (blockIdx.y - 1) * p.q_heads_per_cta;
+        const int h0 = (blockIdx.y - p.kv_ctas) * p.q_heads_per_cta;
         const int nh = min(p.q_heads_per_cta, H - h0);
         const int units = nt * nh * kUnits;
         for (int base = 0; base < units; base += kThreads * kBatch) {
@@ -203,92 +205,87 @@ rope_and_cache_fp8_kernel(const AppendParams p) {
     // ---- K and V: one warp a (K or V, head) ---------------------------------
     const int phys = p.block_tables[static_cast<int64_t>(s) * p.max_blocks_per_seq + blk];
     if (phys < 0 || phys >= p.num_blocks) {
-        if (threadIdx.x == 0) pk::set_error(p.err, PK_DEVERR_BLOCK_ID);
+        if (threadIdx.x == 0 && blockIdx.y == 0) pk::set_error(p.err, PK_DEVERR_BLOCK_ID);
         return;
     }
     const int ju = lane % kUnits, lrow = lane / kUnits;
     const float f2 = p.factor * p.factor;
-    bool have_angles = false;
-    for (int task0 = 0; task0 < 2 * Hkv; task0 += kWarps) {
-        const int task = task0 + warp;
-        const bool active = task < 2 * Hkv;
-        const bool is_k = task < Hkv;
-        const int h = is_k ? task : task - Hkv;
-        const int rot = is_k ? p.rot : 0;
-        const int2 o = pk::unit_offsets(ju, rot, D);
-        const uint16_t *src = is_k ? p.k : p.v;
-        const int64_t stride = is_k ? p.k_stride : p.v_stride;
-        float *scale_at = (is_k ? p.k_scales : p.v_scales) + static_cast<int64_t>(phys) * Hkv + h;
-        uint8_t *rows = (is_k ? p.k_cache : p.v_cache) + (static_cast<int64_t>(phys) * Hkv + h) * (B * D);
-        uint4 a[kIters], b[kIters];
-        float had = 0.f, most = 0.f;
-        if (active) {
-            if (off0 > 0) had = *scale_at;
-#pragma unroll
-            for (int it = 0; it < kIters; ++it) {
-                const int t = it * kRows + lrow;
-                a[it] = b[it] = make_uint4(0, 0, 0, 0);
-                if (t < nt) {
-                    a[it] = pk::ld_stream(src + (row0 + t) * stride + h * D + o.x);
-                    b[it] = pk::ld_stream(src + (row0 + t) * stride + h * D + o.y);
-                }
-            }
-        }
-        if (!have_angles) {          // the same for every thread
-            angles();
-            have_angles = true;
-        }
-        if (!active) continue;
-#pragma unroll
-        for (int it = 0; it < kIters; ++it) {
-            if (it * kRows >= nt) break;
-            float fa[8], fb[8];
-            pk::unpack8(a[it], fa);
-            pk::unpack8(b[it], fb);
-            const float m = ju < rot / 16 ? fminf(largest_pair<kInterleaved>(fa, fb) * f2, 3.402823466e38f)
-                                          : largest_single(fa, fb);
-            most = fmaxf(most, m);
-        }
-#pragma unroll
-        for (int x = 16; x >= 1; x >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, x));
-        float scale = pk::needed_scale(most);
-        if (off0 > 0) {
-            if (!pk::scale_ok(had)) {
-                if (lane == 0) pk::set_error(p.err, PK_DEVERR_SCALE);
-            } else if (had >= scale) {
-                scale = had;
-            } else {
-                // The scale grows: the older rows in the new one's steps.
-                const float ratio = had / scale;       // exact: `scale` is a power of two
-                for (int r = lrow; r < off0; r += kRows) {
-                    uint4 *at = reinterpret_cast<uint4 *>(rows + r * D + ju * 16);
-                    uint4 w = *at;
-                    uint32_t *e = reinterpret_cast<uint32_t *>(&w);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float f[4];
-                        pk::e4m3x4_to_float(e[i], f);
-                        e[i] = pk::e4m3x4(f[0] * ratio, f[1] * ratio, f[2] * ratio, f[3] * ratio);
-                    }
-                    *at = w;
-                }
-            }
-        }
-        __syncwarp();                                  // every lane has its copy of the old scale
-        if (lane == 0) *scale_at = scale;
-        const float inv = 1.f / scale;
+    // Task: K of head `task`, or V of head task - Hkv.
+    const int task = blockIdx.y * kWarps + warp;
+    const bool active = task < 2 * Hkv;
+    const bool is_k = task < Hkv;
+    const int h = is_k ? task : task - Hkv;
+    const int rot = is_k ? p.rot : 0;
+    const int2 o = pk::unit_offsets(ju, rot, D);
+    const uint16_t *src = is_k ? p.k : p.v;
+    const int64_t stride = is_k ? p.k_stride : p.v_stride;
+    float *scale_at = (is_k ? p.k_scales : p.v_scales) + static_cast<int64_t>(phys) * Hkv + h;
+    uint8_t *rows = (is_k ? p.k_cache : p.v_cache) + (static_cast<int64_t>(phys) * Hkv + h) * (B * D);
+    uint4 a[kIters], b[kIters];
+    float had = 0.f, most = 0.f;
+    if (active) {
+        if (off0 > 0) had = *scale_at;
 #pragma unroll
         for (int it = 0; it < kIters; ++it) {
             const int t = it * kRows + lrow;
-            if (t >= nt) break;
-            float fa[8], fb[8];
-            pk::unpack8(a[it], fa);
-            pk::unpack8(b[it], fb);
-            if (ju < rot / 16) pk::rotate_unit<kInterleaved>(fa, fb, cs[t], ju, rot);
-            uint8_t *dst = rows + (off0 + t) * D;
-            *reinterpret_cast<uint2 *>(dst + o.x) = quantise8(fa, inv);
-            *reinterpret_cast<uint2 *>(dst + o.y) = quantise8(fb, inv);
+            a[it] = b[it] = make_uint4(0, 0, 0, 0);
+            if (t < nt) {
+                a[it] = pk::ld_stream(src + (row0 + t) * stride + h * D + o.x);
+                b[it] = pk::ld_stream(src + (row0 + t) * stride + h * D + o.y);
+            }
         }
+    }
+    if (static_cast<int>(blockIdx.y) * kWarps < Hkv) angles();      // some warp has keys
+    if (!active) return;
+#pragma unroll
+    for (int it = 0; it < kIters; ++it) {
+        if (it * kRows >= nt) break;
+        float fa[8], fb[8];
+        pk::unpack8(a[it], fa);
+        pk::unpack8(b[it], fb);
+        const float m = ju < rot / 16 ? fminf(largest_pair<kInterleaved>(fa, fb) * f2, 3.402823466e38f)
+                                      : largest_single(fa, fb);
+        most = fmaxf(most, m);
+    }
+#pragma unroll
+    for (int x = 16; x >= 1; x >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, x));
+    float scale = pk::needed_scale(most);
+    if (off0 > 0) {
+        if (!pk::scale_ok(had)) {
+            if (lane == 0) pk::set_error(p.err, PK_DEVERR_SCALE);
+        } else if (had >= scale) {
+            scale = had;
+        } else {
+            // The scale grows: the older rows in the new one's steps.
+            const float ratio = had / scale;       // exact: `scale` is a power of two
+            for (int r = lrow; r < off0; r += kRows) {
+                uint4 *at = reinterpret_cast<uint4 *>(rows + r * D + ju * 16);
+                uint4 w = *at;
+                uint32_t *e = reinterpret_cast<uint32_t *>(&w);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float f[4];
+                    pk::e4m3x4_to_float(e[i], f);
+                    e[i] = pk::e4m3x4(f[0] * ratio, f[1] * ratio, f[2] * ratio, f[3] * ratio);
+                }
+                *at = w;
+            }
+        }
+    }
+    __syncwarp();                                  // every lane has its copy of the old scale
+    if (lane == 0) *scale_at = scale;
+    const float inv = 1.f / scale;
+#pragma unroll
+    for (int it = 0; it < kIters; ++it) {
+        const int t = it * kRows + lrow;
+        if (t >= nt) break;
+        float fa[8], fb[8];
+        pk::unpack8(a[it], fa);
+        pk::unpack8(b[it], fb);
+        if (ju < rot / 16) pk::rotate_unit<kInterleaved>(fa, fb, cs[t], ju, rot);
+        uint8_t *dst = rows + (off0 + t) * D;
+        *reinterpret_cast<uint2 *>(dst + o.x) = quantise8(fa, inv);
+        *reinterpret_cast<uint2 *>(dst + o.y) = quantise8(fb, inv);
     }
 }
 
@@ -308,12 +305,13 @@ cudaError_t launch_append(AppendParams &p, cudaStream_t stream) {
     }
     const int tokens = std::min(B, std::max(p.cu_q_lens ? p.max_q_len : 1, 1));   // of a cell, at most
     p.q_heads_per_cta = std::max(1, std::min(std::max(p.num_heads, 1), kQueryUnits / (tokens * (D / 16))));
+    p.kv_ctas = (2 * p.num_kv_heads + kWarps - 1) / kWarps;
     const int q_ctas = (p.num_heads + p.q_heads_per_cta - 1) / p.q_heads_per_cta;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(cells), static_cast<unsigned>(1 + q_ctas));
+    cfg.gridDim = dim3(static_cast<unsigned>(cells), static_cast<unsigned>(p.kv_ctas + q_ctas));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
     cfg.attrs = attr;

@@ -9,7 +9,7 @@
 //   q * 2^k = h + l / 32, 2^k bringing the row's largest to [128, 256): two
 //     terms hold a bf16 value exactly down to 2^-13 of the row's largest, and
 //     what is smaller to 2^-22 of it.
-//   u = 2^(t - m) = h1 + h2 / 32 + h3 / 2^16, u <= 256: to 2^-10 of u, and
+//   u = 2^(t - m) = h1 + h2 / 32 + h3 / 2^16, u <= 256: to 2^-9 of u (2^-11 below 4), and
 //     nothing above 2^-25 is lost, of a largest weight that is 1 or more (see
 //     the reference below).  bf16 weights are to 2^-9.
 // The extra columns cost MMA time only, and a tile's MMAs take a tenth of the

@@ -13,7 +13,10 @@
 namespace {
 
 constexpr int kMaxThreads = 256;
-constexpr int kBatch = 4;      // units (2 x 16 bytes) a thread has in flight
+// Eight CTAs an SM, one unit (2 x 16 bytes) of a thread in flight: 64 KiB an SM
+// either way, but more CTAs cover one another's start and end (8,192 tokens of
+// 64 + 16 heads: 53.5 us; four units a thread with four CTAs: 61 us).
+constexpr int kCtasPerSm = 8;
 
 struct RopeParams {
     uint16_t *q_out;
@@ -29,7 +32,7 @@ struct RopeParams {
 };
 
 template <int D, bool kInterleaved>
-__global__ void __launch_bounds__(kMaxThreads)
+__global__ void __launch_bounds__(kMaxThreads, kCtasPerSm)
 rope_and_cache_kernel(const RopeParams p) {
     constexpr int kUnits = D / 16;                 // units a head
     __shared__ __align__(16) float2 cs[D / 2];
@@ -43,20 +46,18 @@ rope_and_cache_kernel(const RopeParams p) {
     if (slot >= p.num_slots && threadIdx.x == 0) pk::set_error(p.err, PK_DEVERR_SLOT);
     const int threads = blockDim.x;
 
-    for (int base = 0; base < units; base += threads * kBatch) {
-        const int u0 = base + threadIdx.x;
-        uint4 a[kBatch], b[kBatch];
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int u = u0 + i * threads;
-            if (u >= units) break;
-            const int head = u / kUnits;
+    for (int base = 0; base < units; base += threads) {
+        const int u = base + threadIdx.x;
+        const bool active = u < units;
+        const int head = u / kUnits, j = u % kUnits;
+        const int2 o = pk::unit_offsets(j, head < H + Hkv ? p.rot : 0, D);
+        uint4 a = make_uint4(0, 0, 0, 0), b = a;
+        if (active) {
             const uint16_t *src = head < H        ? p.q + t * p.q_stride + head * D
                                   : head < H + Hkv ? p.k + t * p.k_stride + (head - H) * D
                                                    : p.v + t * p.v_stride + (head - H - Hkv) * D;
-            const int2 o = pk::unit_offsets(u % kUnits, head < H + Hkv ? p.rot : 0, D);
-            a[i] = pk::ld_stream(src + o.x);
-            b[i] = pk::ld_stream(src + o.y);
+            a = pk::ld_stream(src + o.x);
+            b = pk::ld_stream(src + o.y);
         }
         if (base == 0) {
             const int64_t pos = p.rot ? p.positions[t] : 0;
@@ -64,31 +65,25 @@ rope_and_cache_kernel(const RopeParams p) {
                 cs[i] = pk::rotation(pos, pk::turns_per_position(p.inv_freq[i]), p.factor);
             __syncthreads();
         }
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int u = u0 + i * threads;
-            if (u >= units) break;
-            const int head = u / kUnits, j = u % kUnits;
-            const int2 o = pk::unit_offsets(j, head < H + Hkv ? p.rot : 0, D);
-            if (head < H + Hkv && j < p.rot / 16) {
-                float fa[8], fb[8];
-                pk::unpack8(a[i], fa);
-                pk::unpack8(b[i], fb);
-                pk::rotate_unit<kInterleaved>(fa, fb, cs, j, p.rot);
-                a[i] = pk::pack8(fa);
-                b[i] = pk::pack8(fb);
-            }
-            uint16_t *dst;
-            if (head < H) {
-                dst = p.q_out + t * p.q_out_stride + head * D;
-            } else {
-                if (!store_kv) continue;
-                dst = head < H + Hkv ? p.k_cache + (slot * Hkv + (head - H)) * D
-                                     : p.v_cache + (slot * Hkv + (head - H - Hkv)) * D;
-            }
-            *reinterpret_cast<uint4 *>(dst + o.x) = a[i];
-            *reinterpret_cast<uint4 *>(dst + o.y) = b[i];
+        if (!active) break;
+        if (head < H + Hkv && j < p.rot / 16) {
+            float fa[8], fb[8];
+            pk::unpack8(a, fa);
+            pk::unpack8(b, fb);
+            pk::rotate_unit<kInterleaved>(fa, fb, cs, j, p.rot);
+            a = pk::pack8(fa);
+            b = pk::pack8(fb);
         }
+        uint16_t *dst;
+        if (head < H) {
+            dst = p.q_out + t * p.q_out_stride + head * D;
+        } else {
+            if (!store_kv) break;                  // every further unit is K or V too
+            dst = head < H + Hkv ? p.k_cache + (slot * Hkv + (head - H)) * D
+                                 : p.v_cache + (slot * Hkv + (head - H - Hkv)) * D;
+        }
+        *reinterpret_cast<uint4 *>(dst + o.x) = a;
+        *reinterpret_cast<uint4 *>(dst + o.y) = b;
     }
 }
 
