@@ -90,7 +90,7 @@ def test_a_serving_loop():
                                              to_dev(flat), lens, SCALE)
         x.check([0, 1], counts, q, out)
     # Fork: both write the shared last block; the clone takes the scales along.
-    x.bm.fork(0, 2, len(x.k[0]))
+    x.bm.fork(0, 2)
     x.k[2], x.v[2] = x.k[0].copy(), x.v[0].copy()
     seqs = [0, 1, 2]
     for _ in range(5):
