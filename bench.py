@@ -56,7 +56,8 @@ E2E_CHUNK = 4
 # Kernel source files whose change invalidates the recorded ncu traffic.
 DOMINANT_SOURCES = ["paged_kv_cache_122_gb300/csrc/decode_tc.cu", "paged_kv_cache_122_gb300/csrc/sm100.cuh",
                     "paged_kv_cache_122_gb300/csrc/decode.cuh", "paged_kv_cache_122_gb300/csrc/decode_api.cu",
-                    "paged_kv_cache_122_gb300/csrc/block_scan.cuh"]
+                    "paged_kv_cache_122_gb300/csrc/block_scan.cuh",
+                    "paged_kv_cache_122_gb300/csrc/decode_split.cuh"]
 # DRAM bytes per launch of the dominant kernel from one ncu capture, and the
 # hash of its sources at that time (profiles/ holds the summary).
 RECORDED_TRAFFIC = {"sources_sha1": "66e29afac64e0ca3c432b97dec24cb0ccb78e151", "bytes_per_launch": 1125091840, "workload": "l3-70b"}

@@ -136,23 +136,34 @@ struct MiscT {
     int lens[kLenCache];          // the raw sequence lengths, when there are at most kLenCache
 };
 
-// 32 consecutive columns of this thread's TMEM lane.
-SM100_DEV void tmem_ld32(uint32_t taddr, float (&v)[32]) {
-    uint32_t r[32];
-    __syncwarp();
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr)
-        : "memory");
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+// N consecutive columns of this thread's TMEM lane, on their way: r may be used
+// after tmem_wait_ld(r), which takes it as an operand to say so.
+template <int N>
+SM100_DEV void tmem_ld_start(uint32_t taddr, uint32_t *r) {
+    static_assert(N == 8 || N == 16, "columns");
+    if constexpr (N == 8) {
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                     : "r"(taddr)
+                     : "memory");
+    } else {
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                     "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                       "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                     : "r"(taddr)
+                     : "memory");
+    }
+}
+template <int N>
+SM100_DEV void tmem_wait_ld(uint32_t (&r)[N]) {
+    static_assert(N % 8 == 0, "columns");
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+    for (int i = 0; i < N; i += 8)
+        asm volatile("tcgen05.wait::ld.sync.aligned;"
+                     : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                       "+r"(r[i + 6]), "+r"(r[i + 7])
+                     ::"memory");
 }
 
 // Two floats in one 64-bit register and the packed fp32 instructions on them.
@@ -883,8 +894,14 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             if (i < n_tiles) {
                 const int st = i % kStages;
                 const int sb = i & 1;
-                if (!__all_sync(0xffffffffu, wait_for(smem_u32(&misc->s_full[i % kScores]), (i / kScores) & 1, &misc->never, lim) &&
-                                                 wait_for(smem_u32(&misc->sfull[st]), (i / kStages) & 1, &misc->never, lim))) {
+                // Three barriers asked side by side: the scores, the scales, and whether
+                // P buffer sb is free (P.V of tile i - 2 is done).
+                const bool scores_in = mbar_try_wait(smem_u32(&misc->s_full[i % kScores]), (i / kScores) & 1);
+                const bool scales_in = mbar_test_wait(smem_u32(&misc->sfull[st]), (i / kStages) & 1);
+                const bool p_free = mbar_test_wait(smem_u32(&misc->o_full[sb]), ((i >> 1) & 1) ^ 1);
+                if (!__all_sync(0xffffffffu,
+                                (scores_in || wait_slow(smem_u32(&misc->s_full[i % kScores]), (i / kScores) & 1, &misc->never, lim)) &&
+                                (scales_in || wait_slow(smem_u32(&misc->sfull[st]), (i / kStages) & 1, &misc->never, lim)))) {
                     misc->abort = 1;
                     set_error(p.err, PK_DEVERR_TIMEOUT);
                     break;
@@ -906,33 +923,19 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                     }
                 }
                 tc_fence_after();
-                // Scores: h columns plus 1/32 of the l columns.
+                // Scores: h columns plus 1/32 of the l columns (of this group), on their
+                // way while the token's scales are looked at.
                 uint64_t t2[kPairs];
+                constexpr int kWide = kHeads * 16;
+                uint32_t sr[kWide];
                 const uint32_t saddr = lane_addr + C_::tS + (i % kScores) * C_::SCols;
-                {
-                    // h and l columns of this group.
-                    constexpr int kWide = kHeads * 16;
-                    float x[kWide];
-                    if constexpr (kGroups == 2 && HP == 1) {
-                        float h8[8], l8[8];
-                        tmem_ld<8>(saddr + 8 * grp, h8);
-                        tmem_ld<8>(saddr + HL + 8 * grp, l8);
-#pragma unroll
-                        for (int y = 0; y < 8; ++y) {
-                            x[y] = h8[y];
-                            x[8 + y] = l8[y];
-                        }
-                    } else if constexpr (kWide == 32) {
-                        tmem_ld32(saddr, x);
-                    } else {
-                        tmem_ld16(saddr + hd0 * NS, x);
-                    }
-#pragma unroll
-                    for (int y = 0; y < kPairs; ++y) {
-                        const int h = hd_of(y) * 16 + 2 * (y % kPerHead);
-                        t2[y] = fma2(f2(x[h + 8], NC > 1 ? x[h + 9] : 0.f), f2(kLevel2, kLevel2),
-                                     f2(x[h], NC > 1 ? x[h + 1] : 0.f));
-                    }
+                __syncwarp();
+                if constexpr (kGroups == 2 && HP == 1) {
+                    tmem_ld_start<8>(saddr + 8 * grp, sr);
+                    tmem_ld_start<8>(saddr + HL + 8 * grp, sr + 8);
+                } else {
+                    tmem_ld_start<16>(saddr + hd0 * NS, sr);
+                    if constexpr (kWide == 32) tmem_ld_start<16>(saddr + 16, sr + 16);
                 }
                 // The token's scales; one that is out of range hides the token's head.
                 const int2 held = misc->held[st];
@@ -950,6 +953,13 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                     lv[hd] = static_cast<float>(static_cast<int>(b >> 23) - 127);
                     if (b & 0x7fffffu) lv[hd] = __log2f(v1);
                     ivs[hd] = fast_rcp(v1);
+                }
+                tmem_wait_ld(sr);
+#pragma unroll
+                for (int y = 0; y < kPairs; ++y) {
+                    const int h = hd_of(y) * 16 + 2 * (y % kPerHead);
+                    t2[y] = fma2(f2(__uint_as_float(sr[h + 8]), NC > 1 ? __uint_as_float(sr[h + 9]) : 0.f), f2(kLevel2, kLevel2),
+                                 f2(__uint_as_float(sr[h]), NC > 1 ? __uint_as_float(sr[h + 1]) : 0.f));
                 }
 #pragma unroll
                 for (int x = 0; x < kPairs; ++x) {
@@ -1049,9 +1059,8 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                     words[1][j >> 2] |= h2 << sh;
                     words[2][j >> 2] |= h3 << sh;
                 }
-                // P buffer sb is free once P.V of tile i-2 is done.
-                if (!__all_sync(0xffffffffu, wait_for(smem_u32(&misc->o_full[sb]), ((i >> 1) & 1) ^ 1, &misc->never,
-                                                       lim))) {
+                if (!__all_sync(0xffffffffu, p_free || wait_slow(smem_u32(&misc->o_full[sb]), ((i >> 1) & 1) ^ 1,
+                                                                 &misc->never, lim))) {
                     misc->abort = 1;
                     set_error(p.err, PK_DEVERR_TIMEOUT);
                     break;
