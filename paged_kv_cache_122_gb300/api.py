@@ -325,7 +325,7 @@ def pk_rope_and_cache(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tenso
             raise ValueError("positions must have one entry per token")
     st = _on(dev, load().pk_rope_and_cache, _at(q_out), _at(q), k.data_ptr(), v.data_ptr(), *strides,
              k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), _at(positions), _at(inv_freq), rot,
-             int(interleaved), factor, T, H, Hkv, D, P, B, _raw_stream(dev, stream))
+             int(interleaved), float(factor), T, H, Hkv, D, P, B, _raw_stream(dev, stream))
     check("pk_rope_and_cache", st)
     if stream is not None and q_out is not None and not given:
         q_out.record_stream(stream)

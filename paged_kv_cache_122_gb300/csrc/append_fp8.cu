@@ -14,7 +14,9 @@
 // Bound: HBM bytes for prompts (2 bytes an element read, 2 written for q and 1
 // for K and V); for single tokens the chain of dependent loads (length, table
 // entry, old scale).  The queries' rows are rotated by CTAs of their own
-// (blockIdx.y >= 1), so that a step's K/V chain and its queries overlap.
+// (blockIdx.y >= kv_ctas), so that a step's K/V chain and its queries overlap.
+// Measured: 8,100 tokens of 64 + 16 heads of 128 in 57 us (315 MB, 0.82 of a
+// copy's rate); one token of each of 256 sequences 7.6 us back to back.
 #include "../../include/pagedkv_fp8.h"
 #include "fp8.cuh"
 #include "rope.cuh"
@@ -25,8 +27,14 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kCtasPerSm = 4;
-constexpr int kBatch = 3;          // q units (2 x 16 bytes) a thread has in flight
+// CTAs an SM and q units (2 x 16 bytes) a thread has in flight.  Blocks of 32
+// tokens at head dim 128 keep 64 registers of rows (9 chunks, 9,163 tokens of 32
+// + 16 heads: 35 us so, 39 us with the others' choice, which takes 27.8 us on
+// blocks of 16 where this one takes 28.3).
+template <int D, int B>
+constexpr int ctas_per_sm() { return D * B >= 4096 ? 3 : 4; }
+template <int D, int B>
+constexpr int query_batch() { return D * B >= 4096 ? 4 : 3; }
 constexpr int kQueryUnits = 2048;  // most q units of a CTA: 8 a thread
 
 struct AppendParams {
@@ -68,45 +76,62 @@ __device__ __forceinline__ int find_sequence(const AppendParams &p, int x) {
     return lo + max(fine - 1, 0);
 }
 
+// bf16 magnitudes in pairs: as integers they are ordered, with infinity and NaN
+// above all others.
+__device__ __forceinline__ uint32_t max_magnitude(uint32_t most, const uint4 &v) {
+    most = __vmaxu2(most, v.x & 0x7fff7fffu);
+    most = __vmaxu2(most, v.y & 0x7fff7fffu);
+    most = __vmaxu2(most, v.z & 0x7fff7fffu);
+    return __vmaxu2(most, v.w & 0x7fff7fffu);
+}
+constexpr uint32_t kHuge = 0x5e80;       // 2^62 as bf16: below, no square overflows
+
 // The square of a magnitude for the scale: values that are not finite count
 // as 0, finite ones whose square overflows as the largest float.
+constexpr float kLargest = 3.402823466e38f;
 __device__ __forceinline__ float capped(float m2, float x, float y) {
-    if (m2 <= 3.402823466e38f) return m2;
-    return fabsf(x) <= 3.402823466e38f && fabsf(y) <= 3.402823466e38f ? 3.402823466e38f : 0.f;
+    if (m2 <= kLargest) return m2;
+    return fabsf(x) <= kLargest && fabsf(y) <= kLargest ? kLargest : 0.f;
 }
 
-template <bool kInterleaved>
+// The largest squared length of a unit's pairs (kOdd: some value is huge or not finite).
+template <bool kInterleaved, bool kOdd>
 __device__ __forceinline__ float largest_pair(const float (&a)[8], const float (&b)[8]) {
     float m = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const float x = kInterleaved ? (i < 4 ? a[2 * i] : b[2 * i - 8]) : a[i];
         const float y = kInterleaved ? (i < 4 ? a[2 * i + 1] : b[2 * i - 7]) : b[i];
-        m = fmaxf(m, capped(fmaf(x, x, y * y), x, y));   // both squares are exact in fp32
+        const float m2 = fmaf(x, x, y * y);                    // both squares are exact in fp32
+        m = fmaxf(m, kOdd ? capped(m2, x, y) : m2);
     }
     return m;
 }
 
-__device__ __forceinline__ float largest_single(const float (&a)[8], const float (&b)[8]) {
-    float m = 0.f;
+__device__ __forceinline__ float largest_single_odd(uint4 a, uint4 b) {
+    float fa[8], fb[8], m = 0.f;
+    pk::unpack8(a, fa);
+    pk::unpack8(b, fb);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        m = fmaxf(m, fmaxf(capped(a[i] * a[i], a[i], 0.f), capped(b[i] * b[i], b[i], 0.f)));
+        m = fmaxf(m, fmaxf(capped(fa[i] * fa[i], fa[i], 0.f), capped(fb[i] * fb[i], fb[i], 0.f)));
     return m;
 }
 
-// Eight values to eight e4m3 bytes; what is not finite becomes NaN.
-__device__ __forceinline__ uint2 quantise8(const float (&f)[8], float inv) {
-    float y[8];
+// Eight values to eight e4m3 bytes; where `odd`, what is not finite becomes NaN.
+__device__ __forceinline__ uint2 quantise8(float (&f)[8], float inv, bool odd) {
+    if (odd) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        y[i] = fabsf(f[i]) <= 3.402823466e38f ? f[i] * inv : __int_as_float(0x7fffffff);
-    return make_uint2(pk::e4m3x4(y[0], y[1], y[2], y[3]), pk::e4m3x4(y[4], y[5], y[6], y[7]));
+        for (int i = 0; i < 8; ++i) f[i] = fabsf(f[i]) <= kLargest ? f[i] : __int_as_float(0x7fffffff);
+    }
+    return make_uint2(pk::e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
+                      pk::e4m3x4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv));
 }
 
 template <int D, int B, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+__global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, B>()))
 rope_and_cache_fp8_kernel(const AppendParams p) {
+    constexpr int kBatch = query_batch<D, B>();
     constexpr int kUnits = D / 16;                 // units (two 8-element vectors) a row
     constexpr int kRows = 32 / kUnits;             // rows a warp handles at once
     constexpr int kIters = (B + kRows - 1) / kRows;
@@ -237,15 +262,31 @@ rope_and_cache_fp8_kernel(const AppendParams p) {
     }
     if (static_cast<int>(blockIdx.y) * kWarps < Hkv) angles();      // some warp has keys
     if (!active) return;
+    // The largest magnitude decides how the squares are taken: of elements that
+    // are not rotated it is all there is to know.
+    const bool turned = ju < rot / 16;
+    uint32_t mag = 0;
 #pragma unroll
-    for (int it = 0; it < kIters; ++it) {
-        if (it * kRows >= nt) break;
-        float fa[8], fb[8];
-        pk::unpack8(a[it], fa);
-        pk::unpack8(b[it], fb);
-        const float m = ju < rot / 16 ? fminf(largest_pair<kInterleaved>(fa, fb) * f2, 3.402823466e38f)
-                                      : largest_single(fa, fb);
-        most = fmaxf(most, m);
+    for (int it = 0; it < kIters; ++it) mag = max_magnitude(max_magnitude(mag, a[it]), b[it]);
+    mag = max(mag & 0xffffu, mag >> 16);
+    const bool odd = __any_sync(0xffffffffu, mag >= kHuge);
+    if (turned || odd) {
+#pragma unroll
+        for (int it = 0; it < kIters; ++it) {
+            if (it * kRows >= nt) break;
+            if (!turned) {
+                most = fmaxf(most, largest_single_odd(a[it], b[it]));
+                continue;
+            }
+            float fa[8], fb[8];
+            pk::unpack8(a[it], fa);
+            pk::unpack8(b[it], fb);
+            most = fmaxf(most, odd ? largest_pair<kInterleaved, true>(fa, fb) : largest_pair<kInterleaved, false>(fa, fb));
+        }
+        if (turned) most = fminf(most * f2, kLargest);
+    } else {
+        const float x = pk::bf16_lo(mag);
+        most = x * x;
     }
 #pragma unroll
     for (int x = 16; x >= 1; x >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, x));
@@ -282,10 +323,10 @@ rope_and_cache_fp8_kernel(const AppendParams p) {
         float fa[8], fb[8];
         pk::unpack8(a[it], fa);
         pk::unpack8(b[it], fb);
-        if (ju < rot / 16) pk::rotate_unit<kInterleaved>(fa, fb, cs[t], ju, rot);
+        if (turned) pk::rotate_unit<kInterleaved>(fa, fb, cs[t], ju, rot);
         uint8_t *dst = rows + (off0 + t) * D;
-        *reinterpret_cast<uint2 *>(dst + o.x) = quantise8(fa, inv);
-        *reinterpret_cast<uint2 *>(dst + o.y) = quantise8(fb, inv);
+        *reinterpret_cast<uint2 *>(dst + o.x) = quantise8(fa, inv, odd);
+        *reinterpret_cast<uint2 *>(dst + o.y) = quantise8(fb, inv, odd);
     }
 }
 

@@ -9,26 +9,42 @@
 //   q * 2^k = h + l / 32, 2^k bringing the row's largest to [128, 256): two
 //     terms hold a bf16 value exactly down to 2^-13 of the row's largest, and
 //     what is smaller to 2^-22 of it.
-//   u = 2^(t - m) = h1 + h2 / 32 + h3 / 2^16, u <= 256: to 2^-9 of u (2^-11 below 4), and
-//     nothing above 2^-25 is lost, of a largest weight that is 1 or more (see
-//     the reference below).  bf16 weights are to 2^-9.
-// The extra columns cost MMA time only, and a tile's MMAs take a tenth of the
-// time its bytes take from HBM.
+//   u = 2^(t - m) = h1 + h2 / 32 + h3 / 2^16, u <= 256: to 2^-9 of u (2^-11
+//     below 4), and nothing above 2^-25 is lost, of a largest weight that is 1
+//     or more (m moves when a u exceeds 2^8).  bf16 weights are to 2^-9 too.
+// The extra columns cost MMA time only: the tensor pipe is active 7 % of
+// the time.
 //
 // Bound: HBM bytes of the cache, 2 D a token and KV head.  The work split, the
-// reference maximum that moves rarely, the merge of cut segments and the
-// bounded waits are those of the bf16 kernel (decode_tc.cu, decode_split.cuh).
+// reference maximum that moves rarely and the bounded waits are those of the
+// bf16 kernel (decode_tc.cu, decode_split.cuh).  What half the bytes a token
+// changed: a tile's bytes take 0.75 us of HBM time, less than one warp's chain
+// through it (scores in, exponentials, terms, weights out: 1,100 cycles) and
+// less than one dependent read, so
+//   - two CTAs an SM (three stages of 32 KiB each) where 128 registers do;
+//   - table entries are read four tiles ahead, through shared memory;
+//   - the code is kept small (rolled loops, waits and divisions out of line):
+//     the roles run different code side by side and missed the instruction
+//     cache a quarter of the time at 100 KB, 2 % at 65 KB;
+//   - whole warps wait, so that none runs on split.
+// Measured (back to back, 8 KV heads, head dim 128, block 16; 6,694 GB/s is a
+// copy): 8 sequences of 32k to 128k tokens 171-175 us at 4 query heads a KV
+// head (1.15 GB, 0.98-1.0 of the copy), 256 sequences of 16 to 8,192 tokens 88
+// us at 8 (0.52 GB, 0.88), 16 query columns 194 and 132 us.  The first form
+// took 307 and 151 us, one CTA an SM with table entries ahead 245 and 145.
 //
-// Per 128-token tile, inside a CTA (256 threads):
-//   warp 0    producer: block-table entries four tiles ahead (a lane per page),
-//             one box of K and one of V per page and KV head -- B D contiguous
-//             bytes -- into a ring of six stages, and the pages' scales by
-//             cp.async beside them;
-//   warp 1    MMA issuer (one thread, event loop);
-//   warps 2-5 softmax, thread <-> token (TMEM lane);
-//   warps 6-7 queries: take the (sequence, head) segments in turn, split their
+// Per 128-token tile, inside a CTA:
+//   producers block-table entries (a lane per page), one box of K and one of V
+//             per page and KV head -- B D contiguous bytes -- into the ring of
+//             stages, and the pages' scales by cp.async beside them;
+//   MMA       one warp, event loop: scores as soon as K is in, up to three
+//             tiles ahead; P.V as soon as the weights are;
+//   softmax   four warps a group, thread <-> token (TMEM lane);
+//   queries   two warps take the (sequence, head) segments in turn, split their
 //             rows into h and l and write them in the MMA's layout, ahead of
 //             the tiles.
+// Up to 8 query columns (per tile): 8 warps, two CTAs an SM.  16: two groups of
+// softmax warps, eight columns each, and four producers, one CTA an SM.
 // At head dim 64 a tile holds two adjacent KV heads (HP = 2) where their number
 // is even and the group small enough, so that its bytes are those of head dim 128.
 #include "decode_fp8.cuh"
@@ -238,7 +254,9 @@ SM100_DEV float fast_rcp(float v) {
     return r;
 }
 
-// The weights of the cut, as for the bf16 kernel's (decode_tc.cu).
+// The weights of the cut (see decode_tc.cu): a full tile 272; a segment, from
+// the batches of 256 equal lengths above, 0.3 tiles at 4 columns, 0.6 at 8 and
+// 2.9 at 16 (read-out, first reference, queries).
 constexpr int64_t kTileCost = 400;
 constexpr int kTokCost = 1;
 template <int NUSED, int HP>
@@ -320,7 +338,7 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     // Hkv counts the tile's KV head groups (segments per sequence).
     const int N = p.num_seqs, Hkv = p.num_kv_heads / HP, H = p.num_heads, B = p.block_size;
     const int lgB = __ffs(B) - 1;
-    const int cap = min(p.max_seq_len, p.max_blocks_per_seq * B);
+    const int cap = p.max_seq_len;                    // at most max_blocks_per_seq * B (checked on the host)
     const int Gq = H / p.num_kv_heads, lgG = __ffs(Gq) - 1;     // query heads per KV head (a power of two)
     Slot *slots = static_cast<Slot *>(p.tc_slots);
     const uint64_t lim = kWaitLimitNs;

@@ -91,7 +91,7 @@ extern "C" const char *pk_status_string(int status) {
     }
 }
 
-extern "C" int pk_version(void) { return (1 << 16) | 0; }
+extern "C" int pk_version(void) { return (1 << 16) | 1; }
 
 extern "C" int pk_get_device_error(unsigned int *code_out, pk_stream_t stream) {
     if (!code_out) return PK_ERR_NULL;

@@ -33,14 +33,17 @@ PK_DEV uint64_t turns_per_position(float f) {
 }
 
 // cos and sin of position * frequency, times `factor`.  The nearest quarter
-// turn is taken off in integers, so that the rest, at most an eighth of a
-// turn, keeps 24 significant bits as fp32.
+// turn is taken off in integers; the rest, at most an eighth of a turn, is x
+// below pi / 4, where the Taylor series to x^9 and x^8 are within 2^-25 of sine
+// and cosine (the next terms are x^11 / 11! and x^10 / 10!).
 PK_DEV float2 rotation(int64_t position, uint64_t turns, float factor) {
     const uint64_t a = static_cast<uint64_t>(position) * turns;
     const uint32_t quarter = static_cast<uint32_t>((a + (1ull << 61)) >> 62);
     const int64_t rest = static_cast<int64_t>(a - (static_cast<uint64_t>(quarter) << 62));
-    float s, c;
-    sincospif(static_cast<float>(rest) * 0x1p-63f, &s, &c);     // rest 2^-63 half turns
+    constexpr float kUnit = 3.65729520e-10f;                    // 2 pi / 2^34: of rest >> 30
+    const float x = static_cast<float>(static_cast<int32_t>(rest >> 30)) * kUnit, x2 = x * x;
+    float s = fmaf(x2, fmaf(x2, fmaf(x2, fmaf(x2, 1.f / 362880, -1.f / 5040), 1.f / 120), -1.f / 6), 1.f) * x;
+    float c = fmaf(x2, fmaf(x2, fmaf(x2, fmaf(x2, 1.f / 40320, -1.f / 720), 1.f / 24), -0.5f), 1.f);
     if (quarter & 1) {
         const float t = c;
         c = -s;

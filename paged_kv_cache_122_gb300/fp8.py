@@ -82,8 +82,8 @@ def pk_rope_and_cache_fp8(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.T
             raise ValueError("positions must have one entry per token")
     st = _on(dev, load().pk_rope_and_cache_fp8, _at(q_out), _at(q), k.data_ptr(), v.data_ptr(), *strides,
              k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
-             block_tables.data_ptr(), MB, seq_lens.data_ptr(), _at(cu_q_lens), max_q_len, N, _at(positions),
-             _at(inv_freq), rot, int(interleaved), factor, T, H, Hkv, D, P, B, _raw_stream(dev, stream))
+             block_tables.data_ptr(), MB, seq_lens.data_ptr(), _at(cu_q_lens), int(max_q_len), N, _at(positions),
+             _at(inv_freq), rot, int(interleaved), float(factor), T, H, Hkv, D, P, B, _raw_stream(dev, stream))
     check("pk_rope_and_cache_fp8", st)
     if stream is not None and q_out is not None and not given:
         q_out.record_stream(stream)
@@ -142,8 +142,7 @@ def _attend(name, out, q, cu_q_lens, max_q_len, k_cache, v_cache, k_scales, v_sc
         raise TypeError("out must be bf16 or fp32")
     if given:
         _need(out, "out", out.dtype, 3, dev)
-    if max_seq_len is None:
-        max_seq_len = MB * B
+    max_seq_len = MB * B if max_seq_len is None else int(max_seq_len)
     nbytes = pk_decode_fp8_workspace_bytes(N, H, Hkv, D, max_seq_len)
     if workspace is None:
         workspace = _workspace(dev, nbytes, stream)
@@ -152,13 +151,13 @@ def _attend(name, out, q, cu_q_lens, max_q_len, k_cache, v_cache, k_scales, v_sc
     elif workspace.numel() * workspace.element_size() < nbytes:
         raise ValueError("workspace too small")
     tail = (k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(),
-            MB, seq_lens.data_ptr(), max_seq_len, N, H, Hkv, D, P, B, scale, _at(workspace),
+            MB, seq_lens.data_ptr(), max_seq_len, N, H, Hkv, D, P, B, float(scale), _at(workspace),
             0 if workspace is None else workspace.nbytes, _raw_stream(dev, stream))
     if cu_q_lens is None:
         st = _on(dev, load().pk_paged_attention_decode_fp8, out.data_ptr(), dtype, q.data_ptr(), *tail)
     else:
         st = _on(dev, load().pk_paged_attention_multi_query_fp8, out.data_ptr(), dtype, q.data_ptr(), T,
-                 cu_q_lens.data_ptr(), max_q_len, *tail)
+                 cu_q_lens.data_ptr(), int(max_q_len), *tail)
     check(name, st)
     if stream is not None and not given:
         out.record_stream(stream)
@@ -221,7 +220,7 @@ def pk_gather_kv_fp8(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scales: tor
         max_seq_len = MB * B
     st = _on(dev, load().pk_gather_kv_fp8, out_k.data_ptr(), out_v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
              k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(), MB, seq_lens.data_ptr(),
-             cu_seq_lens.data_ptr(), rows, max_seq_len, N, Hkv, D, P, B, _raw_stream(dev, stream))
+             cu_seq_lens.data_ptr(), rows, int(max_seq_len), N, Hkv, D, P, B, _raw_stream(dev, stream))
     check("pk_gather_kv_fp8", st)
 
 
