@@ -36,6 +36,18 @@ def _stream(device: torch.device, stream=None):
     return ctypes.c_void_p(_raw_stream(device, stream))
 
 
+def _empty_like(t: torch.Tensor, dtype, stream=None) -> torch.Tensor:
+    """A contiguous result of ``t``'s shape for a kernel on ``stream`` that the
+    caller reads on the current stream: memory of the first, not handed out again
+    before the second is done.  (``torch.empty`` takes 2 us longer, for the shape.)"""
+    if stream is None:
+        return torch.empty_like(t, dtype=dtype, memory_format=torch.contiguous_format)
+    with torch.cuda.stream(stream):
+        out = torch.empty_like(t, dtype=dtype, memory_format=torch.contiguous_format)
+    out.record_stream(torch.cuda.current_stream(t.device))
+    return out
+
+
 def _on(device: torch.device, fn, *args) -> int:
     """``fn(*args)`` with ``device`` current."""
     if torch._C._cuda_getDevice() == device.index:
@@ -45,8 +57,9 @@ def _on(device: torch.device, fn, *args) -> int:
 
 
 def _need(t: torch.Tensor, name: str, dtype, ndim: int, device=None):
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == ndim and t.is_cuda
-            and (device is None or t.device == device) and t.is_contiguous()):
+    # The index is a number; a device object costs as much as two of these checks.
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == ndim and t.is_contiguous()
+            and (t.is_cuda if device is None else t.get_device() == device.index)):
         return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -80,7 +93,9 @@ def workspace_for(device: torch.device, nbytes: int, stream=None) -> Optional[to
     key = (device, _raw_stream(device, stream))
     ws = _WORKSPACES.get(key)
     if ws is None or ws.numel() < nbytes:
-        ws = new_workspace(nbytes, device)
+        # The stream's own memory: a smaller one that this replaces may still be in use there.
+        with torch.cuda.stream(stream):
+            ws = new_workspace(nbytes, device)
         _WORKSPACES[key] = ws
     return ws
 
@@ -249,7 +264,7 @@ reshape_and_cache = pk_reshape_and_cache
 def _need_rows(t: torch.Tensor, name: str, device):
     """[tokens, heads, D] bf16 rows whose heads are dense; the tokens may be any
     stride apart (a slice of a fused projection).  Returns that stride."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.dim() == 3 and t.device == device):
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.dim() == 3 and t.get_device() == device.index):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
         if t.dtype != torch.bfloat16:
@@ -266,7 +281,7 @@ def _need_rows(t: torch.Tensor, name: str, device):
     return s0 if T > 1 else max(s0, heads * D + -(heads * D) % 8)
 
 
-def _rope_args(q, k, v, inv_freq, q_out, dev):
+def _rope_args(q, k, v, inv_freq, q_out, dev, stream):
     """Checks what the two rotary appends share; returns the queries' output,
     the number of query heads, the rotated elements and the token strides."""
     k_stride, v_stride = _need_rows(k, "k", dev), _need_rows(v, "v", dev)
@@ -287,7 +302,7 @@ def _rope_args(q, k, v, inv_freq, q_out, dev):
     if q.shape[0] != T or q.shape[2] != D:
         raise ValueError("q must have k's tokens and head dim")
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        q_out = _empty_like(q, q.dtype, stream)
         out_stride = q.shape[1] * D
     else:
         out_stride = _need_rows(q_out, "q_out", dev)
@@ -309,8 +324,7 @@ def pk_rope_and_cache(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tenso
     _need(k_cache, "k_cache", torch.bfloat16, 4, dev)
     _need(v_cache, "v_cache", torch.bfloat16, 4, dev)
     _need(slot_mapping, "slot_mapping", torch.int64, 1, dev)
-    given = q_out is not None
-    q_out, H, rot, strides = _rope_args(q, k, v, inv_freq, q_out, dev)
+    q_out, H, rot, strides = _rope_args(q, k, v, inv_freq, q_out, dev, stream)
     T, Hkv, D = k.shape
     P, B, Hc, Dc = k_cache.shape
     if (Hc, Dc) != (Hkv, D) or v_cache.shape != k_cache.shape:
@@ -327,8 +341,6 @@ def pk_rope_and_cache(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tenso
              k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), _at(positions), _at(inv_freq), rot,
              int(interleaved), float(factor), T, H, Hkv, D, P, B, _raw_stream(dev, stream))
     check("pk_rope_and_cache", st)
-    if stream is not None and q_out is not None and not given:
-        q_out.record_stream(stream)
     return q_out
 
 

@@ -8,6 +8,7 @@ unprefixed names are the same calls.
 """
 from __future__ import annotations
 
+import contextlib
 import functools
 from typing import Optional, Tuple
 
@@ -15,9 +16,10 @@ import torch
 
 from . import _native
 from ._native import check, load
-from .api import _at, _need, _on, _raw_stream, _rope_args, new_workspace, workspace_for
+from .api import _at, _empty_like, _need, _on, _raw_stream, _rope_args, new_workspace, workspace_for
 
 FP8 = torch.float8_e4m3fn
+_NOTHING = contextlib.nullcontext()
 
 
 def new_cache_fp8(num_blocks: int, num_kv_heads: int, block_size: int, head_dim: int, device
@@ -58,8 +60,7 @@ def pk_rope_and_cache_fp8(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.T
     P, Hc, B, Dc = _need_cache(k_cache, v_cache, k_scales, v_scales, dev)
     _need(block_tables, "block_tables", torch.int32, 2, dev)
     _need(seq_lens, "seq_lens", torch.int32, 1, dev)
-    given = q_out is not None
-    q_out, H, rot, strides = _rope_args(q, k, v, inv_freq, q_out, dev)
+    q_out, H, rot, strides = _rope_args(q, k, v, inv_freq, q_out, dev, stream)
     T, Hkv, D = k.shape
     N, MB = block_tables.shape
     if (Hc, Dc) != (Hkv, D):
@@ -85,8 +86,6 @@ def pk_rope_and_cache_fp8(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.T
              block_tables.data_ptr(), MB, seq_lens.data_ptr(), _at(cu_q_lens), int(max_q_len), N, _at(positions),
              _at(inv_freq), rot, int(interleaved), float(factor), T, H, Hkv, D, P, B, _raw_stream(dev, stream))
     check("pk_rope_and_cache_fp8", st)
-    if stream is not None and q_out is not None and not given:
-        q_out.record_stream(stream)
     return q_out
 
 
@@ -104,9 +103,8 @@ def _workspace(dev, nbytes: int, stream) -> Optional[torch.Tensor]:
     the graph's own pool, so that two graphs never share one."""
     if nbytes == 0:
         return None
-    if torch._C._cuda_isCurrentStreamCapturing():
-        return new_workspace(nbytes, dev)
-    return workspace_for(dev, nbytes, stream)
+    with torch.cuda.stream(stream) if stream is not None else _NOTHING:
+        return new_workspace(nbytes, dev) if torch._C._cuda_isCurrentStreamCapturing() else workspace_for(dev, nbytes, stream)
 
 
 def _attend(name, out, q, cu_q_lens, max_q_len, k_cache, v_cache, k_scales, v_scales, block_tables, seq_lens, scale,
@@ -131,7 +129,7 @@ def _attend(name, out, q, cu_q_lens, max_q_len, k_cache, v_cache, k_scales, v_sc
             raise ValueError("cu_q_lens must have one entry more than sequences")
     given = out is not None
     if not given:
-        out = torch.empty(shape, dtype=out_dtype, device=dev)
+        out = _empty_like(q, out_dtype, stream)
     elif out.shape != shape:
         raise ValueError("out must have q's shape")
     if out.dtype is torch.bfloat16:
@@ -159,8 +157,6 @@ def _attend(name, out, q, cu_q_lens, max_q_len, k_cache, v_cache, k_scales, v_sc
         st = _on(dev, load().pk_paged_attention_multi_query_fp8, out.data_ptr(), dtype, q.data_ptr(), T,
                  cu_q_lens.data_ptr(), int(max_q_len), *tail)
     check(name, st)
-    if stream is not None and not given:
-        out.record_stream(stream)
     return out
 
 

@@ -205,3 +205,42 @@ def test_lengths_written_just_before_the_call():
         torch.cuda.synchronize()
         assert torch.equal(out, want)
     pk.pk_get_device_error()
+
+
+def test_memory_of_a_call_on_another_stream():
+    # What a call on a side stream allocates is the side stream's: it is handed
+    # out again only behind the call, eager (a workspace that a larger one
+    # replaces) and captured (one of the graph's pool, on a forked branch).
+    from paged_kv_cache_122_gb300 import api, fp8
+    c = attention_case(11, [9000, 700], [1, 1], 8, 2, 128, 16)
+    want = attend(c)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(50_000_000)                           # about 30 ms
+    old = api.workspace_for(DEV, 3 << 20, side).data_ptr()
+    api.workspace_for(DEV, 5 << 20, side)                       # the first is free now
+    assert torch.empty(3 << 20, dtype=torch.uint8, device=DEV).data_ptr() != old
+    out = attend(c, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(out, want)
+
+    made = []
+    new_workspace, fp8.new_workspace = fp8.new_workspace, lambda n, dev: made.append(new_workspace(n, dev)) or made[-1]
+    try:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            side.wait_stream(torch.cuda.current_stream())
+            out = attend(c, stream=side)
+            ptr, size = made.pop().data_ptr(), 1 << 20
+            other = [torch.full((size,), 7, dtype=torch.uint8, device=DEV) for _ in range(40)]
+            torch.cuda.current_stream().wait_stream(side)
+    finally:
+        fp8.new_workspace = new_workspace
+    assert all(not o.data_ptr() <= ptr < o.data_ptr() + size for o in other)
+    for _ in range(3):
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    assert pk.pk_get_device_error() == 0
