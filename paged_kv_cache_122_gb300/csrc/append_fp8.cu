@@ -145,6 +145,10 @@ rope_and_cache_fp8_kernel(const AppendParams p) {
         s = blockIdx.x / p.cells_per_seq;
         j = blockIdx.x % p.cells_per_seq;
     } else {
+        // The search may pass over a sequence whose rows run backwards: it is reported here.
+        if (blockIdx.y == 0 && threadIdx.x == 0 && static_cast<int>(blockIdx.x) < p.num_seqs &&
+            p.cu_q_lens[blockIdx.x + 1] < p.cu_q_lens[blockIdx.x])
+            pk::set_error(p.err, PK_DEVERR_SEQ_LEN);
         s = find_sequence<B>(p, blockIdx.x);
         j = static_cast<int>(blockIdx.x) - first_cell<B>(p, s);
     }

@@ -182,6 +182,19 @@ def test_bad_metadata_is_reported_and_nothing_of_it_written():
         assert torch.equal(t["ks"][to_dev(c["bt"][0, :1].astype(np.int64))], t0["ks"][to_dev(c["bt"][0, :1].astype(np.int64))])
 
 
+def test_rows_that_run_backwards_are_reported_where_sequences_are_searched():
+    from paged_kv_cache_122_gb300 import _native as N
+    new = [600] + [1] * 30
+    c = _case(33, [5, 5, 400] + [5] * 28, new, 4, 2, 128, 16, 64)
+    cu = c["cu"].copy()
+    cu[2] = 300                                                 # sequence 1 has -300 rows, sequence 2 302 of its 401
+    _run(c, cu_q_lens=to_dev(cu), max_q_len=600)
+    assert pk.pk_get_device_error() == N.DEVERR_SEQ_LEN
+    _, t = _run(c, cu_q_lens=to_dev(c["cu"]), max_q_len=600)
+    assert pk.pk_get_device_error() == 0
+    _compare(c, t)
+
+
 def test_scale_outside_the_range_is_reported():
     c = _case(14, [5], [1], 2, 2, 64, 16, 0)
     b = int(c["bt"][0, 0])
