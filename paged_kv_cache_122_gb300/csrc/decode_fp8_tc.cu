@@ -1005,7 +1005,7 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 for (int x = 0; x < kPairs; ++x) {
                     d[x] = add2(t2[x], neg_m[x]);
                     const float2 v = unf2(d[x]);
-                    top = fmaxf(top, fmaxf(v.x, v.y));
+                    top = fmaxf(top, NC > 1 ? fmaxf(v.x, v.y) : v.x);
                 }
                 if (named_bar_or(bar, 128, top > kHeadroom)) {
                     // Rare: move the references to the running maxima less kStart.
