@@ -20,7 +20,7 @@ struct Pool {
 // grid = (pairs, 2 [K, V], chunks of one block): each thread keeps four
 // 16-byte reads in flight before it writes; chunk 0 moves the block's scales.
 __global__ void __launch_bounds__(kThreads)
-move_blocks_fp8_kernel(const Pool dst, const Pool src, const int64_t *__restrict__ pairs, int64_t block_vecs,
+move_blocks_fp8_kernel(const Pool dst, const Pool src, const int64_t *pairs, int64_t block_vecs,
                        int num_kv_heads, unsigned int *err) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -60,12 +60,11 @@ constexpr int kGatherBatch = 4;
 
 template <int D>
 __global__ void __launch_bounds__(kThreads)
-gather_kv_fp8_kernel(uint4 *__restrict__ out_k, uint4 *__restrict__ out_v, const uint2 *__restrict__ k_cache,
-                     const uint2 *__restrict__ v_cache, const float *__restrict__ k_scales,
-                     const float *__restrict__ v_scales, const int32_t *__restrict__ block_tables,
-                     int max_blocks_per_seq, const int32_t *__restrict__ seq_lens,
-                     const int64_t *__restrict__ cu_seq_lens, int64_t out_rows, int max_seq_len, int num_kv_heads,
-                     int num_blocks, int log2_block, unsigned int *err) {
+gather_kv_fp8_kernel(uint4 *out_k, uint4 *out_v, const uint2 *k_cache, const uint2 *v_cache, const float *k_scales,
+                     const float *v_scales, const int32_t *block_tables, int max_blocks_per_seq, const int32_t *seq_lens,
+                     const int64_t *cu_seq_lens, int64_t out_rows, int max_seq_len, int num_kv_heads, int num_blocks,
+                     int log2_block, unsigned int *err) {
+    // (No __restrict__: what the previous kernel wrote may not be read ahead of the wait.)
     constexpr int kVecs = D / 8;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
