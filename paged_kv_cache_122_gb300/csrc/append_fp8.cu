@@ -15,7 +15,7 @@
 // for K and V); for single tokens the chain of dependent loads (length, table
 // entry, old scale).  The queries' rows are rotated by CTAs of their own
 // (blockIdx.y >= kv_ctas), so that a step's K/V chain and its queries overlap.
-// Measured: 8,100 tokens of 64 + 16 heads of 128 in 57 us (315 MB, 0.82 of a
+// Measured: 8,100 tokens of 64 + 16 heads of 128 in 57 us (315 MB, 0.81 of a
 // copy's rate); one token of each of 256 sequences 7.6 us back to back.
 #include "../../include/pagedkv_fp8.h"
 #include "fp8.cuh"

@@ -27,10 +27,10 @@
 //     the roles run different code side by side and missed the instruction
 //     cache a quarter of the time at 100 KB, 2 % at 65 KB;
 //   - whole warps wait, so that none runs on split.
-// Measured (back to back, 8 KV heads, head dim 128, block 16; 6,694 GB/s is a
+// Measured (back to back, 8 KV heads, head dim 128, block 16; 6,787 GB/s is a
 // copy): 8 sequences of 32k to 128k tokens 171-175 us at 4 query heads a KV
-// head (1.15 GB, 0.98-1.0 of the copy), 256 sequences of 16 to 8,192 tokens 88
-// us at 8 (0.52 GB, 0.88), 16 query columns 194 and 132 us.  The first form
+// head (1.15 GB, 0.97-0.99 of the copy), 256 sequences of 16 to 8,192 tokens 88
+// us at 8 (0.52 GB, 0.87), 16 query columns 194 and 132 us.  The first form
 // took 307 and 151 us, one CTA an SM with table entries ahead 245 and 145.
 //
 // Per 128-token tile, inside a CTA:

@@ -7,7 +7,7 @@
 // shared memory for all of its heads, while the token's vectors are already
 // on their way.  The angles come from the position and the frequency (see
 // rope.cuh), not from a table, so no position is out of range and no table is
-// read.  8,192 tokens of 64 + 16 heads of 128 take 53.5 us (335 MB, 0.94 of a
+// read.  8,192 tokens of 64 + 16 heads of 128 take 53.5 us (335 MB, 0.92 of a
 // copy's rate), four tokens of 24 heads of 64 1.7 us back to back.
 #include "rope.cuh"
 
