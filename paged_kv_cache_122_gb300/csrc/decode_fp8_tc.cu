@@ -902,9 +902,11 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 }
             }
         };
-        // Round n_tiles only reads out the last segment.
+        // Round n_tiles only reads out the last segment.  A warp that gives up leaves
+        // with i the first round whose barriers it has not met.
+        int i = 0;
 #pragma unroll 1
-        for (int i = 0; i <= n_tiles; ++i) {
+        for (; i <= n_tiles; ++i) {
             int4 mt = make_int4(0, 0, 0, 0);             // (s, h, t, nt), written with the stage
             int4 qm = make_int4(0, 1, 0, 0);             // (first query row, query tokens, first query position)
             bool seg_last = false;
@@ -1045,6 +1047,7 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                                                                &misc->never, lim))) {
                             misc->abort = 1;
                             set_error(p.err, PK_DEVERR_TIMEOUT);
+                            ++i;
                             break;
                         }
                         tc_fence_after();
@@ -1081,6 +1084,7 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                                                                  &misc->never, lim))) {
                     misc->abort = 1;
                     set_error(p.err, PK_DEVERR_TIMEOUT);
+                    ++i;
                     break;
                 }
                 // Rows of hidden tokens are zeroed once this tile's V has landed: the
@@ -1091,6 +1095,7 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                                                        lim))) {
                     misc->abort = 1;
                     set_error(p.err, PK_DEVERR_TIMEOUT);
+                    ++i;
                     break;
                 }
                 if (hide && (HP == 2 || grp == 0)) {
@@ -1124,6 +1129,7 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             if (pending && !finalize()) {
                 misc->abort = 1;
                 set_error(p.err, PK_DEVERR_TIMEOUT);
+                ++i;
                 break;
             }
             if (seg_last) {
@@ -1140,6 +1146,12 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 pend_cut_end = mt.z == mt.w - 1;
                 close_segment();
             }
+        }
+        // Its group may be further on (a wait can end for one warp just after another
+        // gave up): it meets them at the barriers that are left, or they would wait for ever.
+#pragma unroll 1
+        for (; i <= n_tiles; ++i) {
+            if (i == n_tiles || named_bar_or(bar, 128, false)) named_bar_sync(bar, 128);
         }
         tc_fence_before();
     }
