@@ -97,13 +97,14 @@ __device__ __forceinline__ float capped(float m2, float x, float y) {
 // The largest squared length of a unit's pairs (kOdd: some value is huge or not finite).
 template <bool kInterleaved, bool kOdd>
 __device__ __forceinline__ float largest_pair(const float (&a)[8], const float (&b)[8]) {
+    auto x = [&](int i) { return kInterleaved ? (i < 4 ? a[2 * i] : b[2 * i - 8]) : a[i]; };
+    auto y = [&](int i) { return kInterleaved ? (i < 4 ? a[2 * i + 1] : b[2 * i - 7]) : b[i]; };
     float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float x = kInterleaved ? (i < 4 ? a[2 * i] : b[2 * i - 8]) : a[i];
-        const float y = kInterleaved ? (i < 4 ? a[2 * i + 1] : b[2 * i - 7]) : b[i];
-        const float m2 = fmaf(x, x, y * y);                    // both squares are exact in fp32
-        m = fmaxf(m, kOdd ? capped(m2, x, y) : m2);
+    for (int i = 0; i < 8; i += 2) {
+        const uint64_t xx = pk::f2(x(i), x(i + 1)), yy = pk::f2(y(i), y(i + 1));
+        const float2 m2 = pk::unf2(pk::fma2(xx, xx, pk::mul2(yy, yy)));     // all squares are exact in fp32
+        m = fmaxf(m, kOdd ? fmaxf(capped(m2.x, x(i), y(i)), capped(m2.y, x(i + 1), y(i + 1))) : fmaxf(m2.x, m2.y));
     }
     return m;
 }
@@ -135,7 +136,7 @@ rope_and_cache_fp8_kernel(const AppendParams p) {
     constexpr int kUnits = D / 16;                 // units (two 8-element vectors) a row
     constexpr int kRows = 32 / kUnits;             // rows a warp handles at once
     constexpr int kIters = (B + kRows - 1) / kRows;
-    __shared__ __align__(16) float2 cs[B][D / 2];
+    __shared__ __align__(16) float cosines[B][D / 2], sines[B][D / 2];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
@@ -183,7 +184,9 @@ rope_and_cache_fp8_kernel(const AppendParams p) {
                 const uint64_t turns = pk::turns_per_position(p.inv_freq[pair]);
                 for (int t = t0; t < nt; t += per) {
                     const int64_t pos = p.positions ? p.positions[row0 + t] : static_cast<int64_t>(tok0 + t);
-                    cs[t][pair] = pk::rotation(pos, turns, p.factor);
+                    const float2 cs = pk::rotation(pos, turns, p.factor);
+                    cosines[t][pair] = cs.x;
+                    sines[t][pair] = cs.y;
                 }
             }
         }
@@ -194,14 +197,16 @@ rope_and_cache_fp8_kernel(const AppendParams p) {
         // ---- queries: heads h0 .. h0 + nh - 1 of the cell's tokens ---------
         const int h0 = (blockIdx.y - p.kv_ctas) * p.q_heads_per_cta;
         const int nh = min(p.q_heads_per_cta, H - h0);
-        const int units = nt * nh * kUnits;
+        const int per_token = nh * kUnits, units = nt * per_token;
+        // u / per_token as a product: exact, since both are at most kQueryUnits.
+        const uint32_t inv_per_token = 0xffffffffu / static_cast<uint32_t>(per_token) + 1u;
         for (int base = 0; base < units; base += kThreads * kBatch) {
             uint4 a[kBatch], b[kBatch];
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
                 const int u = base + i * kThreads + static_cast<int>(threadIdx.x);
                 if (u >= units) break;
-                const int t = u / (nh * kUnits), w = u - t * (nh * kUnits);
+                const int t = static_cast<int>(__umulhi(u, inv_per_token)), w = u - t * per_token;
                 const uint16_t *src = p.q + (row0 + t) * p.q_stride + (h0 + w / kUnits) * D;
                 const int2 o = pk::unit_offsets(w % kUnits, p.rot, D);
                 a[i] = pk::ld_stream(src + o.x);
@@ -212,14 +217,14 @@ rope_and_cache_fp8_kernel(const AppendParams p) {
             for (int i = 0; i < kBatch; ++i) {
                 const int u = base + i * kThreads + static_cast<int>(threadIdx.x);
                 if (u >= units) break;
-                const int t = u / (nh * kUnits), w = u - t * (nh * kUnits);
+                const int t = static_cast<int>(__umulhi(u, inv_per_token)), w = u - t * per_token;
                 const int ju = w % kUnits;
                 const int2 o = pk::unit_offsets(ju, p.rot, D);
                 if (ju < p.rot / 16) {
                     float fa[8], fb[8];
                     pk::unpack8(a[i], fa);
                     pk::unpack8(b[i], fb);
-                    pk::rotate_unit<kInterleaved>(fa, fb, cs[t], ju, p.rot);
+                    pk::rotate_unit<kInterleaved>(fa, fb, cosines[t], sines[t], ju, p.rot);
                     a[i] = pk::pack8(fa);
                     b[i] = pk::pack8(fb);
                 }
@@ -327,7 +332,7 @@ rope_and_cache_fp8_kernel(const AppendParams p) {
         float fa[8], fb[8];
         pk::unpack8(a[it], fa);
         pk::unpack8(b[it], fb);
-        if (turned) pk::rotate_unit<kInterleaved>(fa, fb, cs[t], ju, rot);
+        if (turned) pk::rotate_unit<kInterleaved>(fa, fb, cosines[t], sines[t], ju, rot);
         uint8_t *dst = rows + (off0 + t) * D;
         *reinterpret_cast<uint2 *>(dst + o.x) = quantise8(fa, inv, odd);
         *reinterpret_cast<uint2 *>(dst + o.y) = quantise8(fb, inv, odd);

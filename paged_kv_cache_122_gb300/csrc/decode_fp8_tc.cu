@@ -182,33 +182,6 @@ SM100_DEV void tmem_wait_ld(uint32_t (&r)[N]) {
                      ::"memory");
 }
 
-// Two floats in one 64-bit register and the packed fp32 instructions on them.
-SM100_DEV uint64_t f2(float lo, float hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-SM100_DEV float2 unf2(uint64_t v) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-SM100_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-SM100_DEV uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-SM100_DEV uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
 // The three terms of two weights u <= 256, two e4m3 bytes each.  u is first
 // rounded to fp16 (11 bits; steps of 2^-24 at the bottom), in which the
 // remainders after each term are exact.  The first, at most 8, is scaled by 32;

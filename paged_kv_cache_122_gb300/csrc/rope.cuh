@@ -82,29 +82,31 @@ PK_DEV int2 unit_offsets(int j, int rot, int D) {
     return make_int2(a, a + ((D - rot) >> 1));
 }
 
-// Rotate unit j < rot / 16: `a` and `b` are its two vectors, cs the token's
-// (cos, sin) of pair 0 .. rot / 2 - 1.
+// Rotate unit j < rot / 16: `a` and `b` are its two vectors, `cosines` and
+// `sines` the token's for pair 0 .. rot / 2 - 1.  Two pairs (x, y) at once, in
+// packed instructions: in the half layout a has the x and b the y of eight; in
+// the interleaved one they are neighbours, four pairs in each vector.
 template <bool kInterleaved>
-PK_DEV void rotate_unit(float (&a)[8], float (&b)[8], const float2 *cs, int j, int rot) {
+PK_DEV void rotate_unit(float (&a)[8], float (&b)[8], const float *cosines, const float *sines, int j, int rot) {
+    auto turn = [&](float &x0, float &x1, float &y0, float &y1, int pair) {
+        const uint64_t c = f2(cosines[pair], cosines[pair + 1]), s = f2(sines[pair], sines[pair + 1]);
+        const uint64_t x = f2(x0, x1), y = f2(y0, y1);
+        const float2 ys = unf2(mul2(y, s));
+        const float2 u = unf2(fma2(x, c, f2(-ys.x, -ys.y))), v = unf2(fma2(y, c, mul2(x, s)));
+        x0 = u.x;
+        x1 = u.y;
+        y0 = v.x;
+        y1 = v.y;
+    };
     if constexpr (kInterleaved) {
-        // Pairs lie in neighbouring elements: four in each vector.
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 ca = cs[4 * j + i], cb = cs[(rot >> 2) + 4 * j + i];
-            const float a0 = a[2 * i], a1 = a[2 * i + 1], b0 = b[2 * i], b1 = b[2 * i + 1];
-            a[2 * i] = a0 * ca.x - a1 * ca.y;
-            a[2 * i + 1] = a1 * ca.x + a0 * ca.y;
-            b[2 * i] = b0 * cb.x - b1 * cb.y;
-            b[2 * i + 1] = b1 * cb.x + b0 * cb.y;
+        for (int i = 0; i < 4; i += 2) {
+            turn(a[2 * i], a[2 * i + 2], a[2 * i + 1], a[2 * i + 3], 4 * j + i);
+            turn(b[2 * i], b[2 * i + 2], b[2 * i + 1], b[2 * i + 3], (rot >> 2) + 4 * j + i);
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float2 c = cs[8 * j + i];
-            const float x = a[i], y = b[i];
-            a[i] = x * c.x - y * c.y;
-            b[i] = y * c.x + x * c.y;
-        }
+        for (int i = 0; i < 8; i += 2) turn(a[i], a[i + 1], b[i], b[i + 1], 8 * j + i);
     }
 }
 

@@ -36,7 +36,7 @@ template <int D, bool kInterleaved>
 __global__ void __launch_bounds__(kMaxThreads, kCtasPerSm)
 rope_and_cache_kernel(const RopeParams p) {
     constexpr int kUnits = D / 16;                 // units a head
-    __shared__ __align__(16) float2 cs[D / 2];
+    __shared__ __align__(16) float cosines[D / 2], sines[D / 2];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t t = blockIdx.x;
@@ -62,8 +62,11 @@ rope_and_cache_kernel(const RopeParams p) {
         }
         if (base == 0) {
             const int64_t pos = p.rot ? p.positions[t] : 0;
-            for (int i = threadIdx.x; i < p.rot / 2; i += threads)
-                cs[i] = pk::rotation(pos, pk::turns_per_position(p.inv_freq[i]), p.factor);
+            for (int i = threadIdx.x; i < p.rot / 2; i += threads) {
+                const float2 cs = pk::rotation(pos, pk::turns_per_position(p.inv_freq[i]), p.factor);
+                cosines[i] = cs.x;
+                sines[i] = cs.y;
+            }
             __syncthreads();
         }
         if (!active) break;
@@ -71,7 +74,7 @@ rope_and_cache_kernel(const RopeParams p) {
             float fa[8], fb[8];
             pk::unpack8(a, fa);
             pk::unpack8(b, fb);
-            pk::rotate_unit<kInterleaved>(fa, fb, cs, j, p.rot);
+            pk::rotate_unit<kInterleaved>(fa, fb, cosines, sines, j, p.rot);
             a = pk::pack8(fa);
             b = pk::pack8(fb);
         }
