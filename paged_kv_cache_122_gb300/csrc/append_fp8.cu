@@ -94,28 +94,42 @@ __device__ __forceinline__ float capped(float m2, float x, float y) {
     return fabsf(x) <= kLargest && fabsf(y) <= kLargest ? kLargest : 0.f;
 }
 
-// The largest squared length of a unit's pairs (kOdd: some value is huge or not finite).
+// The largest squared length of two pairs (kOdd: some value is huge or not finite).
+template <bool kOdd>
+__device__ __forceinline__ float longest(float x0, float x1, float y0, float y1) {
+    const uint64_t x = pk::f2(x0, x1), y = pk::f2(y0, y1);
+    const float2 m2 = pk::unf2(pk::fma2(x, x, pk::mul2(y, y)));      // all squares are exact in fp32
+    return kOdd ? fmaxf(capped(m2.x, x0, y0), capped(m2.y, x1, y1)) : fmaxf(m2.x, m2.y);
+}
+
+// Of a unit's rotated pairs; 0 if it has none.
 template <bool kInterleaved, bool kOdd>
-__device__ __forceinline__ float largest_pair(const float (&a)[8], const float (&b)[8]) {
-    auto x = [&](int i) { return kInterleaved ? (i < 4 ? a[2 * i] : b[2 * i - 8]) : a[i]; };
-    auto y = [&](int i) { return kInterleaved ? (i < 4 ? a[2 * i + 1] : b[2 * i - 7]) : b[i]; };
-    float m = 0.f;
+__device__ __forceinline__ float longest_pair(const uint4 &a, const uint4 &b, pk::bool2 turned) {
+    float fa[8], fb[8], m = 0.f;
+    pk::unpack8(a, fa);
+    pk::unpack8(b, fb);
+    if constexpr (kInterleaved) {
+        if (turned.x) {
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-        const uint64_t xx = pk::f2(x(i), x(i + 1)), yy = pk::f2(y(i), y(i + 1));
-        const float2 m2 = pk::unf2(pk::fma2(xx, xx, pk::mul2(yy, yy)));     // all squares are exact in fp32
-        m = fmaxf(m, kOdd ? fmaxf(capped(m2.x, x(i), y(i)), capped(m2.y, x(i + 1), y(i + 1))) : fmaxf(m2.x, m2.y));
+            for (int i = 0; i < 8; i += 4) m = fmaxf(m, longest<kOdd>(fa[i], fa[i + 2], fa[i + 1], fa[i + 3]));
+        }
+        if (turned.y) {
+#pragma unroll
+            for (int i = 0; i < 8; i += 4) m = fmaxf(m, longest<kOdd>(fb[i], fb[i + 2], fb[i + 1], fb[i + 3]));
+        }
+    } else if (turned.x) {
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) m = fmaxf(m, longest<kOdd>(fa[i], fa[i + 1], fb[i], fb[i + 1]));
     }
     return m;
 }
 
-__device__ __forceinline__ float largest_single_odd(uint4 a, uint4 b) {
-    float fa[8], fb[8], m = 0.f;
-    pk::unpack8(a, fa);
-    pk::unpack8(b, fb);
+// The largest square of a vector where some value is huge or not finite.
+__device__ __forceinline__ float largest_odd(const uint4 &v) {
+    float f[8], m = 0.f;
+    pk::unpack8(v, f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        m = fmaxf(m, fmaxf(capped(fa[i] * fa[i], fa[i], 0.f), capped(fb[i] * fb[i], fb[i], 0.f)));
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, capped(f[i] * f[i], f[i], 0.f));
     return m;
 }
 
@@ -208,7 +222,7 @@ rope_and_cache_fp8_kernel(const AppendParams p) {
                 if (u >= units) break;
                 const int t = static_cast<int>(__umulhi(u, inv_per_token)), w = u - t * per_token;
                 const uint16_t *src = p.q + (row0 + t) * p.q_stride + (h0 + w / kUnits) * D;
-                const int2 o = pk::unit_offsets(w % kUnits, p.rot, D);
+                const int2 o = pk::unit_offsets<kInterleaved>(w % kUnits, p.rot, D);
                 a[i] = pk::ld_stream(src + o.x);
                 b[i] = pk::ld_stream(src + o.y);
             }
@@ -219,15 +233,8 @@ rope_and_cache_fp8_kernel(const AppendParams p) {
                 if (u >= units) break;
                 const int t = static_cast<int>(__umulhi(u, inv_per_token)), w = u - t * per_token;
                 const int ju = w % kUnits;
-                const int2 o = pk::unit_offsets(ju, p.rot, D);
-                if (ju < p.rot / 16) {
-                    float fa[8], fb[8];
-                    pk::unpack8(a[i], fa);
-                    pk::unpack8(b[i], fb);
-                    pk::rotate_unit<kInterleaved>(fa, fb, cosines[t], sines[t], ju, p.rot);
-                    a[i] = pk::pack8(fa);
-                    b[i] = pk::pack8(fb);
-                }
+                const int2 o = pk::unit_offsets<kInterleaved>(ju, p.rot, D);
+                pk::rotate_unit<kInterleaved>(a[i], b[i], cosines[t], sines[t], ju, p.rot, D);
                 uint16_t *dst = p.q_out + (row0 + t) * p.q_out_stride + (h0 + w / kUnits) * D;
                 *reinterpret_cast<uint4 *>(dst + o.x) = a[i];
                 *reinterpret_cast<uint4 *>(dst + o.y) = b[i];
@@ -250,7 +257,7 @@ rope_and_cache_fp8_kernel(const AppendParams p) {
     const bool is_k = task < Hkv;
     const int h = is_k ? task : task - Hkv;
     const int rot = is_k ? p.rot : 0;
-    const int2 o = pk::unit_offsets(ju, rot, D);
+    const int2 o = pk::unit_offsets<kInterleaved>(ju, rot, D);
     const uint16_t *src = is_k ? p.k : p.v;
     const int64_t stride = is_k ? p.k_stride : p.v_stride;
     float *scale_at = (is_k ? p.k_scales : p.v_scales) + static_cast<int64_t>(phys) * Hkv + h;
@@ -271,32 +278,39 @@ rope_and_cache_fp8_kernel(const AppendParams p) {
     }
     if (static_cast<int>(blockIdx.y) * kWarps < Hkv) angles();      // some warp has keys
     if (!active) return;
-    // The largest magnitude decides how the squares are taken: of elements that
-    // are not rotated it is all there is to know.
-    const bool turned = ju < rot / 16;
-    uint32_t mag = 0;
+    // The largest magnitudes decide how the squares are taken: of vectors that
+    // are not rotated they are all there is to know.
+    const pk::bool2 turned = pk::unit_turned<kInterleaved>(ju, rot, D);
+    uint32_t mag_a = 0, mag_b = 0;
 #pragma unroll
-    for (int it = 0; it < kIters; ++it) mag = max_magnitude(max_magnitude(mag, a[it]), b[it]);
-    mag = max(mag & 0xffffu, mag >> 16);
-    const bool odd = __any_sync(0xffffffffu, mag >= kHuge);
-    if (turned || odd) {
+    for (int it = 0; it < kIters; ++it) {
+        mag_a = max_magnitude(mag_a, a[it]);
+        mag_b = max_magnitude(mag_b, b[it]);
+    }
+    mag_a = max(mag_a & 0xffffu, mag_a >> 16);
+    mag_b = max(mag_b & 0xffffu, mag_b >> 16);
+    const bool odd = __any_sync(0xffffffffu, max(mag_a, mag_b) >= kHuge);
+    float plain = 0.f;                             // of elements that are not rotated
+    if (odd) {
 #pragma unroll
         for (int it = 0; it < kIters; ++it) {
             if (it * kRows >= nt) break;
-            if (!turned) {
-                most = fmaxf(most, largest_single_odd(a[it], b[it]));
-                continue;
-            }
-            float fa[8], fb[8];
-            pk::unpack8(a[it], fa);
-            pk::unpack8(b[it], fb);
-            most = fmaxf(most, odd ? largest_pair<kInterleaved, true>(fa, fb) : largest_pair<kInterleaved, false>(fa, fb));
+            most = fmaxf(most, longest_pair<kInterleaved, true>(a[it], b[it], turned));
+            if (!turned.x) plain = fmaxf(plain, largest_odd(a[it]));
+            if (!turned.y) plain = fmaxf(plain, largest_odd(b[it]));
         }
-        if (turned) most = fminf(most * f2, kLargest);
     } else {
-        const float x = pk::bf16_lo(mag);
-        most = x * x;
+        if (turned.x) {
+#pragma unroll
+            for (int it = 0; it < kIters; ++it) {
+                if (it * kRows >= nt) break;
+                most = fmaxf(most, longest_pair<kInterleaved, false>(a[it], b[it], turned));
+            }
+        }
+        const float x = turned.x ? 0.f : pk::bf16_lo(mag_a), y = turned.y ? 0.f : pk::bf16_lo(mag_b);
+        plain = fmaxf(x * x, y * y);
     }
+    most = fmaxf(fminf(most * f2, kLargest), plain);
 #pragma unroll
     for (int x = 16; x >= 1; x >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, x));
     float scale = pk::needed_scale(most);
@@ -332,7 +346,7 @@ rope_and_cache_fp8_kernel(const AppendParams p) {
         float fa[8], fb[8];
         pk::unpack8(a[it], fa);
         pk::unpack8(b[it], fb);
-        if (turned) pk::rotate_unit<kInterleaved>(fa, fb, cosines[t], sines[t], ju, rot);
+        pk::rotate_unit<kInterleaved>(fa, fb, cosines[t], sines[t], ju, rot, D);
         uint8_t *dst = rows + (off0 + t) * D;
         *reinterpret_cast<uint2 *>(dst + o.x) = quantise8(fa, inv, odd);
         *reinterpret_cast<uint2 *>(dst + o.y) = quantise8(fb, inv, odd);

@@ -5,6 +5,10 @@
 
 namespace pk {
 
+struct bool2 {
+    bool x, y;
+};
+
 // A frequency f (radians a position) in turns a position, as a 64-bit binary
 // fraction: the integer nearest below f / (2 pi) * 2^64, modulo 2^64 (whole
 // turns do not matter, since positions are integers).
@@ -70,43 +74,83 @@ PK_DEV uint4 pack8(const float f[8]) {
                       pack_bf16x2(f[6], f[7]));
 }
 
-// A head's D elements are handled in units of two 8-element vectors: of the
-// first `rot` elements, unit j < rot / 16 has those at 8 j and rot / 2 + 8 j
-// (in the half layout each other's partners), of the others those at
-// rot + 8 (j - rot / 16) and half of the rest further on.  Neighbouring
-// lanes then touch neighbouring vectors in either layout.
+// A head's D elements are handled in units of two 8-element vectors, so that
+// neighbouring lanes touch neighbouring vectors.  Interleaved layout: unit j has
+// those at 8 j and D / 2 + 8 j (a warp's rows are whole 128-byte lines, and with
+// half of a head rotated every lane rotates its first vector, none its second).
+// Half layout: of the first `rot` elements, unit j < rot / 16 has those at 8 j
+// and rot / 2 + 8 j, each other's partners; of the others those at
+// rot + 8 (j - rot / 16) and half of the rest further on.
+template <bool kInterleaved>
 PK_DEV int2 unit_offsets(int j, int rot, int D) {
+    if constexpr (kInterleaved) return make_int2(8 * j, (D >> 1) + 8 * j);
     const int n = rot >> 4;
     if (j < n) return make_int2(8 * j, (rot >> 1) + 8 * j);
     const int a = rot + 8 * (j - n);
     return make_int2(a, a + ((D - rot) >> 1));
 }
 
-// Rotate unit j < rot / 16: `a` and `b` are its two vectors, `cosines` and
-// `sines` the token's for pair 0 .. rot / 2 - 1.  Two pairs (x, y) at once, in
-// packed instructions: in the half layout a has the x and b the y of eight; in
-// the interleaved one they are neighbours, four pairs in each vector.
+// Whether unit j's vectors are rotated (x: the first, y: the second).
 template <bool kInterleaved>
-PK_DEV void rotate_unit(float (&a)[8], float (&b)[8], const float *cosines, const float *sines, int j, int rot) {
-    auto turn = [&](float &x0, float &x1, float &y0, float &y1, int pair) {
-        const uint64_t c = f2(cosines[pair], cosines[pair + 1]), s = f2(sines[pair], sines[pair + 1]);
-        const uint64_t x = f2(x0, x1), y = f2(y0, y1);
-        const float2 ys = unf2(mul2(y, s));
-        const float2 u = unf2(fma2(x, c, f2(-ys.x, -ys.y))), v = unf2(fma2(y, c, mul2(x, s)));
-        x0 = u.x;
-        x1 = u.y;
-        y0 = v.x;
-        y1 = v.y;
-    };
+PK_DEV bool2 unit_turned(int j, int rot, int D) {
+    if constexpr (kInterleaved) return {8 * j < rot, (D >> 1) + 8 * j < rot};
+    return {16 * j < rot, 16 * j < rot};
+}
+
+// Two pairs (x, y) at once, in packed instructions.
+PK_DEV void turn_pairs(float &x0, float &x1, float &y0, float &y1, const float *cosines, const float *sines) {
+    const uint64_t c = f2(cosines[0], cosines[1]), s = f2(sines[0], sines[1]);
+    const uint64_t x = f2(x0, x1), y = f2(y0, y1);
+    const float2 ys = unf2(mul2(y, s));
+    const float2 u = unf2(fma2(x, c, f2(-ys.x, -ys.y))), v = unf2(fma2(y, c, mul2(x, s)));
+    x0 = u.x;
+    x1 = u.y;
+    y0 = v.x;
+    y1 = v.y;
+}
+
+// Interleaved layout: a vector is four pairs, the first of which is number 0 here.
+PK_DEV void rotate_vector(float (&f)[8], const float *cosines, const float *sines) {
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) turn_pairs(f[2 * i], f[2 * i + 2], f[2 * i + 1], f[2 * i + 3], cosines + i, sines + i);
+}
+
+// Rotate unit j: `a` and `b` are its two vectors, `cosines` and `sines` the
+// token's for pair 0 .. rot / 2 - 1.
+template <bool kInterleaved>
+PK_DEV void rotate_unit(float (&a)[8], float (&b)[8], const float *cosines, const float *sines, int j, int rot, int D) {
+    const bool2 t = unit_turned<kInterleaved>(j, rot, D);
     if constexpr (kInterleaved) {
+        if (t.x) rotate_vector(a, cosines + 4 * j, sines + 4 * j);
+        if (t.y) rotate_vector(b, cosines + (D >> 2) + 4 * j, sines + (D >> 2) + 4 * j);
+    } else if (t.x) {
 #pragma unroll
-        for (int i = 0; i < 4; i += 2) {
-            turn(a[2 * i], a[2 * i + 2], a[2 * i + 1], a[2 * i + 3], 4 * j + i);
-            turn(b[2 * i], b[2 * i + 2], b[2 * i + 1], b[2 * i + 3], (rot >> 2) + 4 * j + i);
+        for (int i = 0; i < 8; i += 2) turn_pairs(a[i], a[i + 1], b[i], b[i + 1], cosines + 8 * j + i, sines + 8 * j + i);
+    }
+}
+
+// The same on bf16 vectors; those that are not rotated keep their bits.
+template <bool kInterleaved>
+PK_DEV void rotate_unit(uint4 &a, uint4 &b, const float *cosines, const float *sines, int j, int rot, int D) {
+    const bool2 t = unit_turned<kInterleaved>(j, rot, D);
+    float fa[8], fb[8];
+    if constexpr (kInterleaved) {
+        if (t.x) {
+            unpack8(a, fa);
+            rotate_vector(fa, cosines + 4 * j, sines + 4 * j);
+            a = pack8(fa);
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) turn(a[i], a[i + 1], b[i], b[i + 1], 8 * j + i);
+        if (t.y) {
+            unpack8(b, fb);
+            rotate_vector(fb, cosines + (D >> 2) + 4 * j, sines + (D >> 2) + 4 * j);
+            b = pack8(fb);
+        }
+    } else if (t.x) {
+        unpack8(a, fa);
+        unpack8(b, fb);
+        rotate_unit<kInterleaved>(fa, fb, cosines, sines, j, rot, D);
+        a = pack8(fa);
+        b = pack8(fb);
     }
 }
 

@@ -51,7 +51,7 @@ rope_and_cache_kernel(const RopeParams p) {
         const int u = base + threadIdx.x;
         const bool active = u < units;
         const int head = u / kUnits, j = u % kUnits;
-        const int2 o = pk::unit_offsets(j, head < H + Hkv ? p.rot : 0, D);
+        const int2 o = pk::unit_offsets<kInterleaved>(j, head < H + Hkv ? p.rot : 0, D);
         uint4 a = make_uint4(0, 0, 0, 0), b = a;
         if (active) {
             const uint16_t *src = head < H        ? p.q + t * p.q_stride + head * D
@@ -70,14 +70,7 @@ rope_and_cache_kernel(const RopeParams p) {
             __syncthreads();
         }
         if (!active) break;
-        if (head < H + Hkv && j < p.rot / 16) {
-            float fa[8], fb[8];
-            pk::unpack8(a, fa);
-            pk::unpack8(b, fb);
-            pk::rotate_unit<kInterleaved>(fa, fb, cosines, sines, j, p.rot);
-            a = pk::pack8(fa);
-            b = pk::pack8(fb);
-        }
+        if (head < H + Hkv) pk::rotate_unit<kInterleaved>(a, b, cosines, sines, j, p.rot, D);
         uint16_t *dst;
         if (head < H) {
             dst = p.q_out + t * p.q_out_stride + head * D;
