@@ -15,8 +15,9 @@
 // for K and V); for single tokens the chain of dependent loads (length, table
 // entry, old scale).  The queries' rows are rotated by CTAs of their own
 // (blockIdx.y >= kv_ctas), so that a step's K/V chain and its queries overlap.
-// Measured: 8,100 tokens of 64 + 16 heads of 128 in 57 us (315 MB, 0.81 of a
-// copy's rate); one token of each of 256 sequences 7.6 us back to back.
+// Measured back to back: 9 chunks, 6,689 tokens, of 32 + 16 heads of 128, half of
+// a head rotated, in 25.0 us (151 MB, 0.89 of a copy's rate), of 64 + 16 in 44.0
+// (0.87); one token of each of 256 sequences 6.8 us.
 #include "../../include/pagedkv_fp8.h"
 #include "fp8.cuh"
 #include "rope.cuh"
@@ -28,9 +29,10 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 // CTAs an SM and q units (2 x 16 bytes) a thread has in flight.  Blocks of 32
-// tokens at head dim 128 keep 64 registers of rows (9 chunks, 9,163 tokens of 32
-// + 16 heads: 35 us so, 39 us with the others' choice, which takes 27.8 us on
-// blocks of 16 where this one takes 28.3).
+// tokens at head dim 128 keep 64 registers of rows (the 9 chunks above: 27.5 us
+// so, 29.9 with the others' choice, which takes 24.9 on blocks of 16 where this
+// one takes 24.7; two CTAs and 8 units take 25.9, but 256 decode tokens 9.5
+// instead of 8.1).
 template <int D, int B>
 constexpr int ctas_per_sm() { return D * B >= 4096 ? 3 : 4; }
 template <int D, int B>
