@@ -7,8 +7,8 @@
 // shared memory for all of its heads, while the token's vectors are already
 // on their way.  The angles come from the position and the frequency (see
 // rope.cuh), not from a table, so no position is out of range and no table is
-// read.  8,192 tokens of 64 + 16 heads of 128 take 53.5 us (335 MB, 0.92 of a
-// copy's rate), four tokens of 24 heads of 64 1.7 us back to back.
+// read.  8,192 tokens of 64 + 16 heads of 128 take 53.3 us (336 MB, 0.93 of a
+// copy's rate), four tokens of 24 heads of 64 2.0 us back to back.
 #include "rope.cuh"
 
 namespace {
@@ -16,7 +16,7 @@ namespace {
 constexpr int kMaxThreads = 256;
 // Eight CTAs an SM, one unit (2 x 16 bytes) of a thread in flight: 64 KiB an SM
 // either way, but more CTAs cover one another's start and end (8,192 tokens of
-// 64 + 16 heads: 53.5 us; four units a thread with four CTAs: 61 us).
+// 64 + 16 heads: 53.3 us; four units a thread with four CTAs: 61 us).
 constexpr int kCtasPerSm = 8;
 
 struct RopeParams {
