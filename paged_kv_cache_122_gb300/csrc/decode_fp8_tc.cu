@@ -227,13 +227,15 @@ SM100_DEV float fast_rcp(float v) {
     return r;
 }
 
-// The weights of the cut (see decode_tc.cu): a full tile 272; a segment, from
-// the batches of 256 equal lengths above, 0.3 tiles at 4 columns, 0.6 at 8 and
-// 2.9 at 16 (read-out, first reference, queries).
+// The weights of the cut (see decode_tc.cu): a full tile 272; a segment (its
+// read-out, first reference and queries) by sweeps over 256 sequences of 16 to
+// 8,192 tokens.  Head dim 128, 16 columns: 132 us at 780, 130 at 500 to 680, 134
+// at 300; 8 columns: 88 at 80 to 160, 89 at 240.  Head pairs, 16 columns: 74 at
+// 780, 69 at 300 to 500; 8 columns: 54.7 at 80, 56 at 160.
 constexpr int64_t kTileCost = 400;
 constexpr int kTokCost = 1;
 template <int NUSED, int HP>
-constexpr int64_t seg_cost() { return NUSED > 8 ? 780 : 20 * NUSED; }
+constexpr int64_t seg_cost() { return NUSED > 8 ? (HP == 2 ? 400 : 600) : (HP == 2 ? 10 : 20) * NUSED; }
 
 // What follows from (head dim, query columns per KV head, KV heads per tile).
 template <int D, int NC, int HP>
