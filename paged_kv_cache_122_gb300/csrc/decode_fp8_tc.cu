@@ -30,7 +30,7 @@
 // Measured (back to back, 8 KV heads, head dim 128, block 16; 6,787 GB/s is a
 // copy): 8 sequences of 32k to 128k tokens 171-175 us at 4 query heads a KV
 // head (1.15 GB, 0.97-0.99 of the copy), 256 sequences of 16 to 8,192 tokens 88
-// us at 8 (0.52 GB, 0.87), 16 query columns 194 and 132 us.  The first form
+// us at 8 (0.52 GB, 0.87), 16 query columns 194 and 130 us.  The first form
 // took 307 and 151 us, one CTA an SM with table entries ahead 245 and 145.
 //
 // Per 128-token tile, inside a CTA:
