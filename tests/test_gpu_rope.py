@@ -124,6 +124,29 @@ def test_not_finite_values_stay_in_their_pair_and_odd_frequencies():
     assert np.all(np.abs(out[good] - ref[good]) <= 2.0 ** -8 * np.abs(ref[good]) + 2.0 ** -20)
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("D,rot", [(128, 16), (128, 64), (128, 80), (64, 32), (64, 48)])
+def test_elements_that_are_not_rotated_keep_their_bits(D, rot, interleaved):
+    # Every 16-bit pattern, NaNs with their payloads among them.
+    T, H, Hkv, B = 9, 6, 2, 16
+    rng = np.random.default_rng(rot)
+    bits = [torch.from_numpy(rng.integers(-2 ** 15, 2 ** 15, size=(T, n, D)).astype(np.int16)).to(DEV) for n in (H, Hkv, Hkv)]
+    q, k, v = (b.view(torch.bfloat16) for b in bits)
+    kc, vc = _pool(T, B, Hkv, D), _pool(T, B, Hkv, D)
+    slots = torch.arange(T, device=DEV)
+    out = pk.rope_and_cache(q, k, v, kc, vc, slots, slots + 100, to_dev(_freq(rot)), interleaved=interleaved)
+    assert torch.equal(out.view(torch.int16)[..., rot:], bits[0][..., rot:])
+    assert torch.equal(kc.view(torch.int16).view(-1, Hkv, D)[:T, :, rot:], bits[1][..., rot:])
+    assert torch.equal(vc.view(torch.int16).view(-1, Hkv, D)[:T], bits[2])
+    cache = pk.new_cache_fp8(1, Hkv, B, D, DEV)
+    bt, sl = torch.zeros(1, 1, dtype=torch.int32, device=DEV), torch.full((1,), T, dtype=torch.int32, device=DEV)
+    cu = torch.tensor([0, T], dtype=torch.int32, device=DEV)
+    out8 = pk.rope_and_cache_fp8(q, k, v, *cache, bt, sl, to_dev(_freq(rot)), cu_q_lens=cu, positions=slots + 100,
+                                 interleaved=interleaved)
+    assert torch.equal(out8.view(torch.int16)[..., rot:], bits[0][..., rot:])
+    assert pk.pk_get_device_error() == 0
+
+
 def test_other_stream_and_refusals():
     rng = np.random.default_rng(8)
     T, H, D, B = 64, 4, 128, 16
