@@ -32,16 +32,23 @@ def new_cache_fp8(num_blocks: int, num_kv_heads: int, block_size: int, head_dim:
 
 
 def _need_cache(k_cache, v_cache, k_scales, v_scales, dev):
+    tensor, index = torch.Tensor, dev.index
+    if (isinstance(k_cache, tensor) and isinstance(v_cache, tensor) and isinstance(k_scales, tensor)
+            and isinstance(v_scales, tensor) and k_cache.dtype is FP8 and v_cache.dtype is FP8
+            and k_scales.dtype is torch.float32 and v_scales.dtype is torch.float32 and k_cache.is_contiguous()
+            and v_cache.is_contiguous() and k_scales.is_contiguous() and v_scales.is_contiguous()
+            and k_cache.get_device() == v_cache.get_device() == k_scales.get_device() == v_scales.get_device() == index):
+        shape, scales = k_cache.shape, k_scales.shape
+        if len(shape) == 4 and v_cache.shape == shape and scales == shape[:2] and v_scales.shape == scales:
+            return shape
+    # Something is wrong: what, and where.
     _need(k_cache, "k_cache", FP8, 4, dev)
     _need(v_cache, "v_cache", FP8, 4, dev)
     _need(k_scales, "k_scales", torch.float32, 2, dev)
     _need(v_scales, "v_scales", torch.float32, 2, dev)
-    shape = k_cache.shape
-    if v_cache.shape != shape:
+    if v_cache.shape != k_cache.shape:
         raise ValueError("k_cache and v_cache must have the same shape")
-    if k_scales.shape != shape[:2] or v_scales.shape != shape[:2]:
-        raise ValueError(f"scales must be [num_blocks, num_kv_heads] = {tuple(shape[:2])}")
-    return shape
+    raise ValueError(f"scales must be [num_blocks, num_kv_heads] = {tuple(k_cache.shape[:2])}")
 
 
 def pk_rope_and_cache_fp8(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
