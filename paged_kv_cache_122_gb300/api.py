@@ -263,7 +263,7 @@ reshape_and_cache = pk_reshape_and_cache
 
 def _need_rows(t: torch.Tensor, name: str, device):
     """[tokens, heads, D] bf16 rows whose heads are dense; the tokens may be any
-    stride apart (a slice of a fused projection).  Returns that stride."""
+    stride apart (a slice of a fused projection).  Returns the shape and that stride."""
     if not (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.dim() == 3 and t.get_device() == device.index):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
@@ -274,41 +274,44 @@ def _need_rows(t: torch.Tensor, name: str, device):
         if not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor (this library has no CPU path)")
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    T, heads, D = t.shape
+    T, heads, D = shape = t.shape
     s0, s1, s2 = t.stride()
     if (s2 != 1 and D > 1) or (s1 != D and heads > 1):
         raise ValueError(f"the heads of a token of {name} must be contiguous")
-    return s0 if T > 1 else max(s0, heads * D + -(heads * D) % 8)
+    return shape, s0 if T > 1 else max(s0, heads * D + -(heads * D) % 8)
 
 
 def _rope_args(q, k, v, inv_freq, q_out, dev, stream):
-    """Checks what the two rotary appends share; returns the queries' output,
-    the number of query heads, the rotated elements and the token strides."""
-    k_stride, v_stride = _need_rows(k, "k", dev), _need_rows(v, "v", dev)
-    T, _, D = k.shape
-    if v.shape != k.shape:
+    """Checks what the two rotary appends share; returns the keys' shape, the
+    queries' output, the number of query heads, the rotated elements and the
+    token strides."""
+    shape, k_stride = _need_rows(k, "k", dev)
+    v_shape, v_stride = _need_rows(v, "v", dev)
+    T, _, D = shape
+    if v_shape != shape:
         raise ValueError("k and v must have the same shape")
     rot = 0
     if inv_freq is not None:
         _need(inv_freq, "inv_freq", torch.float32, 1, dev)
-        rot = 2 * inv_freq.shape[0]
+        rot = 2 * inv_freq.numel()
         if rot > D:
             raise ValueError(f"inv_freq has {rot // 2} frequencies for a head dim of {D}")
     if q is None:
         if q_out is not None:
             raise ValueError("q_out without q")
-        return None, 0, rot, (0, 0, k_stride, v_stride)
-    q_stride = _need_rows(q, "q", dev)
-    if q.shape[0] != T or q.shape[2] != D:
+        return shape, None, 0, rot, (0, 0, k_stride, v_stride)
+    q_shape, q_stride = _need_rows(q, "q", dev)
+    Tq, H, Dq = q_shape
+    if Tq != T or Dq != D:
         raise ValueError("q must have k's tokens and head dim")
     if q_out is None:
         q_out = _empty_like(q, q.dtype, stream)
-        out_stride = q.shape[1] * D
+        out_stride = H * D
     else:
-        out_stride = _need_rows(q_out, "q_out", dev)
-        if q_out.shape != q.shape:
+        out_shape, out_stride = _need_rows(q_out, "q_out", dev)
+        if out_shape != q_shape:
             raise ValueError("q_out must have q's shape")
-    return q_out, q.shape[1], rot, (out_stride, q_stride, k_stride, v_stride)
+    return shape, q_out, H, rot, (out_stride, q_stride, k_stride, v_stride)
 
 
 def pk_rope_and_cache(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
@@ -324,18 +327,17 @@ def pk_rope_and_cache(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tenso
     _need(k_cache, "k_cache", torch.bfloat16, 4, dev)
     _need(v_cache, "v_cache", torch.bfloat16, 4, dev)
     _need(slot_mapping, "slot_mapping", torch.int64, 1, dev)
-    q_out, H, rot, strides = _rope_args(q, k, v, inv_freq, q_out, dev, stream)
-    T, Hkv, D = k.shape
-    P, B, Hc, Dc = k_cache.shape
-    if (Hc, Dc) != (Hkv, D) or v_cache.shape != k_cache.shape:
+    (T, Hkv, D), q_out, H, rot, strides = _rope_args(q, k, v, inv_freq, q_out, dev, stream)
+    P, B, Hc, Dc = pool = k_cache.shape
+    if Hc != Hkv or Dc != D or v_cache.shape != pool:
         raise ValueError("k / v / cache shapes disagree")
-    if slot_mapping.shape[0] != T:
+    if slot_mapping.numel() != T:
         raise ValueError("slot_mapping must have one entry per token")
     if rot:
         if positions is None:
             raise ValueError("a rotation needs positions")
         _need(positions, "positions", torch.int64, 1, dev)
-        if positions.shape[0] != T:
+        if positions.numel() != T:
             raise ValueError("positions must have one entry per token")
     st = _on(dev, load().pk_rope_and_cache, _at(q_out), _at(q), k.data_ptr(), v.data_ptr(), *strides,
              k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), _at(positions), _at(inv_freq), rot,

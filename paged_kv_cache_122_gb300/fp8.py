@@ -67,12 +67,11 @@ def pk_rope_and_cache_fp8(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.T
     P, Hc, B, Dc = _need_cache(k_cache, v_cache, k_scales, v_scales, dev)
     _need(block_tables, "block_tables", torch.int32, 2, dev)
     _need(seq_lens, "seq_lens", torch.int32, 1, dev)
-    q_out, H, rot, strides = _rope_args(q, k, v, inv_freq, q_out, dev, stream)
-    T, Hkv, D = k.shape
+    (T, Hkv, D), q_out, H, rot, strides = _rope_args(q, k, v, inv_freq, q_out, dev, stream)
     N, MB = block_tables.shape
-    if (Hc, Dc) != (Hkv, D):
+    if Hc != Hkv or Dc != D:
         raise ValueError("k / v / cache shapes disagree")
-    if seq_lens.shape[0] != N:
+    if seq_lens.numel() != N:
         raise ValueError("seq_lens do not match the block tables' batch")
     if cu_q_lens is None:
         if T != N:
@@ -80,13 +79,13 @@ def pk_rope_and_cache_fp8(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.T
         max_q_len = 1
     else:
         _need(cu_q_lens, "cu_q_lens", torch.int32, 1, dev)
-        if cu_q_lens.shape[0] != N + 1:
+        if cu_q_lens.numel() != N + 1:
             raise ValueError("cu_q_lens must have one entry more than sequences")
         if max_q_len is None:
             max_q_len = T
     if positions is not None:
         _need(positions, "positions", torch.int64, 1, dev)
-        if positions.shape[0] != T:
+        if positions.numel() != T:
             raise ValueError("positions must have one entry per token")
     st = _on(dev, load().pk_rope_and_cache_fp8, _at(q_out), _at(q), k.data_ptr(), v.data_ptr(), *strides,
              k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
@@ -125,14 +124,14 @@ def _attend(name, out, q, cu_q_lens, max_q_len, k_cache, v_cache, k_scales, v_sc
     N, MB = block_tables.shape
     if Dk != D:
         raise ValueError("k_cache / v_cache / q shapes disagree")
-    if seq_lens.shape[0] != N:
+    if seq_lens.numel() != N:
         raise ValueError("seq_lens do not match the block tables' batch")
     if cu_q_lens is None:
         if T != N:
             raise ValueError("q must have one row per sequence")
     else:
         _need(cu_q_lens, "cu_q_lens", torch.int32, 1, dev)
-        if cu_q_lens.shape[0] != N + 1:
+        if cu_q_lens.numel() != N + 1:
             raise ValueError("cu_q_lens must have one entry more than sequences")
     given = out is not None
     if not given:
@@ -214,7 +213,7 @@ def pk_gather_kv_fp8(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scales: tor
     _need(out_k, "out_k", torch.bfloat16, 3, dev)
     _need(out_v, "out_v", torch.bfloat16, 3, dev)
     N, MB = block_tables.shape
-    if seq_lens.shape[0] != N or cu_seq_lens.shape[0] != N:
+    if seq_lens.numel() != N or cu_seq_lens.numel() != N:
         raise ValueError("seq_lens / cu_seq_lens do not match the block tables' batch")
     rows, heads, width = out_k.shape
     if out_k.shape != out_v.shape or (heads, width) != (Hkv, D):
