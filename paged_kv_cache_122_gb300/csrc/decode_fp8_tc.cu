@@ -72,6 +72,13 @@ constexpr float kLevel2 = 1.f / 32, kLevel3 = 1.f / 65536;   // what the terms o
 constexpr float kHeadroom = 8.f;                             // u <= 2^8: e4m3 holds 256
 constexpr float kNoReference = 3.0e38f;                      // minus the reference of a segment's start
 constexpr float kStart = 0.f;                                // the largest u when the reference moves: 2^0
+// The denominator adds (u * 2^60) * (2^-60 / vs).  Accepted scales span 2^128, so at
+// equal scores u can be 2^-128 where 1 / vs makes it a whole share, and 2^x is 0
+// below 2^-126.  With 2^60 only a u below 2^-186 is lost, a share of at most 2^-122
+// where the token of the largest u alone adds 2^-64; both factors are normal numbers.
+// (Added to the exponent after the reference is taken off: scores of 2^30 would
+// swallow it.)  Costs two packed instructions a pair of columns.
+constexpr float kLift = 60.f, kUnlift = 0x1p-60f;
 
 constexpr uint32_t kLayoutSw64 = 4;
 
@@ -947,7 +954,7 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                     const uint32_t b = __float_as_uint(v1);
                     lv[hd] = static_cast<float>(static_cast<int>(b >> 23) - 127);
                     if (b & 0x7fffffu) lv[hd] = __log2f(v1);
-                    ivs[hd] = fast_rcp(v1);
+                    ivs[hd] = fast_rcp(v1) * kUnlift;
                 }
                 tmem_wait_ld(sr);
 #pragma unroll
@@ -1009,11 +1016,14 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                             const float t = fmaxf(fmaxf(misc->red[0][j], misc->red[1][j]),
                                                   fmaxf(misc->red[2][j], misc->red[3][j]));
                             const float moved = fminf(n2[y], kStart - t);
-                            a[local(x) + y] = fast_exp2(moved - n2[y]);
+                            a[local(x) + y] = fast_exp2(moved - n2[y] + kLift);
                             n2[y] = moved;
                         }
                         neg_m[x] = f2(n2[0], n2[1]);
-                        l_run[x] = mul2(l_run[x], f2(a[local(x)], a[local(x) + 1]));
+                        // The denominator's factor with its 2^60 (as for u), O's without.
+                        l_run[x] = mul2(mul2(l_run[x], f2(kUnlift, kUnlift)), f2(a[local(x)], a[local(x) + 1]));
+                        a[local(x)] *= kUnlift;
+                        a[local(x) + 1] *= kUnlift;
                         d[x] = add2(t2[x], neg_m[x]);
                     }
                     if (!seg_first) {
@@ -1044,12 +1054,13 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 uint32_t words[3][2] = {};
 #pragma unroll
                 for (int x = 0; x < kPairs; ++x) {
-                    const float2 e = unf2(d[x]);
-                    const float u0 = fast_exp2(e.x), u1 = NC > 1 ? fast_exp2(e.y) : 0.f;
+                    const float2 e = unf2(add2(d[x], f2(kLift, kLift)));
+                    const uint64_t u = f2(fast_exp2(e.x), NC > 1 ? fast_exp2(e.y) : 0.f);
                     const float iv = ivs[hd_of(x)];
-                    l_run[x] = fma2(f2(u0, u1), f2(iv, iv), l_run[x]);
+                    l_run[x] = fma2(u, f2(iv, iv), l_run[x]);
                     uint32_t h1, h2, h3;
-                    split_weights(u0, u1, h1, h2, h3);
+                    const float2 w = unf2(mul2(u, f2(kUnlift, kUnlift)));
+                    split_weights(w.x, w.y, h1, h2, h3);
                     const int j = local(x), sh = (j & 2) * 8;
                     words[0][j >> 2] |= h1 << sh;
                     words[1][j >> 2] |= h2 << sh;
@@ -1199,9 +1210,10 @@ decode_fp8_merge_kernel(const DecodeParams p, int C) {
             const float pl = first_of_prev ? al[x] : bl[x];
             const float po = first_of_prev ? ao[x] : bo[x];
             const float M = fmaxf(pm, mm[x]);
-            const float a0 = fast_exp2(pm - M), a1 = fast_exp2(mm[x] - M);
-            den[x] = a0 * pl + a1 * ml[x];
-            num[x] = a0 * po + a1 * mo[x];
+            // 2^60 too large for the denominators (see kLift), which are made as much smaller first.
+            const float a0 = fast_exp2(pm - M + kLift), a1 = fast_exp2(mm[x] - M + kLift);
+            den[x] = a0 * (pl * kUnlift) + a1 * (ml[x] * kUnlift);
+            num[x] = (a0 * kUnlift) * po + (a1 * kUnlift) * mo[x];
         }
     } else {
         const int parts = c - ca + 1;
@@ -1227,9 +1239,9 @@ decode_fp8_merge_kernel(const DecodeParams p, int C) {
 #pragma unroll
             for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
             for (int i = lane; i < parts; i += 32) {
-                const float a = rescale(part_m[i][x], M);
-                part_m[i][x] = a;
-                sum = fmaf(a, part_l[i][x], sum);
+                const float a = fast_exp2(part_m[i][x] - M + kLift);      // (an empty part's -inf: 0)
+                part_m[i][x] = a * kUnlift;
+                sum = fmaf(a, part_l[i][x] * kUnlift, sum);
             }
             sum = warp_sum(sum);
             if (lane == 0) den_all[x] = sum;
