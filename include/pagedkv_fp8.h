@@ -20,8 +20,9 @@
  *   The tokens of a block and KV head share a scale, so they lie together (the
  *   bf16 cache keeps the heads of a token together instead).
  * Scales.  Positive, in [2^-64, 2^64]; the append writes powers of two, other
- *   sources may use any.  A scale outside sets PK_DEVERR_SCALE and its block
- *   is treated as one whose id is outside the pool (skipped).
+ *   sources may use any.  A scale outside sets PK_DEVERR_SCALE.  Attention and
+ *   gather then treat its block and head as one whose id is outside the pool
+ *   (skipped); the append gives its older rows up (below).
  */
 #ifndef PAGEDKV_FP8_H
 #define PAGEDKV_FP8_H
@@ -54,6 +55,10 @@ extern "C" {
  * rounded to nearest even, at most +-448; one that is not finite is stored as
  * NaN and left out of m2.  Rows behind the last new token are left as they
  * were.
+ *   Where the scale of older tokens is out of range, nothing says what their
+ * rows stood for: that head's older rows (of K or of V, whichever scale it is)
+ * become NaN, the block takes the scale that the new tokens need, and
+ * PK_DEVERR_SCALE is set.  What attends to those rows is NaN from then on.
  *
  *   q, k, v, q_out and their strides, inv_freq, rot_dim, interleaved, factor:
  *                 as for pk_rope_and_cache

@@ -129,7 +129,9 @@ def append_fp8(k, v, k_cache, v_cache, k_scales, v_scales, tables, seq_lens, cu_
                     scale = needed_scale(m2[h])
                     if off:
                         had = float(scales[block, h])
-                        if had >= scale:
+                        if not 2.0 ** -64 <= had <= 2.0 ** 64:
+                            cache[block, h, :off] = 0x7F       # what they stood for is not known
+                        elif had >= scale:
                             scale = had
                         else:
                             cache[block, h, :off] = e4m3_encode(e4m3_decode(cache[block, h, :off]) * (had / scale))

@@ -318,7 +318,12 @@ rope_and_cache_fp8_kernel(const AppendParams p) {
     float scale = pk::needed_scale(most);
     if (off0 > 0) {
         if (!pk::scale_ok(had)) {
+            // Nothing says what the older rows stood for.  They become NaN: under the
+            // new scale they would pass for values that nobody wrote.
             if (lane == 0) pk::set_error(p.err, PK_DEVERR_SCALE);
+            const uint32_t nan = 0x7f7f7f7fu;
+            for (int r = lrow; r < off0; r += kRows)
+                *reinterpret_cast<uint4 *>(rows + r * D + ju * 16) = make_uint4(nan, nan, nan, nan);
         } else if (had >= scale) {
             scale = had;
         } else {
