@@ -8,7 +8,7 @@ the pages' spelling of the same calls.
 from __future__ import annotations
 
 import ctypes
-from typing import Optional, Sequence, Tuple
+from typing import Optional, Sequence, Tuple, Union
 
 import torch
 
@@ -26,10 +26,13 @@ def _at(t: Optional[torch.Tensor]) -> int:
     return t.data_ptr() if t is not None else 0
 
 
-def _raw_stream(device: torch.device, stream=None) -> int:
+def _raw_stream(device: Union[torch.device, str, int], stream=None) -> int:
     """The cudaStream_t of ``stream``, or of the device's current stream.  (Asked
     for as a number: a Stream object costs 2 us, half a launch.)"""
-    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device.index)
+    if stream is not None:
+        return stream.cuda_stream
+    index = device if isinstance(device, int) else torch.device(device).index
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
 
 
 def _stream(device: torch.device, stream=None):
@@ -86,7 +89,7 @@ def new_workspace(nbytes: int, device) -> torch.Tensor:
     return torch.empty(max(1, nbytes), dtype=torch.uint8, device=device)
 
 
-def workspace_for(device: torch.device, nbytes: int, stream=None) -> Optional[torch.Tensor]:
+def workspace_for(device: Union[torch.device, str], nbytes: int, stream=None) -> Optional[torch.Tensor]:
     """A cached scratch buffer of at least ``nbytes`` for ``device`` and stream."""
     if nbytes == 0:
         return None
