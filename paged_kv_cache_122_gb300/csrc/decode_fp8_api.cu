@@ -6,6 +6,26 @@
 
 namespace {
 
+// max_seq_len == 0: every sequence is empty, so nothing of the cache is read and
+// the work is the rows' zeros.  CTA s checks sequence s as the attention kernel
+// does and writes its rows alone (not whole `out`: rows that no sequence owns, or
+// one whose rows are bad, stay as they are).
+__global__ void __launch_bounds__(128) empty_sequences_kernel(const pk::DecodeParams p) {
+    const int s = blockIdx.x;
+    int r0 = s, r1 = s + 1;
+    bool bad = p.seq_lens[s] != 0;
+    if (p.cu_q_lens) {
+        r0 = p.cu_q_lens[s];
+        r1 = p.cu_q_lens[s + 1];
+        bad = bad || r1 != r0;                      // more queries than tokens, or rows that run backwards
+    }
+    if (bad && threadIdx.x == 0) pk::set_error(p.err, PK_DEVERR_SEQ_LEN);
+    if (p.cu_q_lens && (r0 < 0 || r1 < r0 || r1 > p.total_q || r1 - r0 > p.q_len)) return;
+    const int64_t row = static_cast<int64_t>(p.num_heads) * p.head_dim * (p.out_fp32 ? 4 : 2) / 16;
+    uint4 *out = static_cast<uint4 *>(p.out) + r0 * row;
+    for (int64_t i = threadIdx.x; i < (r1 - r0) * row; i += blockDim.x) out[i] = make_uint4(0, 0, 0, 0);
+}
+
 bool group_supported(int G) { return G == 1 || G == 2 || G == 4 || G == 8 || G == 16; }
 
 // Both calls; cu_q_lens is NULL for one query token a sequence.
@@ -70,9 +90,13 @@ int attend(void *out, int out_dtype, const void *q, int total_q, const int32_t *
     p.err = pk::error_word_ptr();
     if (!p.err) return PK_ERR_NO_DEVICE;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (max_seq_len == 0) {        // every sequence is empty: the rows are zeros
-        const size_t bytes = static_cast<size_t>(total_q) * num_heads * head_dim * (p.out_fp32 ? 4 : 2);
-        return cudaMemsetAsync(out, 0, bytes, st) == cudaSuccess ? PK_OK : PK_ERR_CUDA;
+    if (max_seq_len == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(num_seqs));
+        cfg.blockDim = dim3(128);
+        cfg.stream = st;
+        return cudaLaunchKernelEx(&cfg, empty_sequences_kernel, static_cast<const pk::DecodeParams &>(p)) == cudaSuccess
+                   ? PK_OK : PK_ERR_CUDA;
     }
     return pk::launch_decode_fp8_tensor_core(p, st) == cudaSuccess ? PK_OK : PK_ERR_CUDA;
 }
