@@ -266,7 +266,8 @@ reshape_and_cache = pk_reshape_and_cache
 
 def _need_rows(t: torch.Tensor, name: str, device):
     """[tokens, heads, D] bf16 rows whose heads are dense; the tokens may be any
-    stride apart (a slice of a fused projection).  Returns the shape and that stride."""
+    stride apart (a slice of a fused projection).  Returns the shape and that stride,
+    for a single token (whose stride no address depends on) the smallest one."""
     if not (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.dim() == 3 and t.get_device() == device.index):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
@@ -281,7 +282,7 @@ def _need_rows(t: torch.Tensor, name: str, device):
     s0, s1, s2 = t.stride()
     if (s2 != 1 and D > 1) or (s1 != D and heads > 1):
         raise ValueError(f"the heads of a token of {name} must be contiguous")
-    return shape, s0 if T > 1 else max(s0, heads * D + -(heads * D) % 8)
+    return shape, s0 if T > 1 else heads * D + -(heads * D) % 8
 
 
 def _rope_args(q, k, v, inv_freq, q_out, dev, stream):
