@@ -31,6 +31,12 @@ def new_cache_fp8(num_blocks: int, num_kv_heads: int, block_size: int, head_dim:
     return caches[0], caches[1], scales[0], scales[1]
 
 
+def _bound(x) -> int:
+    """A length bound as the C calls take it: what does not fit 32 bits stays as far
+    out as it can be (ctypes would take it modulo 2^32)."""
+    return max(-1, min(int(x), 0x7FFFFFFF))
+
+
 def _need_cache(k_cache, v_cache, k_scales, v_scales, dev):
     tensor, index = torch.Tensor, dev.index
     if (isinstance(k_cache, tensor) and isinstance(v_cache, tensor) and isinstance(k_scales, tensor)
@@ -89,7 +95,7 @@ def pk_rope_and_cache_fp8(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.T
             raise ValueError("positions must have one entry per token")
     st = _on(dev, load().pk_rope_and_cache_fp8, _at(q_out), _at(q), k.data_ptr(), v.data_ptr(), *strides,
              k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
-             block_tables.data_ptr(), MB, seq_lens.data_ptr(), _at(cu_q_lens), int(max_q_len), N, _at(positions),
+             block_tables.data_ptr(), MB, seq_lens.data_ptr(), _at(cu_q_lens), _bound(max_q_len), N, _at(positions),
              _at(inv_freq), rot, int(interleaved), float(factor), T, H, Hkv, D, P, B, _raw_stream(dev, stream))
     check("pk_rope_and_cache_fp8", st)
     return q_out
@@ -146,7 +152,7 @@ def _attend(name, out, q, cu_q_lens, max_q_len, k_cache, v_cache, k_scales, v_sc
         raise TypeError("out must be bf16 or fp32")
     if given:
         _need(out, "out", out.dtype, 3, dev)
-    max_seq_len = MB * B if max_seq_len is None else int(max_seq_len)
+    max_seq_len = _bound(MB * B if max_seq_len is None else max_seq_len)
     nbytes = pk_decode_fp8_workspace_bytes(N, H, Hkv, D, max_seq_len)
     if workspace is None:
         workspace = _workspace(dev, nbytes, stream)
@@ -161,7 +167,7 @@ def _attend(name, out, q, cu_q_lens, max_q_len, k_cache, v_cache, k_scales, v_sc
         st = _on(dev, load().pk_paged_attention_decode_fp8, out.data_ptr(), dtype, q.data_ptr(), *tail)
     else:
         st = _on(dev, load().pk_paged_attention_multi_query_fp8, out.data_ptr(), dtype, q.data_ptr(), T,
-                 cu_q_lens.data_ptr(), int(max_q_len), *tail)
+                 cu_q_lens.data_ptr(), _bound(max_q_len), *tail)
     check(name, st)
     return out
 
@@ -222,7 +228,7 @@ def pk_gather_kv_fp8(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scales: tor
         max_seq_len = MB * B
     st = _on(dev, load().pk_gather_kv_fp8, out_k.data_ptr(), out_v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
              k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(), MB, seq_lens.data_ptr(),
-             cu_seq_lens.data_ptr(), rows, int(max_seq_len), N, Hkv, D, P, B, _raw_stream(dev, stream))
+             cu_seq_lens.data_ptr(), rows, _bound(max_seq_len), N, Hkv, D, P, B, _raw_stream(dev, stream))
     check("pk_gather_kv_fp8", st)
 
 
