@@ -49,7 +49,8 @@ extern "C" {
  * first row is new starts afresh, whatever its scale held.  m2 is the largest,
  * over the block's new tokens, of (x1^2 + x2^2) * factor^2 for the pairs of K
  * that are rotated -- a bound on both results that does not depend on the
- * position -- and of x^2 for every other element, in fp32.  If the scale
+ * position -- and of x^2 for every other element, in fp32 (what overflows counts
+ * as the largest fp32 number: the scale is then 2^56).  If the scale
  * grows, the older rows are rounded to it again (exact where they stay above
  * 2^-6 times the new scale).  A new value y is stored as y * (1 / scale)
  * rounded to nearest even, at most +-448; one that is not finite is stored as

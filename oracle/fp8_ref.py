@@ -83,18 +83,19 @@ def largest_square(x: np.ndarray, rot: int, interleaved: bool, factor: float) ->
 
     def square(u, v):
         ok = np.isfinite(u) & np.isfinite(v)
-        m = np.minimum(np.where(ok, u, 0.0) ** 2 + np.where(ok, v, 0.0) ** 2, top)
-        return m.astype(np.float32)
+        m = np.where(ok, u, 0.0) ** 2 + np.where(ok, v, 0.0) ** 2
+        with np.errstate(over="ignore"):
+            return m.astype(np.float32)                        # infinity where it overflows
     pairs = square(x1, x2).reshape(*x.shape[:2], -1)
     rest = square(x[..., rot:], np.zeros_like(x[..., rot:]))
     out = np.zeros(x.shape[1], dtype=np.float32)
     if pairs.size:
         f2 = np.float32(np.float32(factor) * np.float32(factor))
         with np.errstate(over="ignore"):
-            out = np.maximum(out, np.minimum(pairs.max(axis=(0, 2)) * f2, np.float32(top)))
+            out = np.maximum(out, pairs.max(axis=(0, 2)) * f2)
     if rest.size:
         out = np.maximum(out, rest.max(axis=(0, 2)))
-    return out
+    return np.minimum(out, np.float32(top))
 
 
 def needed_scale(m2: float) -> float:

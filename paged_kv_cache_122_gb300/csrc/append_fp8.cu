@@ -301,6 +301,7 @@ rope_and_cache_fp8_kernel(const AppendParams p) {
             if (!turned.x) plain = fmaxf(plain, largest_odd(a[it]));
             if (!turned.y) plain = fmaxf(plain, largest_odd(b[it]));
         }
+        if (most >= kLargest) plain = kLargest;    // overflowed: no factor brings that back
     } else {
         if (turned.x) {
 #pragma unroll
