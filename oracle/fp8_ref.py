@@ -181,6 +181,30 @@ def attention_fp8(q, k_cache, v_cache, k_scales, v_scales, tables, seq_lens, cu_
     return out, spread, scores
 
 
+def attention_floor(q, k_cache, v_cache, k_scales, v_scales, tables, seq_lens, cu_q_lens, scale: float) -> np.ndarray:
+    """[total_q, H, D]: the largest p_j vs_j of a row times sum_j |stored v_j|.
+    A weight p_j vs_j is kept to 2^-24 of the row's largest one beside its relative
+    error, so 2^-24 of this is what the row's small weights can lose together:
+    attention_bound's last term, with ``length`` 1 and this as ``largest_v``.  (That
+    term as such takes p_j vs_j <= largest vs, which a long context is far below.)"""
+    q = np.asarray(q, dtype=np.float64)
+    out = np.zeros_like(q)
+    for s, L in enumerate(seq_lens):
+        r0, r1 = int(cu_q_lens[s]), int(cu_q_lens[s + 1])
+        K, ones = rows_fp8(k_cache, k_scales, tables[s], L), np.ones_like(v_scales)
+        V = np.abs(rows_fp8(v_cache, ones, tables[s], L))
+        B = k_cache.shape[2]
+        G = q.shape[1] // K.shape[1]
+        vs = np.repeat(np.stack([v_scales[int(b)].astype(np.float64) for b in tables[s][:-(-int(L) // B)]]), B, axis=0) if L else None
+        for r in range(r0, r1):
+            n = int(L) - (r1 - r0) + (r - r0) + 1
+            for h in range(q.shape[1]) if n > 0 else ():
+                z = scale * (K[:n, h // G] @ q[r, h])
+                p = np.exp(z - z.max())
+                out[r, h] = np.max(p * vs[:n, h // G]) / p.sum() * V[:n, h // G].sum(axis=0)
+    return out
+
+
 def attention_bound(out, spread, scores: float, length: int, largest_v: float, bf16_out: bool) -> np.ndarray:
     """How far the kernel's result may be from ``out``.  A weight is used to
     2^-9 (its three e4m3 terms) + 2^-11 (fp16 before them) + 2^-18 (exponential
