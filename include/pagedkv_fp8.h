@@ -117,6 +117,31 @@ int pk_paged_attention_decode_fp8(void *out, int out_dtype, const void *q, const
                                   pk_stream_t stream);
 
 /*
+ * Self-tests of pk_paged_attention_decode_fp8, as pk_selftest_decode_wait_timeout
+ * and pk_selftest_decode_stale_lengths are for the bf16 call: the kernel's bounded
+ * waits run out where CTA 0's producers stop before tile `stall_tile` of its range
+ * (>= 1; wait_limit_us in [100, 1000000]), and its first plan comes from the device
+ * array `stale_seq_lens` (unused where the kernel keeps no lengths in shared memory:
+ * above 256 sequences, 2,048 with 16 heads per KV head, or 8 at head dim 64 with an
+ * even number of KV heads).  The other arguments are those of
+ * pk_paged_attention_decode_fp8.
+ */
+int pk_selftest_decode_fp8_wait_timeout(void *out, int out_dtype, const void *q, const void *k_cache,
+                                        const void *v_cache, const float *k_scales, const float *v_scales,
+                                        const int32_t *block_tables, int max_blocks_per_seq,
+                                        const int32_t *seq_lens, int max_seq_len, int num_seqs, int num_heads,
+                                        int num_kv_heads, int head_dim, int num_blocks, int block_size,
+                                        float scale, void *workspace, size_t workspace_bytes, int stall_tile,
+                                        unsigned int wait_limit_us, pk_stream_t stream);
+int pk_selftest_decode_fp8_stale_lengths(void *out, int out_dtype, const void *q, const void *k_cache,
+                                         const void *v_cache, const float *k_scales, const float *v_scales,
+                                         const int32_t *block_tables, int max_blocks_per_seq,
+                                         const int32_t *seq_lens, int max_seq_len, int num_seqs, int num_heads,
+                                         int num_kv_heads, int head_dim, int num_blocks, int block_size,
+                                         float scale, const int32_t *stale_seq_lens, void *workspace,
+                                         size_t workspace_bytes, pk_stream_t stream);
+
+/*
  * Attention of a FEW new tokens per sequence over the 8-bit paged cache,
  * causal among them (verification of drafted tokens), as
  * pk_paged_attention_multi_query defines it: sequence s owns query rows

@@ -52,6 +52,8 @@ from .fp8 import (  # noqa: F401
     pk_paged_attention_decode_fp8,
     pk_paged_attention_multi_query_fp8,
     pk_rope_and_cache_fp8,
+    pk_selftest_decode_fp8_stale_lengths,
+    pk_selftest_decode_fp8_wait_timeout,
     pk_swap_blocks_fp8,
     rope_and_cache_fp8,
     swap_blocks_fp8,

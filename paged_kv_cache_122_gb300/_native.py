@@ -85,6 +85,14 @@ SIGNATURES = {
         c_void_p, c_int, c_void_p, c_int,                        # block_tables, max_blocks_per_seq, seq_lens, max_seq_len
         c_int, c_int, c_int, c_int, c_int, c_int, c_float,       # seqs, heads, kv_heads, head_dim, blocks, block_size, scale
         c_void_p, c_size_t, c_void_p]),                          # workspace, workspace_bytes, stream
+    "pk_selftest_decode_fp8_wait_timeout": (c_int, [
+        c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_void_p, c_int,
+        c_int, c_int, c_int, c_int, c_int, c_int, c_float,
+        c_void_p, c_size_t, c_int, c_uint, c_void_p]),           # workspace, bytes, stall_tile, wait_limit_us, stream
+    "pk_selftest_decode_fp8_stale_lengths": (c_int, [
+        c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_void_p, c_int,
+        c_int, c_int, c_int, c_int, c_int, c_int, c_float,
+        c_void_p, c_void_p, c_size_t, c_void_p]),                # stale_seq_lens, workspace, bytes, stream
     "pk_paged_attention_multi_query_fp8": (c_int, [
         c_void_p, c_int, c_void_p, c_int, c_void_p, c_int,       # out, out_dtype, q, total_q, cu_q_lens, max_q_len
         c_void_p, c_void_p, c_void_p, c_void_p,

@@ -28,12 +28,15 @@ __global__ void __launch_bounds__(128) empty_sequences_kernel(const pk::DecodePa
 
 bool group_supported(int G) { return G == 1 || G == 2 || G == 4 || G == 8 || G == 16; }
 
-// Both calls; cu_q_lens is NULL for one query token a sequence.
+// Both calls; cu_q_lens is NULL for one query token a sequence.  `stall_tile` and
+// `wait_limit_ns` serve the self-test of the bounded waits (0 = off / the default
+// limit), `lens_ahead` that of the second look at the lengths (NULL = off).
 int attend(void *out, int out_dtype, const void *q, int total_q, const int32_t *cu_q_lens, int max_q_len,
            const void *k_cache, const void *v_cache, const float *k_scales, const float *v_scales,
            const int32_t *block_tables, int max_blocks_per_seq, const int32_t *seq_lens, int max_seq_len, int num_seqs,
            int num_heads, int num_kv_heads, int head_dim, int num_blocks, int block_size, float scale, void *workspace,
-           size_t workspace_bytes, pk_stream_t stream, bool multi) {
+           size_t workspace_bytes, pk_stream_t stream, bool multi, int stall_tile = 0, uint64_t wait_limit_ns = 0,
+           const int32_t *lens_ahead = nullptr) {
     if (num_seqs < 0 || num_heads <= 0 || num_kv_heads <= 0 || num_blocks < 0 || max_blocks_per_seq < 0 ||
         max_seq_len < 0 || block_size <= 0 || total_q < 0 || max_q_len < 0)
         return PK_ERR_SHAPE;
@@ -82,6 +85,9 @@ int attend(void *out, int out_dtype, const void *q, int total_q, const int32_t *
     p.cu_q_lens = cu_q_lens;
     p.q_len = q_len;
     p.total_q = total_q;
+    p.stall_tile = stall_tile;
+    p.wait_limit_ns = wait_limit_ns;
+    p.lens_ahead = lens_ahead;
     if (max_seq_len > 128) {       // a longer sequence may span several CTAs: its parts need slots
         if (!workspace || workspace_bytes < pk::tc_workspace_bytes()) return PK_ERR_WORKSPACE;
         if (!pk::aligned16(workspace)) return PK_ERR_ALIGNMENT;
@@ -121,6 +127,33 @@ extern "C" int pk_paged_attention_decode_fp8(void *out, int out_dtype, const voi
     return attend(out, out_dtype, q, num_seqs, nullptr, 1, k_cache, v_cache, k_scales, v_scales, block_tables,
                   max_blocks_per_seq, seq_lens, max_seq_len, num_seqs, num_heads, num_kv_heads, head_dim, num_blocks,
                   block_size, scale, workspace, workspace_bytes, stream, false);
+}
+
+extern "C" int pk_selftest_decode_fp8_wait_timeout(void *out, int out_dtype, const void *q, const void *k_cache,
+                                                   const void *v_cache, const float *k_scales, const float *v_scales,
+                                                   const int32_t *block_tables, int max_blocks_per_seq,
+                                                   const int32_t *seq_lens, int max_seq_len, int num_seqs, int num_heads,
+                                                   int num_kv_heads, int head_dim, int num_blocks, int block_size,
+                                                   float scale, void *workspace, size_t workspace_bytes, int stall_tile,
+                                                   unsigned int wait_limit_us, pk_stream_t stream) {
+    if (stall_tile < 1 || wait_limit_us < 100 || wait_limit_us > 1000000) return PK_ERR_SHAPE;
+    return attend(out, out_dtype, q, num_seqs, nullptr, 1, k_cache, v_cache, k_scales, v_scales, block_tables,
+                  max_blocks_per_seq, seq_lens, max_seq_len, num_seqs, num_heads, num_kv_heads, head_dim, num_blocks,
+                  block_size, scale, workspace, workspace_bytes, stream, false, stall_tile,
+                  static_cast<uint64_t>(wait_limit_us) * 1000u);
+}
+
+extern "C" int pk_selftest_decode_fp8_stale_lengths(void *out, int out_dtype, const void *q, const void *k_cache,
+                                                    const void *v_cache, const float *k_scales, const float *v_scales,
+                                                    const int32_t *block_tables, int max_blocks_per_seq,
+                                                    const int32_t *seq_lens, int max_seq_len, int num_seqs, int num_heads,
+                                                    int num_kv_heads, int head_dim, int num_blocks, int block_size,
+                                                    float scale, const int32_t *stale_seq_lens, void *workspace,
+                                                    size_t workspace_bytes, pk_stream_t stream) {
+    if (!stale_seq_lens) return PK_ERR_NULL;
+    return attend(out, out_dtype, q, num_seqs, nullptr, 1, k_cache, v_cache, k_scales, v_scales, block_tables,
+                  max_blocks_per_seq, seq_lens, max_seq_len, num_seqs, num_heads, num_kv_heads, head_dim, num_blocks,
+                  block_size, scale, workspace, workspace_bytes, stream, false, 0, 0, stale_seq_lens);
 }
 
 extern "C" int pk_paged_attention_multi_query_fp8(void *out, int out_dtype, const void *q, int total_q,

@@ -323,7 +323,7 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     const int cap = p.max_seq_len;                    // at most max_blocks_per_seq * B (checked on the host)
     const int Gq = H / p.num_kv_heads, lgG = __ffs(Gq) - 1;     // query heads per KV head (a power of two)
     Slot *slots = static_cast<Slot *>(p.tc_slots);
-    const uint64_t lim = kWaitLimitNs;
+    const uint64_t lim = p.wait_limit_ns ? p.wait_limit_ns : kWaitLimitNs;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
@@ -378,8 +378,9 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     };
     bool ahead = cached;
     if (cached) {
+        const int32_t *first_read = p.lens_ahead ? p.lens_ahead : p.seq_lens;
 #pragma unroll 1
-        for (int s = threadIdx.x; s < N; s += kThreads) misc->lens[s] = ld_cg(p.seq_lens + s);
+        for (int s = threadIdx.x; s < N; s += kThreads) misc->lens[s] = ld_cg(first_read + s);
         __syncthreads();
     } else {
         wait_prev();
@@ -458,6 +459,7 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         int qr_of = -1;
         const int MB = p.max_blocks_per_seq;
         int issued = 0;
+        bool stalled = false;
         // Table entries (a lane per page) are read kAhead tiles before their tile:
         // a tile's bytes take less time than one read does, so one tile ahead would
         // bound the copies by that read's latency.  They go through shared memory
@@ -478,6 +480,12 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         for (int i = 0; i < kAhead; ++i) fetch_tile(i);
 #pragma unroll 1
         for (int i = 0; i < n_tiles; ++i) {
+            // Self-test: CTA 0 stops issuing copies, so the barriers of this tile
+            // never complete.
+            if (p.stall_tile > 0 && c == 0 && i == p.stall_tile) {
+                stalled = true;
+                break;
+            }
             const int st = i % kStages;
             fetch_tile(i + kAhead);
             cp_async_wait_group<kAhead>();
@@ -541,8 +549,9 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             w.next(lens);
         }
         cp_async_wait_all();
-        // On abort, let this warp's copies land before the CTA can exit.
-        if (misc->abort && lane == 0) {
+        // On abort (or a self-test's stall), let this warp's copies land before the
+        // CTA can exit.
+        if ((misc->abort || stalled) && lane == 0) {
             for (int i = max(0, issued - kStages); i < issued; ++i) {
                 if (do_k) wait_for(smem_u32(&misc->full[i % kStages]), (i / kStages) & 1, &misc->never, lim);
                 if (do_v) wait_for(smem_u32(&misc->vfull[i % kStages]), (i / kStages) & 1, &misc->never, lim);

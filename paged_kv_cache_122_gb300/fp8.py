@@ -186,6 +186,37 @@ def pk_paged_attention_decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cach
 paged_attention_decode_fp8 = pk_paged_attention_decode_fp8
 
 
+def _selftest_args(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, seq_lens, scale, max_seq_len):
+    N, H, D = q.shape
+    P, Hkv, B, _ = k_cache.shape
+    return (out.data_ptr(), _native.PK_FP32 if out.dtype == torch.float32 else _native.PK_BF16, q.data_ptr(),
+            k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(),
+            block_tables.shape[1], seq_lens.data_ptr(), _bound(max_seq_len), N, H, Hkv, D, P, B, float(scale))
+
+
+def pk_selftest_decode_fp8_wait_timeout(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                        k_scales: torch.Tensor, v_scales: torch.Tensor, block_tables: torch.Tensor,
+                                        seq_lens: torch.Tensor, scale: float, max_seq_len: int, workspace: torch.Tensor,
+                                        stall_tile: int, wait_limit_us: int, stream=None) -> int:
+    """Self-test of the bounded waits (see the C header): a decode call whose CTA 0
+    stops issuing copies at ``stall_tile``, so that its waits give up after
+    ``wait_limit_us``.  Returns the call's status."""
+    return int(_on(q.device, load().pk_selftest_decode_fp8_wait_timeout,
+                   *_selftest_args(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, seq_lens, scale, max_seq_len),
+                   workspace.data_ptr(), workspace.nbytes, int(stall_tile), int(wait_limit_us), _raw_stream(q.device, stream)))
+
+
+def pk_selftest_decode_fp8_stale_lengths(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                         k_scales: torch.Tensor, v_scales: torch.Tensor, block_tables: torch.Tensor,
+                                         seq_lens: torch.Tensor, scale: float, max_seq_len: int,
+                                         stale_seq_lens: torch.Tensor, workspace: torch.Tensor, stream=None) -> int:
+    """Self-test of the second look at the lengths (see the C header): a decode call
+    that plans first from ``stale_seq_lens``.  Returns the call's status."""
+    return int(_on(q.device, load().pk_selftest_decode_fp8_stale_lengths,
+                   *_selftest_args(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, seq_lens, scale, max_seq_len),
+                   stale_seq_lens.data_ptr(), workspace.data_ptr(), workspace.nbytes, _raw_stream(q.device, stream)))
+
+
 def pk_paged_attention_multi_query_fp8(q: torch.Tensor, cu_q_lens: torch.Tensor, max_q_len: int,
                                        k_cache: torch.Tensor, v_cache: torch.Tensor, k_scales: torch.Tensor,
                                        v_scales: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor,
