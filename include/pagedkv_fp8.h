@@ -103,9 +103,10 @@ size_t pk_decode_fp8_workspace_bytes(int num_seqs, int num_heads, int num_kv_hea
  * with k_j, v_j the e4m3 rows of token j and KV head h / G and ks_j, vs_j the
  * scales of its block and that head.  Everything else -- arguments, table
  * walk, lengths, workspace, errors, determinism -- is as for
- * pk_paged_attention_decode.  Queries are bf16 and used to at least 13
- * significant bits of their row's largest; weights are used to at least 9
- * bits.  The partial results of split sequences and the denominators are fp32.
+ * pk_paged_attention_decode.  Queries are bf16, used exactly down to 2^-13 of
+ * their row's largest and to 2^-22 of it below.  Numerators take a weight (times
+ * its value scale) to 2^-11 of itself and to 2^-24 of the row's largest one;
+ * denominators and the partial results of split sequences are fp32.
  * A NaN in a key or a value of an attended token shows in its output.
  */
 int pk_paged_attention_decode_fp8(void *out, int out_dtype, const void *q, const void *k_cache,

@@ -205,12 +205,14 @@ def attention_floor(q, k_cache, v_cache, k_scales, v_scales, tables, seq_lens, c
     return out
 
 
-def attention_bound(out, spread, scores: float, length: int, largest_v: float, bf16_out: bool) -> np.ndarray:
+def attention_bound(out, spread, scores: float, length: int, largest_v: float, bf16_out: bool,
+                    weight_error: float = 2.0 ** -9 + 2.0 ** -11) -> np.ndarray:
     """How far the kernel's result may be from ``out``.  A weight is used to
-    2^-9 (its three e4m3 terms) + 2^-11 (fp16 before them) + 2^-18 (exponential
-    and 32-bit arithmetic) of itself and to 2^-24 of the largest one; a score is
-    off by at most 2^-20 of sum |q||k| (query terms to 2^-22 of the row's
-    largest, 32-bit sums), which moves numerator and denominator alike."""
-    weight = 2.0 ** -9 + 2.0 ** -11 + 2.0 ** -18 + 2.0 * math.expm1(scores * 2.0 ** -20)
+    ``weight_error`` + 2^-18 (exponential and 32-bit arithmetic) of itself and to
+    2^-24 of the largest one; a score is off by at most 2^-20 of sum |q||k| (query
+    terms to 2^-22 of the row's largest, 32-bit sums), which moves numerator and
+    denominator alike.  The kernel's weights are to 2^-11 (fp16, which three e5m2
+    terms hold exactly); the default also covers three e4m3 terms, 2^-9 more."""
+    weight = weight_error + 2.0 ** -18 + 2.0 * math.expm1(scores * 2.0 ** -20)
     tol = weight * (spread + np.abs(out)) + length * 2.0 ** -24 * largest_v
     return tol + (2.0 ** -8 * (np.abs(out) + tol) if bf16_out else 2.0 ** -23 * np.abs(out))

@@ -5,13 +5,17 @@
 //   t_j = s_j log2(e) + log2(vs_j),
 // k_j and v_j the stored e4m3 rows.  Both contractions run on kind::f8f6f4
 // MMAs straight from the pages as TMA lands them: nothing widens K or V.  The
-// other operands are split into e4m3 terms that each take columns of their own:
-//   q * 2^k = h + l / 32, 2^k bringing the row's largest to [128, 256): two
+// other operands are split into 8-bit terms that each take columns of their own:
+//   q * 2^k = h + l / 32, 2^k bringing the row's largest to [128, 256): two e4m3
 //     terms hold a bf16 value exactly down to 2^-13 of the row's largest, and
 //     what is smaller to 2^-22 of it.
-//   u = 2^(t - m) = h1 + h2 / 32 + h3 / 2^16, u <= 256: to 2^-9 of u (2^-11
-//     below 4), and nothing above 2^-25 is lost, of a largest weight that is 1
-//     or more (m moves when a u exceeds 2^8).  bf16 weights are to 2^-9 too.
+//   u = 2^(t - m) = h1 + h2 + h3, e5m2 terms of u rounded to fp16, u <= 2^15: three
+//     hold an fp16 value exactly down to 2^-6, so u to 2^-11 of itself, and below
+//     to 2^-17, which is 2^-24 of the largest weight: that is 2^7 or more (m moves
+//     when a u exceeds 2^15).  bf16 weights are to 2^-8.  e4m3 terms with scales
+//     between them have a bit more each but 2^-20 of the largest weight for small
+//     ones: a tail of 16,000 tokens 2^-16 below one peak was off by 6 % (a tail's
+//     weights are alike, so their rounding does not average out).
 // The extra columns cost MMA time only: the tensor pipe is active 7 % of
 // the time.
 //
@@ -68,10 +72,10 @@ constexpr int kAhead = 4;                                    // tiles whose tabl
 constexpr int kScores = 3;                                   // score buffers: two tiles ahead of the weights
 constexpr int kQRing = 6;                                    // query scales kept, by segment
 constexpr uint64_t kWaitLimitNs = 1000000000ull;             // 1 s: far beyond any legal wait
-constexpr float kLevel2 = 1.f / 32, kLevel3 = 1.f / 65536;   // what the terms of u stand for
-constexpr float kHeadroom = 8.f;                             // u <= 2^8: e4m3 holds 256
+constexpr float kLevel2 = 1.f / 32;                          // what the second term of a query stands for
+constexpr float kHeadroom = 15.f;                            // u <= 2^15: e5m2 holds 57344
 constexpr float kNoReference = 3.0e38f;                      // minus the reference of a segment's start
-constexpr float kStart = 0.f;                                // the largest u when the reference moves: 2^0
+constexpr float kStart = 7.f;                                // the largest u when the reference moves: 2^7
 // The denominator adds (u * 2^60) * (2^-60 / vs).  Accepted scales span 2^128, so at
 // equal scores u can be 2^-128 where 1 / vs makes it a whole share, and 2^x is 0
 // below 2^-126.  With 2^60 only a u below 2^-186 is lost, a share of at most 2^-122
@@ -82,12 +86,14 @@ constexpr float kLift = 60.f, kUnlift = 0x1p-60f;
 
 constexpr uint32_t kLayoutSw64 = 4;
 
-// Instruction descriptor for kind::f8f6f4: fp32 accumulator, e4m3 A and B.
-__host__ __device__ constexpr uint32_t idesc_e4m3(uint32_t m, uint32_t n, uint32_t a_mn_major, uint32_t b_mn_major) {
-    return (1u << 4) | (a_mn_major << 15) | (b_mn_major << 16) | ((n >> 3) << 17) | ((m >> 4) << 24);
+// Instruction descriptor for kind::f8f6f4: fp32 accumulator, A of e4m3, B of e4m3 or e5m2.
+__host__ __device__ constexpr uint32_t idesc_fp8(uint32_t m, uint32_t n, uint32_t a_mn_major, uint32_t b_mn_major,
+                                                 bool b_e5m2) {
+    return (1u << 4) | ((b_e5m2 ? 1u : 0u) << 10) | (a_mn_major << 15) | (b_mn_major << 16) | ((n >> 3) << 17) |
+           ((m >> 4) << 24);
 }
 
-SM100_DEV void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+SM100_DEV void mma_fp8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
@@ -189,27 +195,25 @@ SM100_DEV void tmem_wait_ld(uint32_t (&r)[N]) {
                      ::"memory");
 }
 
-// The three terms of two weights u <= 256, two e4m3 bytes each.  u is first
-// rounded to fp16 (11 bits; steps of 2^-24 at the bottom), in which the
-// remainders after each term are exact.  The first, at most 8, is scaled by 32;
-// the second by 2048, and beyond 448 / 2048 its term stops at 448.
+// The three terms of two weights u <= 2^15, two e5m2 bytes each.  u is first
+// rounded to fp16 (11 bits), in which the remainders after each term are exact:
+// each takes off three bits and leaves half a step with its sign, so nothing is
+// left after the third but below e5m2's smallest steps of 2^-16.
 SM100_DEV void split_weights(float u0, float u1, uint32_t &h1, uint32_t &h2, uint32_t &h3) {
     asm("{\n\t.reg .b32 u, b, r;\n\t.reg .b16 a;\n\t"
         "cvt.rn.f16x2.f32 u, %4, %3;\n\t"
-        "cvt.rn.satfinite.e4m3x2.f16x2 a, u;\n\t"
+        "cvt.rn.satfinite.e5m2x2.f16x2 a, u;\n\t"
         "cvt.u32.u16 %0, a;\n\t"
-        "cvt.rn.f16x2.e4m3x2 b, a;\n\t"
+        "cvt.rn.f16x2.e5m2x2 b, a;\n\t"
         "sub.rn.f16x2 r, u, b;\n\t"
-        "mul.rn.f16x2 r, r, %5;\n\t"
-        "cvt.rn.satfinite.e4m3x2.f16x2 a, r;\n\t"
+        "cvt.rn.satfinite.e5m2x2.f16x2 a, r;\n\t"
         "cvt.u32.u16 %1, a;\n\t"
-        "cvt.rn.f16x2.e4m3x2 b, a;\n\t"
+        "cvt.rn.f16x2.e5m2x2 b, a;\n\t"
         "sub.rn.f16x2 r, r, b;\n\t"
-        "mul.rn.f16x2 r, r, %6;\n\t"
-        "cvt.rn.satfinite.e4m3x2.f16x2 a, r;\n\t"
+        "cvt.rn.satfinite.e5m2x2.f16x2 a, r;\n\t"
         "cvt.u32.u16 %2, a;\n\t}"
         : "=r"(h1), "=r"(h2), "=r"(h3)
-        : "f"(u0), "f"(u1), "r"(0x50005000u), "r"(0x68006800u));
+        : "f"(u0), "f"(u1));
 }
 
 // The two terms of two query values below 256, which fp16 holds exactly down
@@ -301,8 +305,8 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     constexpr int CW = C_::CW, HL = C_::HL, NS = C_::NS, PW = C_::PW, PC = C_::PC, NP = C_::NP;
     constexpr uint32_t kLayout = D == 128 ? kLayoutSw128 : kLayoutSw64;
     constexpr uint32_t kAtom = 8 * D;                 // eight rows: the swizzle's atom
-    constexpr uint32_t kIdescQK = idesc_e4m3(kTile, NS, 0, 0);   // A = K (K-major), B = Q (K-major)
-    constexpr uint32_t kIdescPV = idesc_e4m3(128, NP, 1, 1);     // A = V^T (MN-major), B = P^T (MN-major)
+    constexpr uint32_t kIdescQK = idesc_fp8(kTile, NS, 0, 0, false);   // A = K (K-major), B = Q (K-major)
+    constexpr uint32_t kIdescPV = idesc_fp8(128, NP, 1, 1, true);      // A = V^T (MN-major), B = P^T (MN-major)
     constexpr int64_t kSegCost = seg_cost<HP * NC, HP>();
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
@@ -577,7 +581,7 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
 #pragma unroll
                 for (int kk = 0; kk < kTile / 32; ++kk) {
                     // Tokens 32 kk .. 32 kk + 31: four 8-row atoms of V.
-                    mma_e4m3(tmem + C_::tO + (sg & 1) * NP, v_desc + ((st * C_::StageBytes + kk * 4 * kAtom) >> 4),
+                    mma_fp8(tmem + C_::tO + (sg & 1) * NP, v_desc + ((st * C_::StageBytes + kk * 4 * kAtom) >> 4),
                              p_desc + ((pb * C_::PBytes + kk * 32 * NP) >> 4), kIdescPV, (first && kk == 0) ? 0u : 1u);
                 }
                 mma_commit(smem_u32(&misc->o_full[pb]));
@@ -593,7 +597,7 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 for (int hd = 0; hd < HP; ++hd) {
 #pragma unroll
                     for (int kk = 0; kk < D / 32; ++kk) {
-                        mma_e4m3(tmem + C_::tS + sb * C_::SCols + hd * NS,
+                        mma_fp8(tmem + C_::tS + sb * C_::SCols + hd * NS,
                                  k_desc + ((st * C_::StageBytes + hd * C_::HeadBytes + kk * 32) >> 4),
                                  q_desc + ((qb * C_::QBufBytes + hd * C_::QHeadBytes + kk * 32) >> 4), kIdescQK, kk > 0 ? 1u : 0u);
                     }
@@ -794,7 +798,7 @@ decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 tmem_ld<kGW>(oaddr + PW, o2);
                 tmem_ld<kGW>(oaddr + 2 * PW, o3);
 #pragma unroll
-                for (int j = 0; j < kGW; ++j) ov[j] = fmaf(o3[j], kLevel3, fmaf(o2[j], kLevel2, o1[j]));
+                for (int j = 0; j < kGW; ++j) ov[j] = (o3[j] + o2[j]) + o1[j];
             }
             tc_fence_before();
             __syncwarp();

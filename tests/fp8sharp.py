@@ -44,11 +44,11 @@ def sharp_case(seed, lens, qlens, G, Hkv, D, B):
     return c
 
 
-def reference(c):
+def reference(c, **kw):
     """(result, how far off it may be in fp32)."""
     args = (c["q64"], c["kb"], c["vb"], c["ks"], c["vs"], c["bt"], c["lens"], c["cu"], c["scale"])
     ref, spread, scores = R.attention_fp8(*args)
-    return ref, R.attention_bound(ref, spread, scores, 1, R.attention_floor(*args), False)
+    return ref, R.attention_bound(ref, spread, scores, 1, R.attention_floor(*args), False, **kw)
 
 
 def check_sharp(c, out, what=""):
