@@ -76,7 +76,10 @@ extern "C" {
  * tokens than tokens or than max_q_len, or whose rows are not within the
  * num_tokens given sets PK_DEVERR_SEQ_LEN, and nothing of it is written.  A
  * block id outside the pool sets PK_DEVERR_BLOCK_ID: that block's K and V are
- * not written.  num_seqs <= 65535.
+ * not written.  num_seqs <= 65535.  Rows of q_out that no sequence owns are left
+ * as they were: a batch of fixed size is padded with sequences of length 0 and no
+ * rows (cu_q_lens stays at its last value).  Where cu_q_lens runs backwards, tokens
+ * of later sequences may be left out too.
  */
 int pk_rope_and_cache_fp8(void *q_out, const void *q, const void *k, const void *v, int64_t q_out_stride,
                           int64_t q_stride, int64_t k_stride, int64_t v_stride, void *k_cache,
@@ -179,7 +182,8 @@ int pk_paged_attention_multi_query_fp8(void *out, int out_dtype, const void *q, 
  *                 PK_DEVERR_SEQ_LEN and is left out
  *   max_seq_len   host-side bound of seq_lens; a longer one sets
  *                 PK_DEVERR_SEQ_LEN and its first max_seq_len rows are written
- * Rows of a block whose id or scale is bad are left unwritten.
+ * Rows of a block whose id or scale is bad are left unwritten.  max_seq_len = 0 or
+ * out_rows = 0 is a no-op.
  */
 int pk_gather_kv_fp8(void *out_k, void *out_v, const void *k_cache, const void *v_cache,
                      const float *k_scales, const float *v_scales, const int32_t *block_tables,

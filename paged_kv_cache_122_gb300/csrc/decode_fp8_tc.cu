@@ -32,9 +32,10 @@
 //     cache a quarter of the time at 100 KB, 2 % at 65 KB;
 //   - whole warps wait, so that none runs on split.
 // Measured (back to back, 8 KV heads, head dim 128, block 16; 6,787 GB/s is a
-// copy): 8 sequences of 32k to 128k tokens 171-175 us at 4 query heads a KV
-// head (1.15 GB, 0.97-0.99 of the copy), 256 sequences of 16 to 8,192 tokens 88
-// us at 8 (0.52 GB, 0.87), 16 query columns 194 and 130 us.  The first form
+// copy): 8 sequences of 32k to 128k tokens 172 us at 4 query heads a KV head
+// (1.15 GB, 0.99 of the copy), 256 sequences of 16 to 8,192 tokens 88 us at 8
+// (0.52 GB, 0.87), 16 query columns 197 and 132 us; 512 tokens each of 256
+// sequences 49 us, of 257 (no lengths in shared memory) 51.  The first form
 // took 307 and 151 us, one CTA an SM with table entries ahead 245 and 145.
 //
 // Per 128-token tile, inside a CTA:
@@ -79,9 +80,10 @@ constexpr float kStart = 7.f;                                // the largest u wh
 // The denominator adds (u * 2^60) * (2^-60 / vs).  Accepted scales span 2^128, so at
 // equal scores u can be 2^-128 where 1 / vs makes it a whole share, and 2^x is 0
 // below 2^-126.  With 2^60 only a u below 2^-186 is lost, a share of at most 2^-122
-// where the token of the largest u alone adds 2^-64; both factors are normal numbers.
+// where the token of the largest u alone adds 2^-57; both factors are normal numbers.
 // (Added to the exponent after the reference is taken off: scores of 2^30 would
-// swallow it.)  Costs two packed instructions a pair of columns.
+// swallow it.)  Costs two packed instructions a pair of columns, 1 to 2 % at 16
+// columns; a second case for small scales, behind a vote, cost 3 %.
 constexpr float kLift = 60.f, kUnlift = 0x1p-60f;
 
 constexpr uint32_t kLayoutSw64 = 4;
@@ -242,7 +244,9 @@ SM100_DEV float fast_rcp(float v) {
 // read-out, first reference and queries) by sweeps over 256 sequences of 16 to
 // 8,192 tokens.  Head dim 128, 16 columns: 132 us at 780, 130 at 500 to 680, 134
 // at 300; 8 columns: 88 at 80 to 160, 89 at 240.  Head pairs, 16 columns: 74 at
-// 780, 69 at 300 to 500; 8 columns: 54.7 at 80, 56 at 160.
+// 780, 69 at 300 to 500; 8 columns: 54.7 at 80, 56 at 160.  (Swept before the
+// denominators reached over the whole scale range; with these weights 132, 88, 70
+// and 56 us now.)
 constexpr int64_t kTileCost = 400;
 constexpr int kTokCost = 1;
 template <int NUSED, int HP>
