@@ -83,6 +83,8 @@ enum pk_dtype { PK_BF16 = 0, PK_FP32 = 1 };
                                     barriers (never expected; the results are invalid) */
 #define PK_DEVERR_SCALE    0x40u /* a scale of the 8-bit cache (pagedkv_fp8.h) is outside
                                     [2^-64, 2^64] or not a number */
+#define PK_DEVERR_DRAFT    0x80u /* a list of accepted drafts (pagedkv_tree.h) is not strictly
+                                    increasing or does not fit its tree */
 #define PK_DEVERR_POINTER  0x20u /* a per-layer pointer of a *_layers call is NULL or not
                                     16-byte aligned (that layer was skipped) */
 

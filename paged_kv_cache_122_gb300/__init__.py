@@ -8,7 +8,9 @@ The calls follow the pages' statement of the problem:
 
 Next to them: ``rope_and_cache`` (rotary positions and the append in one pass) and
 the 8-bit cache (``fp8``: e4m3 values with a scale per block and KV head) with its
-own append, attention, gather and block copies (``*_fp8``).
+own append, attention, gather and block copies (``*_fp8``).  ``paged_attention_tree``,
+``accept_tree`` and ``keep_tokens`` verify trees of drafted tokens;
+``paged_attention_cross`` attends to an encoder's states.
 
 All work runs in the library's sm_103a kernels (``csrc/``); PyTorch supplies
 device memory and streams.  ``BlockManager`` is the library's host-side C++
@@ -57,6 +59,19 @@ from .fp8 import (  # noqa: F401
     pk_swap_blocks_fp8,
     rope_and_cache_fp8,
     swap_blocks_fp8,
+)
+from .tree import (  # noqa: F401
+    accept_tree,
+    keep_tokens,
+    paged_attention_cross,
+    paged_attention_tree,
+    pk_accept_tree,
+    pk_keep_tokens,
+    pk_keep_tokens_layers,
+    pk_paged_attention_cross,
+    pk_paged_attention_tree,
+    pk_selftest_cross_wait_timeout,
+    pk_tree_workspace_bytes,
 )
 from ._native import PagedKVError, load as load_library  # noqa: F401
 from .block_manager import BlockManager  # noqa: F401

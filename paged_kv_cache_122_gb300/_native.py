@@ -108,6 +108,36 @@ SIGNATURES = {
     "pk_swap_blocks_fp8": (c_int, [
         c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
         c_int, c_int, c_int, c_int, c_int, c_int, c_void_p]),
+    # include/pagedkv_tree.h
+    "pk_tree_workspace_bytes": (c_size_t, [c_int, c_int, c_int, c_int, c_int]),
+    "pk_paged_attention_tree": (c_int, [
+        c_void_p, c_int, c_void_p, c_int, c_void_p, c_int,       # out, out_dtype, q, total_q, cu_q_lens, max_q_len
+        c_void_p, c_int,                                         # tree_mask, mask_words
+        c_void_p, c_void_p, c_void_p, c_int, c_void_p, c_int,    # k_cache, v_cache, tables, max_blocks, seq_lens, max_seq_len
+        c_int, c_int, c_int, c_int, c_int, c_int, c_float,       # seqs, heads, kv_heads, head_dim, blocks, block_size, scale
+        c_void_p, c_size_t, c_void_p]),                          # workspace, workspace_bytes, stream
+    "pk_paged_attention_cross": (c_int, [
+        c_void_p, c_int, c_void_p, c_int, c_void_p, c_int,
+        c_void_p, c_void_p, c_void_p, c_int, c_void_p, c_int,
+        c_int, c_int, c_int, c_int, c_int, c_int, c_float,
+        c_void_p, c_size_t, c_void_p]),
+    "pk_selftest_cross_wait_timeout": (c_int, [
+        c_void_p, c_int, c_void_p, c_int, c_void_p, c_int,
+        c_void_p, c_void_p, c_void_p, c_int, c_void_p, c_int,
+        c_int, c_int, c_int, c_int, c_int, c_int, c_float,
+        c_void_p, c_size_t, c_int, c_uint, c_void_p]),           # workspace, bytes, stall_tile, wait_limit_us, stream
+    "pk_accept_tree": (c_int, [
+        c_void_p, c_void_p, c_void_p, c_void_p,                  # accepted, num_accepted, next_tokens, new_seq_lens
+        c_void_p, c_void_p, c_void_p, c_int,                     # draft_tokens, parents, target_tokens, total_q
+        c_void_p, c_int, c_void_p, c_int, c_void_p]),            # cu_q_lens, max_q_len, seq_lens, num_seqs, stream
+    "pk_keep_tokens": (c_int, [
+        c_void_p, c_void_p, c_void_p, c_int,                     # k_cache, v_cache, block_tables, max_blocks_per_seq
+        c_void_p, c_void_p, c_void_p, c_int, c_void_p,           # seq_lens, cu_q_lens, accepted, its stride, num_accepted
+        c_int, c_int, c_int, c_int, c_int, c_void_p]),           # seqs, kv_heads, head_dim, blocks, block_size, stream
+    "pk_keep_tokens_layers": (c_int, [
+        c_void_p, c_void_p, c_void_p, c_int,
+        c_void_p, c_void_p, c_void_p, c_int, c_void_p,
+        c_int, c_int, c_int, c_int, c_int, c_int, c_void_p]),    # seqs, layers, kv_heads, head_dim, blocks, block_size, stream
     # include/pagedkv_block_manager.h
     "pk_bm_create": (c_void_p, [c_int, c_int]),
     "pk_bm_destroy": (None, [c_void_p]),
@@ -115,6 +145,7 @@ SIGNATURES = {
     "pk_bm_append_slots": (c_int, [c_void_p, c_void_p, c_int, c_void_p]),
     "pk_bm_fork": (c_int, [c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64]),
     "pk_bm_free_sequence": (c_int, [c_void_p, ctypes.c_int64]),
+    "pk_bm_truncate": (c_int, [c_void_p, ctypes.c_int64, ctypes.c_int64]),
     "pk_bm_num_pending_copies": (c_int, [c_void_p]),
     "pk_bm_take_copies": (c_int, [c_void_p, c_void_p, c_int, ctypes.POINTER(c_int)]),
     "pk_bm_export": (c_int, [c_void_p, c_void_p, c_int, c_void_p, c_int, c_void_p]),
@@ -134,7 +165,7 @@ STATUS_NAMES = {
 }
 PK_ERR_NO_BLOCKS, PK_ERR_UNKNOWN_SEQUENCE, PK_ERR_SEQUENCE_EXISTS = -8, -9, -10
 DEVERR_BLOCK_ID, DEVERR_SLOT, DEVERR_PAIR, DEVERR_SEQ_LEN, DEVERR_TIMEOUT = 0x1, 0x2, 0x4, 0x8, 0x10
-DEVERR_POINTER, DEVERR_SCALE = 0x20, 0x40
+DEVERR_POINTER, DEVERR_SCALE, DEVERR_DRAFT = 0x20, 0x40, 0x80
 PATH_AUTO, PATH_CUDA_CORE, PATH_TENSOR_CORE = 0, 1, 2
 
 _lib = None

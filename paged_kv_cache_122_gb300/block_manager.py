@@ -67,6 +67,10 @@ class BlockManager:
     def free_sequence(self, seq_id: int) -> None:
         check("pk_bm_free_sequence", self._lib.pk_bm_free_sequence(self._h, int(seq_id)))
 
+    def truncate(self, seq_id: int, num_tokens: int) -> None:
+        """Keep the first ``num_tokens`` tokens; blocks behind them are given back."""
+        check("pk_bm_truncate", self._lib.pk_bm_truncate(self._h, int(seq_id), int(num_tokens)))
+
     # -- outputs ------------------------------------------------------------
     def take_copies(self) -> np.ndarray:
         """The queued (src, dst) pairs, in decision order, as int64 [k, 2]."""

@@ -226,6 +226,19 @@ extern "C" int pk_bm_free_sequence(pk_block_manager *bm, int64_t seq_id) {
     return PK_OK;
 }
 
+extern "C" int pk_bm_truncate(pk_block_manager *bm, int64_t seq_id, int64_t num_tokens) {
+    if (!bm) return PK_ERR_NULL;
+    auto it = bm->seqs.find(seq_id);
+    if (it == bm->seqs.end()) return PK_ERR_UNKNOWN_SEQUENCE;
+    pk_block_manager::Seq &sq = it->second;
+    if (num_tokens < 0 || num_tokens > sq.length) return PK_ERR_SHAPE;
+    const size_t keep = static_cast<size_t>(num_tokens / bm->block_size + (num_tokens % bm->block_size != 0));
+    for (size_t j = keep; j < sq.table.size(); ++j) bm->drop(sq.table[j]);
+    sq.table.resize(keep);
+    sq.length = num_tokens;
+    return PK_OK;
+}
+
 extern "C" int pk_bm_num_pending_copies(const pk_block_manager *bm) {
     if (!bm) return PK_ERR_NULL;
     return static_cast<int>(bm->copies.size() / 2);

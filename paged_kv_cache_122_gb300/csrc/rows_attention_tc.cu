@@ -1,0 +1,1122 @@
+// Attention of many query rows per sequence over its paged keys, split along
+// the keys: a tree of drafted tokens (a bit mask among the drafts, the context
+// in full) and cross attention (every key).
+//
+// Mathematics.  For a query row, scores s_j = c q.k_j (c holds log2 e) over the
+// visible keys; weights 2^(s_j - m) against a reference max m that moves only when
+// a score exceeds it by more than 8; O = sum of weights times v_j, l = sum of
+// weights, result O / l.  Parts over disjoint keys join by M = max m, factors
+// 2^(m - M): between the two groups of a CTA and between CTAs.
+//
+// Shapes.  A query tile is 128 rows -- 128 / G tokens x the G heads of one KV
+// head -- on the M of both products, as in the prefill kernel:
+//   S[128 x 128] = Q K_tile^T,  O[128 x D] += P V_tile   (tcgen05, fp32 in TMEM).
+// A segment is one (sequence, KV head, block of query tiles) over all of the
+// sequence's 128-key tiles.  A block is two query tiles that share every K and V
+// tile, or one.  With one, the two softmax groups take the key tiles in turn,
+// each with its own O and m, and join at the end of the part through tensor
+// memory, where both see the same lanes: a single tile's chain of scores, weights
+// and product takes longer than the 1.6 us in which an SM's share of the memory
+// bandwidth brings a tile, two chains side by side do not.
+//
+// Work.  The flattened (segment, key tile) space is cut into one range of equal
+// cost for each persistent CTA, so few long sequences fill the GPU as many short
+// ones do; a segment that is cut leaves (m, l, O) in a workspace slot, and a merge
+// kernel joins its parts.
+//
+// Steps.  Step k belongs to group x = k mod 2.  A block of one tile has a step per
+// key tile, a block of two has two.  The MMA thread issues, at step k, P.V of step
+// k - 2 (the same group's last one, whose P lies where S is going) and S of step
+// k, across parts without a pause.
+//
+// Per CTA (384 threads): warps 0-3 and 4-7 the softmax groups (thread <-> query
+// row = TMEM lane), warp 8 copies K, 9 V, 10 issues MMAs, 11 copies Q.
+#include "rows_attention.cuh"
+#include "block_scan.cuh"
+#include "sm100.cuh"
+#include "tmem_wide.cuh"
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <mutex>
+#include <type_traits>
+
+namespace pk {
+namespace {
+
+using namespace sm100;
+
+constexpr int kRows = 128;                      // query rows per tile = MMA M
+constexpr int kKeys = 128;                      // keys per tile = MMA N of S
+constexpr int kThreads = 384;
+constexpr uint32_t kChunk = 128 * 128;          // 128 rows x 128 bytes (64 bf16)
+constexpr uint32_t kTmemCols = 512;             // S_0, S_1, O_0, O_1 (128 columns each)
+constexpr uint32_t kTmemS = 0;                  // + x * 128; P_x over its first 64 columns
+constexpr uint32_t kTmemO = 256;                // + x * 128
+constexpr uint64_t kWaitLimitNs = 1000000000ull;
+constexpr float kRescaleLog2 = 8.0f;
+
+// What a part costs, in units of 0.1 us: a segment's set-up and read-out, a key
+// tile under one query tile (bound by the copies) and under two (by the softmax
+// groups and the MMAs).
+constexpr int64_t kSegCost = 16, kTileCost1 = 16, kTileCost2 = 24;
+// A CTA is not given less than this: a cut costs a merge.
+constexpr int64_t kMinCost = 32;
+
+// Rings of 128-key tiles: what 224 KB hold.  TWO: segments may have two query
+// tiles, both resident; otherwise one, or two of at most 64 rows.
+template <int D, bool TWO>
+struct Cfg {
+    static constexpr uint32_t kTile = kChunk * (D / 64);     // Q, K or V of 128 rows
+    static constexpr uint32_t kQRegion = (TWO ? 2 : 1) * kTile;
+    static constexpr int kKS = D == 128 ? 3 : 6;
+    static constexpr int kVS = D == 128 ? (TWO ? 2 : 3) : 6;
+    static constexpr uint32_t kKOff = kQRegion;
+    static constexpr uint32_t kVOff = kKOff + kKS * kTile;
+    static constexpr uint32_t kEnd = kVOff + kVS * kTile;
+    // Tile masks in flight: the K producer runs at most kKS + 1 tiles ahead of a
+    // softmax group (its S done frees a slot; the step two on waits for its P).
+    static constexpr int kMasks = D == 128 ? 8 : 16;
+    static_assert(kMasks > kKS + 2, "masks in flight");
+};
+
+struct Pos {          // a place in the flattened (segment, key tile) space
+    int64_t tile;     // index of the key tile
+    int32_t s, h, j, t;
+};
+
+template <int KS, int VS, int MASKS>
+struct Misc {
+    uint64_t kfull[KS], kempty[KS], vfull[VS], vempty[VS];
+    uint64_t qfull[2], qempty[2];
+    uint64_t s_full[2], p_full[2], pv_done[2];
+    uint64_t ml_ready, o_taken;   // the join of two groups' parts
+    uint64_t drain;
+    Pos pos[2];                   // start of this range and of the next one
+    int32_t first_cta;            // the CTA in whose range this range's first segment starts
+    uint32_t tmem_base;
+    int abort;
+    int never;
+    uint32_t mask[MASKS][4];      // valid keys of a tile
+    union {
+        struct {
+            int64_t tiles[kThreads / 32 + 1], costs[kThreads / 32 + 1];
+        } scan;                   // while planning
+        struct {
+            float m[kRows], l[kRows];
+        } part;                   // what the group that is not the last one leaves
+    };
+};
+
+// Slot of a cut part: slot 0 of a CTA for its first segment, slot 1 for its last.
+struct SlotHead {
+    int32_t flag;          // slot 0: the merge joins this segment at this CTA
+    int32_t s, h, tok0;    // sequence, KV head, first token of the block's first tile
+    int32_t ntiles;        // query tiles
+    int32_t first_cta;     // slot 0: the CTA in whose range the segment starts
+    int64_t start_tile;    // flattened index of the segment's key tile 0
+    int64_t range_beg;     // slot 0: first tile of this CTA's range
+    int64_t total_tiles;   // slot 0
+    int64_t pad[2];
+};
+static_assert(sizeof(SlotHead) == 64, "slot header");
+
+template <int D>
+constexpr size_t slot_bytes(int ntiles) {
+    return sizeof(SlotHead) + static_cast<size_t>(ntiles) * (2 * kRows + D * kRows) * sizeof(float);
+}
+__device__ __forceinline__ char *slot_at(const RowsParams &p, size_t bytes, int cta, int which) {
+    return static_cast<char *>(p.slots) + (2 * static_cast<size_t>(cta) + which) * bytes;
+}
+// m, l and O^T of query tile x of a slot.
+__device__ __forceinline__ float *slot_m(char *slot, int x, int D) {
+    return reinterpret_cast<float *>(slot + sizeof(SlotHead)) + static_cast<size_t>(x) * (2 + D) * kRows;
+}
+
+struct Seq {
+    int L, q0, qn;      // keys; first query row; query rows (0 for a sequence to leave out)
+    int nt, n2, n1;     // key tiles; blocks of two query tiles; blocks of one (0 or 1)
+    bool bad;
+};
+
+template <bool TWO>
+__device__ __forceinline__ Seq load_seq(const RowsParams &p, int s, int lgG) {
+    Seq r;
+    r.L = p.seq_lens[s];
+    r.q0 = p.cu_q_lens[s];
+    const int q1 = p.cu_q_lens[s + 1];
+    const int64_t cap = min(static_cast<int64_t>(p.max_seq_len),
+                            static_cast<int64_t>(p.max_blocks_per_seq) * p.block_size);
+    r.bad = r.L < 0 || r.L > cap || r.q0 < 0 || q1 < r.q0 || q1 > p.total_q || q1 - r.q0 > p.max_q_len ||
+            (p.tree_mask && q1 - r.q0 > r.L);
+    r.qn = r.bad ? 0 : q1 - r.q0;
+    r.nt = r.qn > 0 ? (r.L >> 7) + ((r.L & 127) != 0) : 0;
+    const int qt = kRows >> lgG;
+    const int tiles = r.nt > 0 ? (r.qn + qt - 1) / qt : 0;
+    r.n2 = TWO ? tiles >> 1 : 0;
+    r.n1 = tiles - 2 * r.n2;
+    return r;
+}
+
+__device__ __forceinline__ int64_t block_cost(const Seq &q, bool two) {
+    return kSegCost + (two ? kTileCost2 : kTileCost1) * q.nt;
+}
+__device__ __forceinline__ int64_t head_cost(const Seq &q) {
+    return q.n2 * block_cost(q, true) + q.n1 * block_cost(q, false);
+}
+
+// One CTA's part of a segment, and the walk from part to part.
+struct Part {
+    int s, h, j;
+    int t0, t1;          // key tiles
+    int tok0;            // first query token of the block, in its sequence
+    bool two;
+};
+template <bool TWO>
+struct Walk {
+    const RowsParams &p;
+    int lgG;
+    int64_t left;        // key tiles left in the range
+    int s, h, j, t;
+    Seq q;
+    __device__ __forceinline__ Walk(const RowsParams &pp, int lg, const Pos &from, int64_t n)
+        : p(pp), lgG(lg), left(n), s(from.s), h(from.h), j(from.j), t(from.t) {
+        if (left > 0) q = load_seq<TWO>(p, s, lgG);
+    }
+    __device__ __forceinline__ bool next(Part &a) {
+        if (left <= 0) return false;
+        const int n = static_cast<int>(min(left, static_cast<int64_t>(q.nt - t)));
+        a.s = s;
+        a.h = h;
+        a.j = j;
+        a.t0 = t;
+        a.t1 = t + n;
+        a.two = TWO && j < q.n2;
+        a.tok0 = j * (2 * (kRows >> lgG));
+        left -= n;
+        return true;
+    }
+    // To the part after the one that next() gave (its fields of q stay until here).
+    __device__ __forceinline__ void advance() {
+        if (left <= 0) return;
+        t = 0;
+        if (++j < q.n2 + q.n1) return;
+        j = 0;
+        if (++h < p.num_kv_heads) return;
+        h = 0;
+#pragma unroll 1
+        do {
+            ++s;                                  // (tiles are left, so there is such a sequence)
+            q = load_seq<TWO>(p, s, lgG);
+        } while (q.nt == 0);
+    }
+};
+
+// Cuts the flattened space: CTA c of C takes the tiles whose cost starts in
+// [c W / C, (c + 1) W / C), W the total cost, C no more than gives every CTA
+// kMinCost.  A segment's tile 0 starts at its start, tile t at start + kSegCost + t
+// tiles.  Every thread calls it; returns the total tile count, and in *odd whether
+// a sequence is to be reported or to get zeros.
+template <bool TWO, typename M>
+__device__ __forceinline__ int64_t plan(const RowsParams &p, M *misc, int lgG, int c, int C, int *odd) {
+    const int N = p.num_seqs, Hkv = p.num_kv_heads;
+    const int per = (N + kThreads - 1) / kThreads;
+    const int s_lo = min(N, static_cast<int>(threadIdx.x) * per), s_hi = min(N, s_lo + per);
+    int64_t mine = 0, mine_w = 0;
+    int strange = 0;
+#pragma unroll 1
+    for (int s = s_lo; s < s_hi; ++s) {
+        const Seq q = load_seq<TWO>(p, s, lgG);
+        strange |= q.bad || (q.qn > 0 && q.L == 0);
+        mine += static_cast<int64_t>(q.nt) * (q.n2 + q.n1) * Hkv;
+        mine_w += head_cost(q) * Hkv;
+    }
+    int64_t T, W;
+    const int64_t off = block_exclusive_scan<kThreads>(mine, misc->scan.tiles, &T);
+    const int64_t off_w = block_exclusive_scan<kThreads>(mine_w, misc->scan.costs, &W);
+    const int64_t Ce = max(static_cast<int64_t>(1), min(static_cast<int64_t>(C), W / kMinCost));
+    auto bound = [&](int64_t k) -> int64_t { return k >= Ce ? W : k * W / Ce; };
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k) {
+        const int64_t P = bound(c + k);
+        if (P >= W) {
+            if (threadIdx.x == 0) misc->pos[k].tile = T;
+            continue;
+        }
+        if (P < off_w || P >= off_w + mine_w) continue;
+        int64_t at = off, at_w = off_w;
+#pragma unroll 1
+        for (int s = s_lo; s < s_hi; ++s) {
+            const Seq q = load_seq<TWO>(p, s, lgG);
+            const int64_t hc = head_cost(q);
+            if (P >= at_w + hc * Hkv) {
+                at += static_cast<int64_t>(q.nt) * (q.n2 + q.n1) * Hkv;
+                at_w += hc * Hkv;
+                continue;
+            }
+            int64_t r = P - at_w;
+            int64_t h = r / hc;
+            r -= h * hc;
+            const int64_t b2 = block_cost(q, true);
+            int64_t j = min(r / b2, static_cast<int64_t>(q.n2));
+            r -= j * b2;
+            const int64_t tc = j < q.n2 ? kTileCost2 : kTileCost1;
+            // The first tile that starts at or after r.
+            int64_t t = r == 0 ? 0 : max(static_cast<int64_t>(1), (r - kSegCost + tc - 1) / tc);
+            int64_t a = P - r;                        // where the segment starts
+            if (t >= q.nt) {                          // behind its last one: the next segment
+                a += block_cost(q, j < q.n2);
+                t = 0;
+                if (++j == q.n2 + q.n1) {
+                    j = 0;
+                    ++h;
+                }
+            }
+            Pos &o = misc->pos[k];
+            o.tile = at + (h * (q.n2 + q.n1) + j) * q.nt + t;
+            if (h == Hkv) {                           // the first segment of a later sequence
+                h = 0;
+                int s2 = s;
+#pragma unroll 1
+                while (++s2 < N && load_seq<TWO>(p, s2, lgG).nt == 0) {}
+                o.s = s2;
+            } else {
+                o.s = s;
+            }
+            o.h = static_cast<int>(h);
+            o.j = static_cast<int>(j);
+            o.t = static_cast<int>(t);
+            if (k == 0) {
+                int64_t f = min(a * Ce / W, Ce - 1);
+                while (f + 1 < Ce && bound(f + 1) <= a) ++f;
+                while (f > 0 && bound(f) > a) --f;
+                misc->first_cta = static_cast<int>(f);
+            }
+            break;
+        }
+    }
+    *odd = __syncthreads_or(strange);
+    return T;
+}
+
+__device__ __forceinline__ float ex2(float x) { return fast_exp2(x); }
+// Three-input max / min (NaN inputs are skipped, as by fmaxf / fminf).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+    float r;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// N results of a row, to element idx of the output (idx and N multiples of 8).
+template <int N>
+__device__ __forceinline__ void store_row(const RowsParams &p, size_t idx, const float (&f)[N]) {
+    if (p.out_fp32) {
+        float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + idx);
+#pragma unroll
+        for (int k = 0; k < N / 4; ++k) o[k] = make_float4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
+    } else {
+        uint4 *o = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + idx);
+#pragma unroll
+        for (int k = 0; k < N / 8; ++k)
+            o[k] = make_uint4(pack_bf16x2(f[8 * k], f[8 * k + 1]), pack_bf16x2(f[8 * k + 2], f[8 * k + 3]),
+                              pack_bf16x2(f[8 * k + 4], f[8 * k + 5]), pack_bf16x2(f[8 * k + 6], f[8 * k + 7]));
+    }
+}
+
+// q_box: query tokens of a query copy (q_box * G rows, at most 128); q_slots: how
+// many query buffers the region holds (1 or 2; always 2 with TWO).
+template <int D, bool TWO>
+__global__ void __launch_bounds__(kThreads, 1)
+rows_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                      const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ RowsParams p, int q_box,
+                      int q_slots) {
+    static_assert(D == 64 || D == 128, "head_dim");
+    using C_ = Cfg<D, TWO>;
+    using M_ = Misc<C_::kKS, C_::kVS, C_::kMasks>;
+    constexpr int NCH = D / 64;
+    constexpr int KS = C_::kKS, VS = C_::kVS;
+    constexpr uint32_t kTile = C_::kTile;
+    static_assert(1024 + C_::kEnd + sizeof(M_) <= 232448, "shared memory per CTA");
+    // K and V of a key tile: each page in one TMA box as B / 8 blocks of 8 rows,
+    // each block [half][8 rows][64], so the 8-row swizzle atoms of a half lie
+    // kAtomStride apart whatever the block size.
+    constexpr uint32_t kAtomStride = 1024u * NCH;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int Hkv = p.num_kv_heads, H = p.num_heads, B = p.block_size;
+    const int G = H / Hkv, lgG = __ffs(G) - 1;
+    const int QT = kRows >> lgG;                    // query tokens per tile
+    const int c = blockIdx.x, C = gridDim.x;
+    const uint64_t lim = p.wait_limit_ns ? p.wait_limit_ns : kWaitLimitNs;
+    const size_t slot_sz = slot_bytes<D>(TWO ? 2 : 1);
+
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_addr = smem_u32(smem_raw);
+    uint8_t *smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+    M_ *misc = reinterpret_cast<M_ *>(smem + C_::kEnd);
+    const uint32_t base = smem_u32(smem);
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < KS; ++i) {
+            mbar_init(smem_u32(&misc->kfull[i]), 1);
+            mbar_init(smem_u32(&misc->kempty[i]), 1);
+        }
+        for (int i = 0; i < VS; ++i) {
+            mbar_init(smem_u32(&misc->vfull[i]), 1);
+            mbar_init(smem_u32(&misc->vempty[i]), 1);
+        }
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(smem_u32(&misc->qfull[x]), 1);
+            mbar_init(smem_u32(&misc->qempty[x]), 1);
+            mbar_init(smem_u32(&misc->s_full[x]), 1);
+            mbar_init(smem_u32(&misc->p_full[x]), 4);
+            mbar_init(smem_u32(&misc->pv_done[x]), 1);
+        }
+        mbar_init(smem_u32(&misc->ml_ready), 4);
+        mbar_init(smem_u32(&misc->o_taken), 4);
+        mbar_init(smem_u32(&misc->drain), 1);
+        misc->abort = 0;
+        misc->never = 0;
+        fence_mbar_init();
+    }
+    if (warp == 10) {
+        tmem_alloc(smem_u32(&misc->tmem_base), kTmemCols);
+        tmem_relinquish();
+    }
+    if (warp == 8 && lane == 0) {
+        prefetch_tmap(&tm_k);
+        prefetch_tmap(&tm_v);
+        prefetch_tmap(&tm_q);
+    }
+    // A programmatic dependent of the previous kernel in the stream: nothing
+    // global is read or written before this wait.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    int odd;
+    const int64_t T = plan<TWO>(p, misc, lgG, c, C, &odd);
+    const Pos from = misc->pos[0];
+    const int64_t n_tiles = misc->pos[1].tile - from.tile;
+    if (threadIdx.x == 0 && p.slots) {
+        SlotHead *hd = reinterpret_cast<SlotHead *>(slot_at(p, slot_sz, c, 0));
+        hd->flag = 0;
+        hd->range_beg = from.tile;
+    }
+    // Sequences out of range are reported, and rows without keys get zeros, by CTA s % C.
+    if (odd) {
+        for (int s = c; s < p.num_seqs; s += C) {
+            const Seq q = load_seq<TWO>(p, s, lgG);
+            if (q.bad && threadIdx.x == 0) set_error(p.err, PK_DEVERR_SEQ_LEN);
+            if (q.qn == 0 || q.L != 0) continue;
+            const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            const size_t first = static_cast<size_t>(q.q0) * H * D;
+            for (int64_t i = threadIdx.x; i < static_cast<int64_t>(q.qn) * H * (D / 8); i += kThreads)
+                store_row<8>(p, first + 8 * i, zero);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = misc->tmem_base;
+
+    Walk<TWO> walk(p, lgG, from, n_tiles);
+    Part a;
+    auto give_up = [&]() {
+        misc->abort = 1;
+        set_error(p.err, PK_DEVERR_TIMEOUT);
+    };
+    // Query buffers: a block of two tiles fills both; blocks of one take them in turn.
+    const uint32_t q_chunk = static_cast<uint32_t>(max(8, q_box << lgG)) * 128u;
+    const uint32_t q_slot = TWO ? kTile : q_chunk * NCH;
+
+    if (warp == 8 || warp == 9) {
+        // ================= producers: warp 8 K, warp 9 V =================
+        const bool kprod = warp == 8;
+        const int MB = p.max_blocks_per_seq;
+        const int nst = kprod ? KS : VS;
+        uint64_t *full = kprod ? misc->kfull : misc->vfull, *empty = kprod ? misc->kempty : misc->vempty;
+        const uint32_t ring = base + (kprod ? C_::kKOff : C_::kVOff);
+        const void *tm = kprod ? static_cast<const void *>(&tm_k) : static_cast<const void *>(&tm_v);
+        int issued = 0, st = 0;
+        uint32_t ph = 1;
+        bool ok_run = true, stalled = false;
+        while (ok_run && walk.next(a)) {
+            const int L = walk.q.L;
+            const int32_t *table = p.block_tables + static_cast<size_t>(a.s) * MB;
+            // Block-table entries of a key tile, one page per lane; the next
+            // tile's are fetched while the current tile's copies are issued.
+            auto fetch = [&](int t) -> int {
+                const int tok = t * kKeys;
+                const int pg = (min(kKeys, L - tok) + B - 1) / B;
+                return lane < pg ? table[tok / B + lane] : -1;
+            };
+            int phys_next = fetch(a.t0);
+            for (int t = a.t0; t < a.t1; ++t) {
+                // Self-test of the bounded waits: CTA 0 stops copying keys here.
+                if (kprod && p.stall_tile > 0 && c == 0 && issued == p.stall_tile) {
+                    stalled = true;
+                    ok_run = false;
+                    break;
+                }
+                const int phys = phys_next;
+                int got = 1;
+                if (lane == 0) got = mbar_wait(smem_u32(&empty[st]), ph, &misc->abort, lim);
+                if (!__shfl_sync(0xffffffffu, got, 0)) {
+                    if (lane == 0) give_up();
+                    ok_run = false;
+                    break;
+                }
+                const int vlen = min(kKeys, L - t * kKeys);
+                const int r0 = lane * B;
+                const bool in = r0 < vlen;
+                const bool ok = in && phys >= 0 && phys < p.num_blocks;
+                const uint32_t nok = __popc(__ballot_sync(0xffffffffu, ok));
+                const uint32_t bar = smem_u32(&full[st]);
+                if (kprod) {
+                    if (in && !ok) set_error(p.err, PK_DEVERR_BLOCK_ID);
+                    uint32_t bits = 0;
+                    if (ok) {
+                        const int nrows = min(B, vlen - r0);
+                        bits = (nrows >= 32 ? 0xffffffffu : ((1u << nrows) - 1u)) << (r0 & 31);
+                    }
+                    const int word = r0 >> 5;
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const uint32_t m = __reduce_or_sync(0xffffffffu, word == w ? bits : 0u);
+                        if (lane == 0) misc->mask[issued & (C_::kMasks - 1)][w] = m;
+                    }
+                }
+                if (lane == 0) mbar_arrive_expect_tx(bar, nok * B * 128u * NCH);
+                __syncwarp();
+                // One box per page, at the page's place in the tile.
+                if (ok) tma_load_5d(ring + st * kTile + r0 * 128 * NCH, tm, bar, 0, 0, 0, phys * (B >> 3), a.h);
+                ++issued;
+                if (++st == nst) {
+                    st = 0;
+                    ph ^= 1;
+                }
+                if (t + 1 < a.t1) phys_next = fetch(t + 1);
+            }
+            walk.advance();
+        }
+        if ((misc->abort || stalled) && lane == 0) {
+            // Let the copies in flight land before the CTA can exit.
+            for (int i = max(0, issued - nst); i < issued; ++i)
+                mbar_wait(smem_u32(&full[i % nst]), (i / nst) & 1, &misc->never, lim);
+        }
+    } else if (warp == 11) {
+        // ================= producer of the queries =================
+        if (lane == 0) {
+            int fill0 = 0, fill1 = 0;
+            int turn = 0;
+            bool ok_run = true;
+            const uint32_t bytes = static_cast<uint32_t>(q_box << lgG) * 128u * NCH;
+            while (ok_run && walk.next(a)) {
+                const int q0 = walk.q.q0;
+                for (int x = 0; x < (a.two ? 2 : 1) && ok_run; ++x) {
+                    const int sl = a.two ? x : turn;
+                    if (!mbar_wait(smem_u32(&misc->qempty[sl]), ((sl ? fill1 : fill0) & 1) ^ 1, &misc->abort, lim)) {
+                        give_up();
+                        ok_run = false;
+                        break;
+                    }
+                    const uint32_t bar = smem_u32(&misc->qfull[sl]);
+                    mbar_arrive_expect_tx(bar, bytes);
+#pragma unroll
+                    for (int ch = 0; ch < NCH; ++ch)
+                        tma_load_3d(base + sl * q_slot + ch * q_chunk, &tm_q, bar, ch * 64, a.h * G,
+                                    q0 + a.tok0 + x * QT);
+                    if (sl) ++fill1;
+                    else ++fill0;
+                }
+                if (!a.two && q_slots == 2) turn ^= 1;
+                walk.advance();
+            }
+            if (misc->abort)
+                for (int sl = 0; sl < 2; ++sl) {
+                    const int n = sl ? fill1 : fill0;
+                    if (n > 0) mbar_wait(smem_u32(&misc->qfull[sl]), (n - 1) & 1, &misc->never, lim);
+                }
+        }
+        __syncwarp();
+    } else if (warp == 10) {
+        // ================= MMA issuer =================
+        if (lane == 0) {
+            constexpr uint32_t kIdescS = idesc_bf16(kRows, kKeys, 0, 0);   // A = Q, B = K, both K-major
+            constexpr uint32_t kIdescO = idesc_bf16(kRows, D, 0, 1);       // A = P (TMEM), B = V (MN-major)
+            bool alive = true;
+            int k = 0;                         // step
+            int ks = 0, kph = 0;               // K ring
+            int vs = 0, vph = 0;               // V ring: the next tile whose P.V comes
+            // What P.V needs of the last step of either group.
+            // (Bit x is group x's; in registers, as no array with a runtime index is.)
+            uint32_t pend = 0, pfirst = 0, plast = 0;
+            uint32_t jobs = 0;                 // parity of the P.V issued
+            bool vready = false;               // the V tile of the ring's head has been waited for
+            auto pv = [&](int x) {
+                alive = mbar_wait(smem_u32(&misc->p_full[x]), (jobs >> x) & 1, &misc->abort, lim) &&
+                        (vready || mbar_wait(smem_u32(&misc->vfull[vs]), vph, &misc->abort, lim));
+                if (!alive) return;
+                vready = true;
+                tc_fence_after();
+                const uint32_t vbase = base + C_::kVOff + vs * kTile;
+                const uint32_t acol = tmem + kTmemS + x * 128;
+#pragma unroll
+                for (int kk = 0; kk < kKeys / 16; ++kk) {
+                    // Keys 16kk .. 16kk+15: 8-row blocks 2kk and 2kk + 1; the
+                    // two 64-element halves 1,024 bytes apart.
+                    const uint64_t b = smem_desc(vbase + kk * 2 * kAtomStride, 1024, kAtomStride, kLayoutSw128);
+                    mma_bf16_tmem_a(tmem + kTmemO + x * 128, acol + kk * 8, b, kIdescO,
+                                    (!((pfirst >> x) & 1) || kk > 0) ? 1u : 0u);
+                }
+                mma_commit(smem_u32(&misc->pv_done[x]));
+                if ((plast >> x) & 1) {        // the tile's last product: its V slot is free
+                    mma_commit(smem_u32(&misc->vempty[vs]));
+                    vready = false;
+                    if (++vs == VS) {
+                        vs = 0;
+                        vph ^= 1;
+                    }
+                }
+                jobs ^= 1u << x;
+                pend &= ~(1u << x);
+            };
+            uint32_t uses = 0;                 // parity of the parts that read each query buffer
+            int turn = 0;
+            while (alive && walk.next(a)) {
+                const int sl1 = turn;          // buffer of a block of one tile
+                if (!a.two && q_slots == 2) turn ^= 1;
+                const int per = a.two ? 2 : 1;
+                uint32_t started = 0;
+                for (int t = a.t0; t < a.t1 && alive; ++t) {
+                    bool kready = false;
+                    for (int y = 0; y < per && alive; ++y, ++k) {
+                        const int x = k & 1;
+                        if ((pend >> x) & 1) pv(x);
+                        if (!alive) break;
+                        const int sl = a.two ? x : sl1;
+                        if (t == a.t0)
+                            alive = mbar_wait(smem_u32(&misc->qfull[sl]), (uses >> sl) & 1, &misc->abort, lim);
+                        if (alive && !kready)
+                            alive = mbar_wait(smem_u32(&misc->kfull[ks]), kph, &misc->abort, lim);
+                        if (!alive) break;
+                        kready = true;
+                        tc_fence_after();
+                        const uint32_t kbase = base + C_::kKOff + ks * kTile;
+                        const uint32_t qbase = base + sl * q_slot;
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint64_t qa = smem_desc(qbase + (kk >> 2) * q_chunk + (kk & 3) * 32, 16, 1024,
+                                                          kLayoutSw128);
+                            const uint64_t kb = smem_desc(kbase + (kk >> 2) * 1024u + (kk & 3) * 32, 16, kAtomStride,
+                                                          kLayoutSw128);
+                            mma_bf16(tmem + kTmemS + x * 128, qa, kb, kIdescS, kk > 0 ? 1u : 0u);
+                        }
+                        mma_commit(smem_u32(&misc->s_full[x]));
+                        if (t == a.t1 - 1) {   // the part's last scores from this buffer
+                            mma_commit(smem_u32(&misc->qempty[sl]));
+                            uses ^= 1u << sl;
+                        }
+                        const uint32_t bit = 1u << x;
+                        pend |= bit;
+                        pfirst = (started & bit) ? pfirst & ~bit : pfirst | bit;
+                        plast = y == per - 1 ? plast | bit : plast & ~bit;
+                        started |= bit;
+                    }
+                    if (!alive) break;
+                    mma_commit(smem_u32(&misc->kempty[ks]));
+                    if (++ks == KS) {
+                        ks = 0;
+                        kph ^= 1;
+                    }
+                }
+                walk.advance();
+            }
+            for (int e = 0; e < 2 && alive; ++e, ++k)
+                if ((pend >> (k & 1)) & 1) pv(k & 1);
+            if (!alive) give_up();
+            // Let every issued MMA finish before the CTA can release TMEM.
+            mma_commit(smem_u32(&misc->drain));
+            mbar_wait(smem_u32(&misc->drain), 0, &misc->never, lim);
+        }
+        __syncwarp();
+    } else {
+        // ================= softmax: warps 0-3 group 0, 4-7 group 1; thread <-> query row =================
+        const int x = warp >> 2;
+        const int quad = warp & 3;                      // TMEM lanes 32 * (warp % 4) ..
+        const int row = quad * 32 + lane;
+        const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+        const uint32_t s_col = lane_addr + kTmemS + x * 128;
+        const uint32_t o_col = lane_addr + kTmemO + x * 128;
+        const uint32_t o_other = lane_addr + kTmemO + (1 - x) * 128;
+        const int rr = row >> lgG;                      // query token of this row in its tile
+        const float cs = p.scale_log2;
+        const uint64_t c2 = f2(cs, cs);
+        int k = 0;                                      // step at the start of the part
+        int ktile = 0;                                  // key tile (of the CTA's range) there
+        int jobs = 0;                                   // this group's steps so far
+        int joins = 0;                                  // joins of two groups so far
+        bool owe = false;                               // the other group still reads this group's O
+        bool alive = true;
+        auto wait = [&](uint64_t *bar, int phase) -> bool {
+            return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), phase & 1, &misc->abort, lim));
+        };
+        while (alive && walk.next(a)) {
+            const Seq q = walk.q;
+            const int per = a.two ? 2 : 1;
+            const int nsteps = (a.t1 - a.t0) * per;
+            const int tok0 = a.tok0 + (a.two ? x * QT : 0);   // first query token of this tile
+            const int ntok = min(q.qn - tok0, QT);
+            const bool busy = (quad * 32) >> lgG < ntok;      // this warp has a row in use
+            const int base_pos = q.L - q.qn;                  // position of the tree's node 0
+            const uint32_t *mrow_bits = p.tree_mask
+                ? p.tree_mask + static_cast<size_t>(q.q0 + tok0 + min(rr, ntok - 1)) * p.mask_words : nullptr;
+            float m_ref = -INFINITY, l_run = 0.f;
+            bool first = true;
+            // This group's first step, and from there every second one (one tile)
+            // or every key tile (two).
+            int i0 = (k & 1) == x ? 0 : 1;
+            for (int i = i0; i < nsteps; i += 2) {
+                const int t = a.t0 + (a.two ? i >> 1 : i);
+                const int kt = ktile + (a.two ? i >> 1 : i);
+                if (!wait(&misc->s_full[x], jobs) || (jobs > 0 && !wait(&misc->pv_done[x], jobs - 1))) {
+                    alive = false;
+                    break;
+                }
+                tc_fence_after();
+                uint32_t msk[4];
+#pragma unroll
+                for (int w = 0; w < 4; ++w) msk[w] = misc->mask[kt & (C_::kMasks - 1)][w];
+                // V rows of keys outside the sequence or behind a bad table entry
+                // may hold stale or non-finite bits; the MMA multiplies them by 0,
+                // so the first group to use the tile zeroes them (thread <-> key row)
+                // once V has landed.
+                const uint32_t mrow = quad == 0 ? msk[0] : quad == 1 ? msk[1] : quad == 2 ? msk[2] : msk[3];
+                const bool stale = !((mrow >> lane) & 1u) && (!a.two || (i & 1) == 0);
+                if (busy) {
+                    uint32_t vis[4];
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) vis[w] = msk[w];
+                    const int over = t * kKeys + kKeys - base_pos;   // > 0: the tile holds nodes of the tree
+                    if (mrow_bits && over > 0) {
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            // Bits of the nodes at this word's 32 keys; the keys before
+                            // node 0 are context.
+                            const int n0 = t * kKeys + 32 * w - base_pos;
+                            const int at = n0 >> 5;                  // (rounds down)
+                            const uint32_t lo = at >= 0 && at < p.mask_words ? mrow_bits[at] : (at < 0 ? 0xffffffffu : 0u);
+                            const uint32_t hi = at + 1 >= 0 && at + 1 < p.mask_words ? mrow_bits[at + 1]
+                                                                                    : (at + 1 < 0 ? 0xffffffffu : 0u);
+                            vis[w] &= __funnelshift_r(lo, hi, n0 & 31);
+                        }
+                    }
+                    // Rows in use that see every key of the tile (warp-uniform: the
+                    // tensor-memory moves below are warp-collective).
+                    const bool easy = __all_sync(0xffffffffu, rr >= ntok || (vis[0] & vis[1] & vis[2] & vis[3]) == 0xffffffffu);
+                    auto visible = [&](int kk) -> bool { return (vis[kk >> 5] >> (kk & 31)) & 1u; };
+                    // The row's max, 32 scores at a time with the next load in flight, in
+                    // eight independent chains; a masked key is NaN, which max and min
+                    // skip.  The max of c s is that of c times the largest s (c >= 0) or
+                    // smallest: rounding is monotone.
+                    auto gather = [&](auto easy_tag, auto max_tag) -> float {
+                        constexpr bool kEasy = decltype(easy_tag)::value;
+                        constexpr bool kMax = decltype(max_tag)::value;
+                        auto pick3 = [&](float e0, float e1, float e2) {
+                            return kMax ? max3(e0, e1, e2) : min3(e0, e1, e2);
+                        };
+                        float e[8];
+#pragma unroll
+                        for (int n = 0; n < 8; ++n) e[n] = __int_as_float(0x7fffffff);
+                        uint32_t cb[2][32];
+                        tmemw::ld32(s_col, cb[0]);
+                        tmemw::wait_ld(cb[0]);
+#pragma unroll
+                        for (int cc = 0; cc < 4; ++cc) {
+                            if (cc < 3) tmemw::ld32(s_col + 32 * (cc + 1), cb[(cc + 1) & 1]);
+                            auto v = [&](int n) -> float {
+                                const float sc = __uint_as_float(cb[cc & 1][n]);
+                                return kEasy || visible(cc * 32 + n) ? sc : __int_as_float(0x7fffffff);
+                            };
+#pragma unroll
+                            for (int n = 0; n < 32; n += 16) {
+#pragma unroll
+                                for (int u = 0; u < 8; ++u) e[u] = pick3(e[u], v(n + u), v(n + 8 + u));
+                            }
+                            if (cc < 3) tmemw::wait_ld(cb[(cc + 1) & 1]);
+                        }
+                        const float e0 = pick3(e[0], e[1], e[2]), e1 = pick3(e[3], e[4], e[5]);
+                        return pick3(e0, e1, kMax ? fmaxf(e[6], e[7]) : fminf(e[6], e[7]));
+                    };
+                    const float ext = easy ? (cs >= 0.f ? gather(std::true_type{}, std::true_type{})
+                                                        : gather(std::true_type{}, std::false_type{}))
+                                           : (cs >= 0.f ? gather(std::false_type{}, std::true_type{})
+                                                        : gather(std::false_type{}, std::false_type{}));
+                    // No visible key (NaN): no candidate for the reference max.
+                    const float tmax = ext == ext ? ext * cs : -INFINITY;
+                    const bool need = tmax > m_ref + kRescaleLog2;
+                    if (__any_sync(0xffffffffu, need)) {
+                        // Move this row's reference max and rescale its O (complete up
+                        // to this group's last step) and denominator; rare after the
+                        // first tile.
+                        const float mn = need ? tmax : m_ref;
+                        const float f = rescale(m_ref, mn);
+                        if (!first) {
+#pragma unroll
+                            for (int cc = 0; cc < D / 8; ++cc) {
+                                float ov[8];
+                                tmem_ld<8>(o_col + cc * 8, ov);
+#pragma unroll
+                                for (int n = 0; n < 8; ++n) ov[n] *= f;
+                                tmem_st8(o_col + cc * 8, ov);
+                            }
+                        }
+                        l_run *= f;
+                        m_ref = mn;
+                    }
+                    // p = 2^(c s - m_ref) as bf16 pairs over the first 64 columns of S
+                    // (the A operand of P.V): half the tensor work of fp32 weights at
+                    // an error of 2^-9 of each weight; the denominator sums the rounded
+                    // weights, so that their mean stays a mean.  The scores are read
+                    // again, 32 columns at a time: P of columns 32cc.. goes to columns
+                    // 16cc.., already read.
+                    const float nm = m_ref == -INFINITY ? 0.f : -m_ref;
+                    const uint64_t nm2 = f2(nm, nm);
+                    uint64_t lacc[2] = {0ull, 0ull};
+                    auto emit = [&](auto easy_tag) {
+                        constexpr bool kEasy = decltype(easy_tag)::value;
+                        uint32_t cb[2][32];
+                        tmemw::ld32(s_col, cb[0]);
+                        tmemw::wait_ld(cb[0]);
+#pragma unroll
+                        for (int cc = 0; cc < 4; ++cc) {
+                            if (cc < 3) tmemw::ld32(s_col + 32 * (cc + 1), cb[(cc + 1) & 1]);
+                            uint32_t packed[16];
+#pragma unroll
+                            for (int n = 0; n < 32; n += 2) {
+                                const int kk = cc * 32 + n;
+                                const float2 arg = unf2(fma2(f2(__uint_as_float(cb[cc & 1][n]),
+                                                                __uint_as_float(cb[cc & 1][n + 1])), c2, nm2));
+                                float p0 = ex2(arg.x), p1 = ex2(arg.y);
+                                if constexpr (!kEasy) {
+                                    p0 = visible(kk) ? p0 : 0.f;
+                                    p1 = visible(kk + 1) ? p1 : 0.f;
+                                }
+                                const uint32_t w = pack_bf16x2(p0, p1);
+                                packed[n / 2] = w;
+                                lacc[(n >> 1) & 1] = add2(lacc[(n >> 1) & 1], f2(bf16_lo(w), bf16_hi(w)));
+                            }
+                            tmem_st16(s_col + cc * 16, packed);   // keys 32cc .. 32cc+31 of this row
+                            if (cc < 3) tmemw::wait_ld(cb[(cc + 1) & 1]);
+                        }
+                    };
+                    if (easy) emit(std::true_type{});
+                    else emit(std::false_type{});
+                    const float2 la = unf2(lacc[0]), lb = unf2(lacc[1]);
+                    l_run += (la.x + la.y) + (lb.x + lb.y);
+                }
+                if (__any_sync(0xffffffffu, stale)) {
+                    if (!wait(&misc->vfull[kt % VS], kt / VS)) {
+                        alive = false;
+                        break;
+                    }
+                    if (stale) {
+#pragma unroll
+                        for (int ch = 0; ch < NCH; ++ch) {
+                            uint4 *vrow = reinterpret_cast<uint4 *>(smem + C_::kVOff + (kt % VS) * kTile +
+                                                                    (row >> 3) * kAtomStride + ch * 1024 + (row & 7) * 128);
+#pragma unroll
+                            for (int n = 0; n < 8; ++n) vrow[n] = make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                    fence_proxy_async_smem();       // zeroed V rows are visible to the MMA
+                }
+                // The first product of a part overwrites O: the other group has to have
+                // read it, where it joined the last part.
+                if (owe) {
+                    if (!wait(&misc->o_taken, joins - 1)) {
+                        alive = false;
+                        break;
+                    }
+                    owe = false;
+                }
+                tmem_wait_st();                     // P is in TMEM before the MMA may read it
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&misc->p_full[x]));
+                ++jobs;
+                first = false;
+            }
+            if (!alive) break;
+            // ---- the part's end ----
+            const int last_x = (k + nsteps - 1) & 1;
+            const bool joined = !a.two && nsteps > 1;
+            const bool mine = a.two || last_x == x;     // this group gives the result out
+            if (joined && !mine) {
+                // Leave m and l to the other group, which reads this group's O itself.
+                misc->part.m[row] = m_ref;
+                misc->part.l[row] = l_run;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&misc->ml_ready));
+                owe = true;
+            }
+            if (mine) {
+                // P.V of this group's last step done; the other group's last one was
+                // issued before it, so that is done too.
+                if (!wait(&misc->pv_done[x], jobs - 1) || (joined && !wait(&misc->ml_ready, joins))) {
+                    alive = false;
+                    break;
+                }
+                tc_fence_after();
+                float f_own = 1.f, f_other = 0.f;
+                if (joined) {
+                    const float m2 = misc->part.m[row], l2 = misc->part.l[row];
+                    const float mm = fmaxf(m_ref, m2);
+                    f_own = rescale(m_ref, mm);
+                    f_other = rescale(m2, mm);
+                    l_run = l_run * f_own + l2 * f_other;
+                    m_ref = mm;
+                }
+                const bool complete = a.t0 == 0 && a.t1 == q.nt;
+                const int tile_x = a.two ? x : 0;
+                const bool first_part = a.s == from.s && a.h == from.h && a.j == from.j;
+                char *slot = complete ? nullptr : slot_at(p, slot_sz, c, first_part ? 0 : 1);
+                const bool use = rr < ntok;
+                const float inv = l_run > 0.f ? 1.f / l_run : (l_run == 0.f ? 0.f : l_run);
+                const float g_own = complete ? f_own * inv : f_own, g_other = complete ? f_other * inv : f_other;
+                const size_t oidx = (static_cast<size_t>(q.q0 + tok0 + rr) * H + a.h * G + (row & (G - 1))) *
+                                    static_cast<size_t>(D);
+                if (busy) {
+#pragma unroll
+                    for (int cc = 0; cc < D / 32; ++cc) {
+                        uint32_t ov[32];
+                        tmemw::ld32(o_col + cc * 32, ov);
+                        float f[32];
+                        if (joined) {
+                            uint32_t ow[32];
+                            tmemw::ld32(o_other + cc * 32, ow);
+                            tmemw::wait_ld(ov);
+                            tmemw::wait_ld(ow);
+#pragma unroll
+                            for (int n = 0; n < 32; ++n)
+                                f[n] = __uint_as_float(ov[n]) * g_own + __uint_as_float(ow[n]) * g_other;
+                        } else {
+                            tmemw::wait_ld(ov);
+#pragma unroll
+                            for (int n = 0; n < 32; ++n) f[n] = __uint_as_float(ov[n]) * g_own;
+                        }
+                        if (complete) {
+                            if (use) store_row<32>(p, oidx + cc * 32, f);
+                        } else {
+                            float *so = slot_m(slot, tile_x, D) + 2 * kRows + static_cast<size_t>(cc) * 32 * kRows + row;
+#pragma unroll
+                            for (int n = 0; n < 32; ++n) so[n * kRows] = f[n];
+                        }
+                    }
+                }
+                if (joined) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&misc->o_taken));
+                }
+                if (!complete) {
+                    float *sm = slot_m(slot, tile_x, D);
+                    sm[row] = m_ref;
+                    sm[kRows + row] = l_run;
+                    if (row == 0 && tile_x == 0) {
+                        SlotHead *hd = reinterpret_cast<SlotHead *>(slot);
+                        hd->s = a.s;
+                        hd->h = a.h;
+                        hd->tok0 = a.tok0;
+                        hd->ntiles = per;
+                        if (first_part) {
+                            // Cut at its start and finished here: this CTA's merge joins it.
+                            hd->start_tile = from.tile - a.t0;
+                            hd->total_tiles = T;
+                            hd->first_cta = misc->first_cta;
+                            hd->flag = a.t0 > 0 && a.t1 == q.nt ? 1 : 0;
+                        }
+                    }
+                }
+            }
+            if (joined) ++joins;
+            k += nsteps;
+            ktile += a.t1 - a.t0;
+            walk.advance();
+        }
+        if (!alive) give_up();
+        tc_fence_before();
+    }
+
+    __syncthreads();
+    if (warp == 10) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// grid (CTAs, D / 16, query tiles of a block), 128 threads: where CTA c's first
+// segment was cut at its start and ends in c, join its parts.  Thread <-> query
+// row, 16 elements of the head; O^T in the slots makes the reads whole lines.
+template <int D>
+__global__ void __launch_bounds__(kRows)
+rows_merge_kernel(const RowsParams p, int C, int slot_tiles) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const size_t slot_sz = slot_bytes<D>(slot_tiles);
+    const int c = blockIdx.x, x = blockIdx.z, row = threadIdx.x, d0 = blockIdx.y * 16;
+    const SlotHead *hd = reinterpret_cast<const SlotHead *>(slot_at(p, slot_sz, c, 0));
+    if (hd->flag != 1 || x >= hd->ntiles) return;
+    const int64_t start = hd->start_tile, T = hd->total_tiles;
+    const int s = hd->s, h = hd->h;
+    auto range_beg = [&](int cc) -> int64_t {
+        return cc < C ? reinterpret_cast<const SlotHead *>(slot_at(p, slot_sz, cc, 0))->range_beg : T;
+    };
+    const int lgG = __ffs(p.num_heads / p.num_kv_heads) - 1;
+    const int tok = hd->tok0 + x * (kRows >> lgG) + (row >> lgG);
+    const int q0 = p.cu_q_lens[s];
+    if (tok >= p.cu_q_lens[s + 1] - q0) return;
+    float M = -INFINITY, l = 0.f, o[16];
+#pragma unroll
+    for (int n = 0; n < 16; ++n) o[n] = 0.f;
+    // Contributors: the CTAs from first_cta to c whose range is not empty.
+    int64_t rb = range_beg(hd->first_cta);
+#pragma unroll 2
+    for (int cc = hd->first_cta; cc <= c; ++cc) {
+        const int64_t rn = range_beg(cc + 1);
+        const bool some = rn > rb;
+        char *slot = slot_at(p, slot_sz, cc, rb >= start ? 0 : 1);
+        rb = rn;
+        if (!some) continue;
+        const float *sm = slot_m(slot, x, D) + row;
+        const float m = sm[0], lp = sm[kRows];
+        float v[16];
+#pragma unroll
+        for (int n = 0; n < 16; ++n) v[n] = sm[(2 + d0 + n) * kRows];
+        const float mm = fmaxf(M, m);
+        const float fa = rescale(M, mm), fb = rescale(m, mm);
+        l = l * fa + lp * fb;
+#pragma unroll
+        for (int n = 0; n < 16; ++n) o[n] = o[n] * fa + v[n] * fb;
+        M = mm;
+    }
+    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+#pragma unroll
+    for (int n = 0; n < 16; ++n) o[n] *= inv;
+    const int G = 1 << lgG;
+    store_row<16>(p, (static_cast<size_t>(q0 + tok) * p.num_heads + h * G + (row & (G - 1))) * static_cast<size_t>(D) + d0,
+                  o);
+}
+
+// ---------------------------------------------------------------- host side
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+        else
+            cudaGetLastError();
+    });
+    return fn;
+}
+
+// A tiled bf16 map with the 128-byte swizzle the MMA descriptors expect.
+bool encode(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
+            const cuuint32_t *box) {
+    auto enc = encoder();
+    if (!enc) return false;
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Blocks of two query tiles exist where a sequence can have more rows than one holds.
+bool two_tiles(int num_heads, int num_kv_heads, int max_q_len) {
+    return max_q_len > kRows / (num_heads / num_kv_heads);
+}
+
+template <int D, bool TWO>
+cudaError_t launch(const RowsParams &p, cudaStream_t stream) {
+    using C_ = Cfg<D, TWO>;
+    const cuuint64_t Dd = D, Hkv = p.num_kv_heads, B = p.block_size;
+    const cuuint64_t P = p.num_blocks > 0 ? p.num_blocks : 1;
+    const int G = p.num_heads / p.num_kv_heads;
+    // K and V: one box per (page, KV head) holding its B rows as B / 8 blocks of
+    // [half][8 rows][64] (dimensions: 64 elements; row within the block; half, 128
+    // bytes apart; 8-row block, page * B / 8 + block; KV head).
+    const cuuint64_t pdims[5] = {64, 8, Dd / 64, P * (B / 8), Hkv};
+    const cuuint64_t pstr[4] = {Hkv * Dd * 2, 128, 8 * Hkv * Dd * 2, Dd * 2};
+    const cuuint32_t pbox[5] = {64, 8, static_cast<cuuint32_t>(Dd / 64), static_cast<cuuint32_t>(B / 8), 1};
+    // Queries [total_q, H, D]: box (64 elements, G heads, q_box tokens), row =
+    // token * G + head; no more tokens than a sequence has, rounded up to a power of
+    // two.
+    int q_box = kRows / G;
+    if (!TWO)
+        while (q_box > 1 && q_box / 2 >= p.max_q_len) q_box /= 2;
+    const int q_slots = TWO || q_box * G <= kRows / 2 ? 2 : 1;
+    const cuuint64_t qdims[3] = {Dd, static_cast<cuuint64_t>(p.num_heads), static_cast<cuuint64_t>(p.total_q)};
+    const cuuint64_t qstr[2] = {Dd * 2, Dd * p.num_heads * 2};
+    const cuuint32_t qbox[3] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(q_box)};
+    CUtensorMap mk, mv, mq;
+    if (!encode(&mq, p.q, 3, qdims, qstr, qbox)) return cudaErrorInvalidValue;
+    if (p.k_cache) {
+        if (!encode(&mk, p.k_cache, 5, pdims, pstr, pbox) || !encode(&mv, p.v_cache, 5, pdims, pstr, pbox))
+            return cudaErrorInvalidValue;
+    } else {
+        mk = mv = mq;                    // no sequence can have keys: never read
+    }
+    constexpr int smem = static_cast<int>(1024 + C_::kEnd + sizeof(Misc<C_::kKS, C_::kVS, C_::kMasks>));
+    {
+        const cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(rows_attention_kernel<D, TWO>), smem);
+        if (e != cudaSuccess) return e;
+    }
+    // No more CTAs than the longest sequences could have key tiles.
+    int C = std::min(sm_count(), kRowsMaxCtas);
+    if (C <= 0) return cudaErrorNoDevice;
+    const int64_t qt = kRows / G;
+    const int64_t tiles = static_cast<int64_t>(p.num_seqs) * p.num_kv_heads * ((p.max_q_len + qt - 1) / qt) *
+                          ((static_cast<int64_t>(p.max_seq_len) + kKeys - 1) / kKeys);
+    C = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(C, tiles)));
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(C);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, rows_attention_kernel<D, TWO>, mk, mv, mq, p, q_box, q_slots);
+    if (e != cudaSuccess || !p.slots) return e;          // without slots nothing is cut
+    cfg.gridDim = dim3(C, D / 16, TWO ? 2 : 1);
+    cfg.blockDim = dim3(kRows);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, rows_merge_kernel<D>, p, C, TWO ? 2 : 1);
+}
+
+}  // namespace
+
+size_t rows_workspace_bytes(int num_heads, int num_kv_heads, int head_dim, int max_q_len) {
+    const int tiles = two_tiles(num_heads, num_kv_heads, max_q_len) ? 2 : 1;
+    return 2 * kRowsMaxCtas * (head_dim == 64 ? slot_bytes<64>(tiles) : slot_bytes<128>(tiles));
+}
+
+cudaError_t launch_rows_attention(const RowsParams &p, cudaStream_t stream) {
+    const bool two = two_tiles(p.num_heads, p.num_kv_heads, p.max_q_len);
+    if (p.head_dim == 64) return two ? launch<64, true>(p, stream) : launch<64, false>(p, stream);
+    return two ? launch<128, true>(p, stream) : launch<128, false>(p, stream);
+}
+
+}  // namespace pk

@@ -1,0 +1,228 @@
+// The accepted path of each tree of drafted tokens, and the move of its K and V
+// rows together in the paged cache.
+#include "../../include/pagedkv_tree.h"
+#include "common.cuh"
+
+namespace {
+
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                             Args... args) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
+// ------------------------------------------------------------------ accept_tree
+// One CTA per sequence.  next[p], the lowest node c with parent p and the token
+// that the target chose after p, is a minimum over the nodes, so all nodes are
+// looked at side by side; the path is then a chain of shared-memory reads by one
+// thread.  Bound by two dependent trips to memory (node -> its parent's target).
+constexpr int kAcceptThreads = 128;
+constexpr int kMaxTree = 8192;      // next[] and the path in 48 KB
+constexpr int kNone = 0x7fffffff;
+
+__global__ void __launch_bounds__(kAcceptThreads)
+accept_tree_kernel(int32_t *accepted, int32_t *num_accepted, int64_t *next_tokens, int32_t *new_seq_lens,
+                   const int64_t *draft_tokens, const int32_t *parents, const int64_t *target_tokens, int total_q,
+                   const int32_t *cu_q_lens, int max_q_len, const int32_t *seq_lens, unsigned int *err) {
+    extern __shared__ int32_t next[];
+    __shared__ int path_len;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int s = blockIdx.x;
+    const int L = seq_lens[s], q0 = cu_q_lens[s], q1 = cu_q_lens[s + 1];
+    const bool bad = L < 0 || q0 < 0 || q1 < q0 || q1 > total_q || q1 - q0 > max_q_len || q1 - q0 > L;
+    const int n = bad ? 0 : q1 - q0;
+    if (bad && threadIdx.x == 0) pk::set_error(err, PK_DEVERR_SEQ_LEN);
+    for (int i = threadIdx.x; i < n; i += kAcceptThreads) next[i] = kNone;
+    __syncthreads();
+    for (int c = 1 + threadIdx.x; c < n; c += kAcceptThreads) {
+        const int p = parents[q0 + c];
+        if (p < 0 || p >= c) continue;
+        if (draft_tokens[q0 + c] == target_tokens[q0 + p]) atomicMin(&next[p], c);
+    }
+    __syncthreads();
+    // The path in place: entry i of the path goes where next[] of a node before it
+    // was (path nodes increase, so node i's entry has been read when i <= node).
+    if (threadIdx.x == 0) {
+        int len = 0, last = -1;
+        for (int node = n > 0 ? 0 : kNone; node != kNone;) {
+            const int following = next[node];
+            next[len++] = node;
+            last = node;
+            node = following;
+        }
+        path_len = len;
+        num_accepted[s] = len;
+        next_tokens[s] = last >= 0 ? target_tokens[q0 + last] : -1;
+        new_seq_lens[s] = L - n + len;
+    }
+    __syncthreads();
+    const int len = path_len;
+    int32_t *row = accepted + static_cast<size_t>(s) * max_q_len;
+    for (int i = threadIdx.x; i < max_q_len; i += kAcceptThreads) row[i] = i < len ? next[i] : -1;
+}
+
+// ------------------------------------------------------------------ keep_tokens
+// grid (sequences, layers x 2 [K, V], chunks of a token's row).  A pass takes as
+// many tokens as give every thread kKeepVecs 16-byte vectors: all are read, then
+// all are written.  Lists increase strictly, so accepted[i] >= i, and a row that a
+// pass writes (i) comes before every row that a later pass reads (accepted[j] >= j
+// > i).  Bound by memory: two rows moved per kept token that is not in its place.
+constexpr int kKeepThreads = 128;
+constexpr int kKeepVecs = 8;
+constexpr int kKeepColumns = 128;    // vectors of a row in one chunk (at most)
+
+struct KeepParams {
+    uint4 *k_cache, *v_cache;                 // one layer, or
+    uint4 *const *k_layers, *const *v_layers; // a device array of them
+    const int32_t *block_tables;
+    int max_blocks_per_seq;
+    const int32_t *seq_lens, *cu_q_lens, *accepted;
+    int accepted_stride;
+    const int32_t *num_accepted;
+    int row_vecs, num_blocks, log2_block;
+    unsigned int *err;
+};
+
+__global__ void __launch_bounds__(kKeepThreads)
+keep_tokens_kernel(const KeepParams p) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int s = blockIdx.x;
+    const bool reports = blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0;
+    const int L = p.seq_lens[s], q0 = p.cu_q_lens[s], q1 = p.cu_q_lens[s + 1];
+    const int n = p.num_accepted[s];
+    const int32_t *list = p.accepted + static_cast<size_t>(s) * p.accepted_stride;
+    const int64_t cap = static_cast<int64_t>(p.max_blocks_per_seq) << p.log2_block;
+    if (L < 0 || L > cap || q0 < 0 || q1 < q0 || q1 - q0 > L) {
+        if (reports) pk::set_error(p.err, PK_DEVERR_SEQ_LEN);
+        return;
+    }
+    const int nodes = q1 - q0;
+    bool bad = n < 0 || n > nodes || n > p.accepted_stride;
+    if (!bad)
+        for (int i = threadIdx.x; i < n; i += kKeepThreads) {
+            const int at = list[i];
+            bad |= at >= nodes || at <= (i > 0 ? list[i - 1] : -1);
+        }
+    if (__syncthreads_or(bad)) {
+        if (reports) pk::set_error(p.err, PK_DEVERR_DRAFT);
+        return;
+    }
+    uint4 *cache;
+    if (p.k_layers) {
+        cache = (blockIdx.y & 1 ? p.v_layers : p.k_layers)[blockIdx.y >> 1];
+        if (!cache || (reinterpret_cast<uintptr_t>(cache) & 15u)) {
+            if (s == 0 && blockIdx.z == 0 && threadIdx.x == 0) pk::set_error(p.err, PK_DEVERR_POINTER);
+            return;
+        }
+    } else {
+        cache = blockIdx.y & 1 ? p.v_cache : p.k_cache;
+    }
+    const int32_t *table = p.block_tables + static_cast<size_t>(s) * p.max_blocks_per_seq;
+    const int B1 = (1 << p.log2_block) - 1;
+    const int base = L - nodes;
+    const int col0 = blockIdx.z * kKeepColumns;
+    const int cols = min(kKeepColumns, p.row_vecs - col0);
+    const int per = kKeepThreads * kKeepVecs / cols;          // tokens of a pass
+    for (int i0 = 0; i0 < n; i0 += per) {
+        const int items = min(per, n - i0) * cols;
+        uint4 buf[kKeepVecs];
+        int64_t dst[kKeepVecs];
+#pragma unroll
+        for (int u = 0; u < kKeepVecs; ++u) {
+            const int e = u * kKeepThreads + threadIdx.x;
+            dst[u] = -1;
+            if (e >= items) continue;
+            const int i = i0 + e / cols, col = e % cols;
+            const int from = list[i];
+            if (from == i) continue;                          // in its place
+            const int sp = base + from, dp = base + i;
+            const int sb = table[sp >> p.log2_block], db = table[dp >> p.log2_block];
+            if (sb < 0 || sb >= p.num_blocks || db < 0 || db >= p.num_blocks) {
+                pk::set_error(p.err, PK_DEVERR_BLOCK_ID);
+                continue;
+            }
+            buf[u] = cache[((static_cast<int64_t>(sb) << p.log2_block) + (sp & B1)) * p.row_vecs + col0 + col];
+            dst[u] = ((static_cast<int64_t>(db) << p.log2_block) + (dp & B1)) * p.row_vecs + col0 + col;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < kKeepVecs; ++u)
+            if (dst[u] >= 0) cache[dst[u]] = buf[u];
+    }
+}
+
+int keep(KeepParams &p, const void *const *ptrs, int num_seqs, int num_layers, int num_kv_heads, int head_dim,
+         int block_size, bool check_alignment, pk_stream_t stream) {
+    if (num_seqs < 0 || p.max_blocks_per_seq < 0 || p.accepted_stride < 0 || num_kv_heads <= 0 || p.num_blocks < 0 ||
+        block_size <= 0 || num_layers < 0)
+        return PK_ERR_SHAPE;
+    if (head_dim != 64 && head_dim != 128) return PK_ERR_UNSUPPORTED;
+    if (block_size != 8 && block_size != 16 && block_size != 32) return PK_ERR_UNSUPPORTED;
+    if (num_seqs > 65535 || num_layers > 32767 || num_kv_heads > 65535) return PK_ERR_SHAPE;
+    if (num_seqs == 0 || num_layers == 0 || p.accepted_stride == 0 || p.max_blocks_per_seq == 0) return PK_OK;
+    if (!ptrs[0] || !ptrs[1] || !p.block_tables || !p.seq_lens || !p.cu_q_lens || !p.accepted || !p.num_accepted)
+        return PK_ERR_NULL;
+    if (check_alignment && (!pk::aligned16(ptrs[0]) || !pk::aligned16(ptrs[1]))) return PK_ERR_ALIGNMENT;
+    p.row_vecs = num_kv_heads * head_dim / 8;
+    p.log2_block = block_size == 8 ? 3 : block_size == 16 ? 4 : 5;
+    p.err = pk::error_word_ptr();
+    if (!p.err) return PK_ERR_NO_DEVICE;
+    const dim3 grid(num_seqs, 2 * num_layers, (p.row_vecs + kKeepColumns - 1) / kKeepColumns);
+    return launch_dependent(keep_tokens_kernel, grid, kKeepThreads, 0, reinterpret_cast<cudaStream_t>(stream), p) ==
+                   cudaSuccess ? PK_OK : PK_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" int pk_accept_tree(int32_t *accepted, int32_t *num_accepted, int64_t *next_tokens, int32_t *new_seq_lens,
+                              const int64_t *draft_tokens, const int32_t *parents, const int64_t *target_tokens,
+                              int total_q, const int32_t *cu_q_lens, int max_q_len, const int32_t *seq_lens,
+                              int num_seqs, pk_stream_t stream) {
+    if (total_q < 0 || max_q_len < 0 || num_seqs < 0) return PK_ERR_SHAPE;
+    if (max_q_len > kMaxTree) return PK_ERR_UNSUPPORTED;
+    if (num_seqs == 0) return PK_OK;
+    if (!num_accepted || !next_tokens || !new_seq_lens || !cu_q_lens || !seq_lens || (max_q_len > 0 && !accepted) ||
+        (total_q > 0 && (!draft_tokens || !parents || !target_tokens)))
+        return PK_ERR_NULL;
+    unsigned int *err = pk::error_word_ptr();
+    if (!err) return PK_ERR_NO_DEVICE;
+    return launch_dependent(accept_tree_kernel, dim3(num_seqs), kAcceptThreads, max_q_len * sizeof(int32_t),
+                            reinterpret_cast<cudaStream_t>(stream), accepted, num_accepted, next_tokens, new_seq_lens,
+                            draft_tokens, parents, target_tokens, total_q, cu_q_lens, max_q_len, seq_lens, err) ==
+                   cudaSuccess ? PK_OK : PK_ERR_CUDA;
+}
+
+extern "C" int pk_keep_tokens(void *k_cache, void *v_cache, const int32_t *block_tables, int max_blocks_per_seq,
+                              const int32_t *seq_lens, const int32_t *cu_q_lens, const int32_t *accepted,
+                              int accepted_stride, const int32_t *num_accepted, int num_seqs, int num_kv_heads,
+                              int head_dim, int num_blocks, int block_size, pk_stream_t stream) {
+    const void *ptrs[2] = {k_cache, v_cache};
+    KeepParams p{static_cast<uint4 *>(k_cache), static_cast<uint4 *>(v_cache), nullptr, nullptr, block_tables,
+                 max_blocks_per_seq, seq_lens, cu_q_lens, accepted, accepted_stride, num_accepted, 0, num_blocks, 0,
+                 nullptr};
+    return keep(p, ptrs, num_seqs, 1, num_kv_heads, head_dim, block_size, true, stream);
+}
+
+extern "C" int pk_keep_tokens_layers(void *const *k_cache_layers, void *const *v_cache_layers,
+                                     const int32_t *block_tables, int max_blocks_per_seq, const int32_t *seq_lens,
+                                     const int32_t *cu_q_lens, const int32_t *accepted, int accepted_stride,
+                                     const int32_t *num_accepted, int num_seqs, int num_layers, int num_kv_heads,
+                                     int head_dim, int num_blocks, int block_size, pk_stream_t stream) {
+    const void *ptrs[2] = {k_cache_layers, v_cache_layers};
+    KeepParams p{nullptr, nullptr, reinterpret_cast<uint4 *const *>(k_cache_layers),
+                 reinterpret_cast<uint4 *const *>(v_cache_layers), block_tables, max_blocks_per_seq, seq_lens, cu_q_lens,
+                 accepted, accepted_stride, num_accepted, 0, num_blocks, 0, nullptr};
+    return keep(p, ptrs, num_seqs, num_layers, num_kv_heads, head_dim, block_size, false, stream);
+}
