@@ -25,7 +25,7 @@
 // kernel joins its parts.
 //
 // Steps.  Step k belongs to group x = k mod 2.  A block of one tile has a step per
-// key tile, a block of two has two.  The MMA thread issues, at step k, P.V of step
+// key tile, a block of two has two.  The MMA warp issues, at step k, P.V of step
 // k - 2 (the same group's last one, whose P lies where S is going) and S of step
 // k, across parts without a pause.
 //
@@ -82,6 +82,11 @@ struct Cfg {
     static_assert(kMasks > kKS + 2, "masks in flight");
 };
 
+// A tile in the MMA warp's eyes: the block has two query tiles; this is the first tile
+// of its part for the group at hand; the part's last tile; the query buffer of a block
+// of one; keys of the 16-key groups are not there; the number of those groups.
+constexpr int kMetaTwo = 1, kMetaFirst = 2, kMetaDone = 4, kMetaBuffer = 16, kMetaStale = 32, kMetaKeysShift = 8;
+
 struct Pos {          // a place in the flattened (segment, key tile) space
     int64_t tile;     // index of the key tile
     int32_t s, h, j, t;
@@ -100,6 +105,8 @@ struct Misc {
     int abort;
     int never;
     uint32_t mask[MASKS][4];      // valid keys of a tile
+    int4 meta[MASKS];             // of a tile, for the MMA warp: kMeta* bits (y), and which fill of
+                                  // its query buffer(s) it reads (z, w)
     union {
         struct {
             int64_t tiles[kThreads / 32 + 1], costs[kThreads / 32 + 1];
@@ -302,18 +309,12 @@ __device__ __forceinline__ int64_t plan(const RowsParams &p, M *misc, int lgG, i
 }
 
 __device__ __forceinline__ float ex2(float x) { return fast_exp2(x); }
-// Three-input max / min (NaN inputs are skipped, as by fmaxf / fminf).
+// Three-input max (NaN inputs are skipped, as by fmaxf).
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
-__device__ __forceinline__ float min3(float a, float b, float c) {
-    float r;
-    asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
-
 // N results of a row, to element idx of the output (idx and N multiples of 8).
 template <int N>
 __device__ __forceinline__ void store_row(const RowsParams &p, size_t idx, const float (&f)[N]) {
@@ -445,6 +446,7 @@ rows_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
         int issued = 0, st = 0;
         uint32_t ph = 1;
         bool ok_run = true, stalled = false;
+        int turn = 0, fill0 = 0, fill1 = 0;    // query buffers, as the warp that fills them counts
         while (ok_run && walk.next(a)) {
             const int L = walk.q.L;
             const int32_t *table = p.block_tables + static_cast<size_t>(a.s) * MB;
@@ -485,11 +487,21 @@ rows_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                         bits = (nrows >= 32 ? 0xffffffffu : ((1u << nrows) - 1u)) << (r0 & 31);
                     }
                     const int word = r0 >> 5;
+                    // Rows that P.V reads and that hold no key: the end of the last 16, and
+                    // pages that are not there.
+                    const bool stale = (vlen & 15) != 0 || nok * B < static_cast<uint32_t>(vlen);
 #pragma unroll
                     for (int w = 0; w < 4; ++w) {
                         const uint32_t m = __reduce_or_sync(0xffffffffu, word == w ? bits : 0u);
                         if (lane == 0) misc->mask[issued & (C_::kMasks - 1)][w] = m;
                     }
+                    // (A block of one: a group's first tile is the part's first or second.)
+                    if (lane == 0)
+                        misc->meta[issued & (C_::kMasks - 1)] =
+                            make_int4(0, (a.two ? kMetaTwo : 0) | (t - a.t0 < (a.two ? 1 : 2) ? kMetaFirst : 0) |
+                                             (t == a.t1 - 1 ? kMetaDone : 0) | (turn ? kMetaBuffer : 0) |
+                                             (stale ? kMetaStale : 0) | ((vlen + 15) >> 4) << kMetaKeysShift,
+                                      !a.two && turn ? fill1 : fill0, fill1);
                 }
                 if (lane == 0) mbar_arrive_expect_tx(bar, nok * B * 128u * NCH);
                 __syncwarp();
@@ -502,6 +514,9 @@ rows_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                 }
                 if (t + 1 < a.t1) phys_next = fetch(t + 1);
             }
+            if (a.two || !turn) ++fill0;
+            if (a.two || turn) ++fill1;
+            if (!a.two && q_slots == 2) turn ^= 1;
             walk.advance();
         }
         if ((misc->abort || stalled) && lane == 0) {
@@ -546,103 +561,141 @@ rows_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
         __syncwarp();
     } else if (warp == 10) {
         // ================= MMA issuer =================
+        // One thread.  Steps come in order: P.V of step k - 2, then S of step k.  (A loop that probed for
+        // whichever group is ready let the groups drift a whole tile apart, each K and V
+        // slot then held that much longer: 15-30 % slower.)
         if (lane == 0) {
-            constexpr uint32_t kIdescS = idesc_bf16(kRows, kKeys, 0, 0);   // A = Q, B = K, both K-major
-            constexpr uint32_t kIdescO = idesc_bf16(kRows, D, 0, 1);       // A = P (TMEM), B = V (MN-major)
-            bool alive = true;
-            int k = 0;                         // step
-            int ks = 0, kph = 0;               // K ring
-            int vs = 0, vph = 0;               // V ring: the next tile whose P.V comes
-            // What P.V needs of the last step of either group.
-            // (Bit x is group x's; in registers, as no array with a runtime index is.)
-            uint32_t pend = 0, pfirst = 0, plast = 0;
-            uint32_t jobs = 0;                 // parity of the P.V issued
-            bool vready = false;               // the V tile of the ring's head has been waited for
-            auto pv = [&](int x) {
-                alive = mbar_wait(smem_u32(&misc->p_full[x]), (jobs >> x) & 1, &misc->abort, lim) &&
-                        (vready || mbar_wait(smem_u32(&misc->vfull[vs]), vph, &misc->abort, lim));
-                if (!alive) return;
-                vready = true;
-                tc_fence_after();
-                const uint32_t vbase = base + C_::kVOff + vs * kTile;
-                const uint32_t acol = tmem + kTmemS + x * 128;
+        constexpr uint32_t kIdescO = idesc_bf16(kRows, D, 0, 1);           // A = P (TMEM), B = V (MN-major)
+        constexpr uint32_t kIdescS = idesc_bf16(kRows, kKeys, 0, 0);       // A = Q, B = K, both K-major
+        // Descriptors of the rings' starts; an address moves on in 16-byte units.
+        const uint64_t qdesc = smem_desc(base, 16, 1024, kLayoutSw128);
+        const uint64_t kdesc = smem_desc(base + C_::kKOff, 16, kAtomStride, kLayoutSw128);
+        const uint64_t vdesc = smem_desc(base + C_::kVOff, 1024, kAtomStride, kLayoutSw128);
+        auto wait = [&](uint64_t *bar, int phase) -> bool {
+            return mbar_wait(smem_u32(bar), phase & 1, &misc->abort, lim);
+        };
+        bool alive = true;
+        int kslot = 0, kpar = 0, vslot = 0, vpar = 0;
+        bool vready = false;                   // the V tile at the ring's head has been waited for
+        uint32_t pend = 0, jobs = 0;           // by group (bit x): a P.V to come; parity of those issued
+        int pflags0 = 0, pflags1 = 0, pkt0 = 0, pkt1 = 0;   // of the step whose P.V is to come
+        auto pv = [&](int x, bool last_use) {
+            const int flags = x ? pflags1 : pflags0, kt = x ? pkt1 : pkt0;
+            alive = wait(&misc->p_full[x], jobs >> x) && (vready || wait(&misc->vfull[vslot], vpar));
+            if (!alive) return;
+            const int n16 = flags >> kMetaKeysShift;
+            if (!vready && (flags & kMetaStale)) {
+                // V rows of keys outside the sequence or behind a bad table entry may hold
+                // stale or non-finite bits, which weights of 0 do not cancel: zero those
+                // that the product reads.
+#pragma unroll 1
+                for (int q4 = 0; q4 < 4; ++q4) {
+                    const int nrow = max(0, min(32, n16 * 16 - 32 * q4));
+                    uint32_t gone = ~misc->mask[kt & (C_::kMasks - 1)][q4];
+                    if (nrow < 32) gone &= (1u << nrow) - 1u;
+                    while (gone) {
+                        const int r = 32 * q4 + __ffs(gone) - 1;
+                        gone &= gone - 1;
+                        uint8_t *vrow = smem + C_::kVOff + vslot * kTile + (r >> 3) * kAtomStride + (r & 7) * 128;
 #pragma unroll
-                for (int kk = 0; kk < kKeys / 16; ++kk) {
-                    // Keys 16kk .. 16kk+15: 8-row blocks 2kk and 2kk + 1; the
-                    // two 64-element halves 1,024 bytes apart.
-                    const uint64_t b = smem_desc(vbase + kk * 2 * kAtomStride, 1024, kAtomStride, kLayoutSw128);
-                    mma_bf16_tmem_a(tmem + kTmemO + x * 128, acol + kk * 8, b, kIdescO,
-                                    (!((pfirst >> x) & 1) || kk > 0) ? 1u : 0u);
+                        for (int n = 0; n < 8 * NCH; ++n)
+                            *reinterpret_cast<uint4 *>(vrow + (n >> 3) * 1024 + (n & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                }
+                fence_proxy_async_smem();
+            }
+            vready = true;
+            tc_fence_after();
+            {
+                const uint32_t acol = tmem + kTmemS + x * 128, ocol = tmem + kTmemO + x * 128;
+                const uint64_t vd = vdesc + static_cast<uint32_t>(vslot) * (kTile >> 4);
+                const uint32_t acc = flags & kMetaFirst ? 0u : 1u;
+                // Keys 16kk .. 16kk+15: 8-row blocks 2kk and 2kk + 1; the two 64-element
+                // halves 1,024 bytes apart.
+                auto product = [&](int kk) {
+                    mma_bf16_tmem_a(ocol, acol + kk * 8, vd + kk * (2 * kAtomStride >> 4), kIdescO, kk > 0 ? 1u : acc);
+                };
+                if (n16 == kKeys / 16) {
+#pragma unroll
+                    for (int kk = 0; kk < kKeys / 16; ++kk) product(kk);
+                } else {
+#pragma unroll 1
+                    for (int kk = 0; kk < n16; ++kk) product(kk);
                 }
                 mma_commit(smem_u32(&misc->pv_done[x]));
-                if ((plast >> x) & 1) {        // the tile's last product: its V slot is free
-                    mma_commit(smem_u32(&misc->vempty[vs]));
-                    vready = false;
-                    if (++vs == VS) {
-                        vs = 0;
-                        vph ^= 1;
-                    }
-                }
-                jobs ^= 1u << x;
-                pend &= ~(1u << x);
-            };
-            uint32_t uses = 0;                 // parity of the parts that read each query buffer
-            int turn = 0;
-            while (alive && walk.next(a)) {
-                const int sl1 = turn;          // buffer of a block of one tile
-                if (!a.two && q_slots == 2) turn ^= 1;
-                const int per = a.two ? 2 : 1;
-                uint32_t started = 0;
-                for (int t = a.t0; t < a.t1 && alive; ++t) {
-                    bool kready = false;
-                    for (int y = 0; y < per && alive; ++y, ++k) {
-                        const int x = k & 1;
-                        if ((pend >> x) & 1) pv(x);
-                        if (!alive) break;
-                        const int sl = a.two ? x : sl1;
-                        if (t == a.t0)
-                            alive = mbar_wait(smem_u32(&misc->qfull[sl]), (uses >> sl) & 1, &misc->abort, lim);
-                        if (alive && !kready)
-                            alive = mbar_wait(smem_u32(&misc->kfull[ks]), kph, &misc->abort, lim);
-                        if (!alive) break;
-                        kready = true;
-                        tc_fence_after();
-                        const uint32_t kbase = base + C_::kKOff + ks * kTile;
-                        const uint32_t qbase = base + sl * q_slot;
-#pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint64_t qa = smem_desc(qbase + (kk >> 2) * q_chunk + (kk & 3) * 32, 16, 1024,
-                                                          kLayoutSw128);
-                            const uint64_t kb = smem_desc(kbase + (kk >> 2) * 1024u + (kk & 3) * 32, 16, kAtomStride,
-                                                          kLayoutSw128);
-                            mma_bf16(tmem + kTmemS + x * 128, qa, kb, kIdescS, kk > 0 ? 1u : 0u);
-                        }
-                        mma_commit(smem_u32(&misc->s_full[x]));
-                        if (t == a.t1 - 1) {   // the part's last scores from this buffer
-                            mma_commit(smem_u32(&misc->qempty[sl]));
-                            uses ^= 1u << sl;
-                        }
-                        const uint32_t bit = 1u << x;
-                        pend |= bit;
-                        pfirst = (started & bit) ? pfirst & ~bit : pfirst | bit;
-                        plast = y == per - 1 ? plast | bit : plast & ~bit;
-                        started |= bit;
-                    }
-                    if (!alive) break;
-                    mma_commit(smem_u32(&misc->kempty[ks]));
-                    if (++ks == KS) {
-                        ks = 0;
-                        kph ^= 1;
-                    }
-                }
-                walk.advance();
+                if (last_use) mma_commit(smem_u32(&misc->vempty[vslot]));
             }
-            for (int e = 0; e < 2 && alive; ++e, ++k)
-                if ((pend >> (k & 1)) & 1) pv(k & 1);
-            if (!alive) give_up();
-            // Let every issued MMA finish before the CTA can release TMEM.
-            mma_commit(smem_u32(&misc->drain));
-            mbar_wait(smem_u32(&misc->drain), 0, &misc->never, lim);
+            if (last_use) {
+                vready = false;
+                if (++vslot == VS) {
+                    vslot = 0;
+                    vpar ^= 1;
+                }
+            }
+            jobs ^= 1u << x;
+            pend &= ~(1u << x);
+        };
+        // P.V of group x: the last use of its V tile if the block has one query tile, or if
+        // it is the later of the two groups (the other's P.V of this tile has been issued).
+        auto flush = [&](int x) {
+            if (!((pend >> x) & 1)) return;
+            const bool two = (x ? pflags1 : pflags0) & kMetaTwo;
+            pv(x, !two || vready);
+        };
+        int k = 0;                             // step
+        for (int kt = 0; kt < static_cast<int>(n_tiles) && alive; ++kt) {
+            bool kready = false;
+            int per = 1;
+            for (int y = 0; y < per && alive; ++y, ++k) {
+                const int x = k & 1;
+                flush(x);
+                if (!alive) break;
+                if (!kready && !wait(&misc->kfull[kslot], kpar)) {
+                    alive = false;
+                    break;
+                }
+                kready = true;
+                const int4 mt = misc->meta[kt & (C_::kMasks - 1)];
+                const bool two = mt.y & kMetaTwo;
+                per = two ? 2 : 1;
+                const int sl = two ? x : (mt.y & kMetaBuffer ? 1 : 0);
+                if ((mt.y & kMetaFirst) && !wait(&misc->qfull[sl], two && x ? mt.w : mt.z)) {
+                    alive = false;
+                    break;
+                }
+                tc_fence_after();
+                {
+                    const int n16 = mt.y >> kMetaKeysShift;
+                    const uint64_t kd = kdesc + static_cast<uint32_t>(kslot) * (kTile >> 4);
+                    const uint64_t qd = qdesc + ((static_cast<uint32_t>(sl) * q_slot) >> 4);
+                    const uint32_t idesc = n16 == kKeys / 16 ? kIdescS : idesc_bf16(kRows, n16 * 16, 0, 0);
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        mma_bf16(tmem + kTmemS + x * 128, qd + (((kk >> 2) * q_chunk + (kk & 3) * 32) >> 4),
+                                 kd + (((kk >> 2) * 1024u + (kk & 3) * 32) >> 4), idesc, kk > 0 ? 1u : 0u);
+                    mma_commit(smem_u32(&misc->s_full[x]));
+                    if (y == per - 1) mma_commit(smem_u32(&misc->kempty[kslot]));
+                    if (mt.y & kMetaDone) mma_commit(smem_u32(&misc->qempty[sl]));   // the part's last scores
+                }
+                pend |= 1u << x;
+                if (x) {
+                    pflags1 = mt.y;
+                    pkt1 = kt;
+                } else {
+                    pflags0 = mt.y;
+                    pkt0 = kt;
+                }
+            }
+            if (++kslot == KS) {
+                kslot = 0;
+                kpar ^= 1;
+            }
+        }
+        for (int e = 0; e < 2 && alive; ++e, ++k) flush(k & 1);
+        if (!alive) give_up();
+        // Let every issued MMA finish before the CTA can release TMEM.
+        mma_commit(smem_u32(&misc->drain));
+        mbar_wait(smem_u32(&misc->drain), 0, &misc->never, lim);
         }
         __syncwarp();
     } else {
@@ -674,13 +727,24 @@ rows_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
             const int ntok = min(q.qn - tok0, QT);
             const bool busy = (quad * 32) >> lgG < ntok;      // this warp has a row in use
             const int base_pos = q.L - q.qn;                  // position of the tree's node 0
-            const uint32_t *mrow_bits = p.tree_mask
+            const uint32_t *mrow_bits = p.tree_mask && busy
                 ? p.tree_mask + static_cast<size_t>(q.q0 + tok0 + min(rr, ntok - 1)) * p.mask_words : nullptr;
+            // The mask words that 128 keys of tile t can touch, read a step ahead:
+            // all ones before node 0 (the context), zeros behind the row's words.
+            uint32_t mw[5];
+            auto fetch_mask = [&](int t) {
+                const int at = (t * kKeys - base_pos) >> 5;          // (rounds down)
+                if (!mrow_bits || t >= a.t1 || at <= -5) return;     // (-5: nothing of the tree in these keys)
+#pragma unroll
+                for (int w = 0; w < 5; ++w)
+                    mw[w] = at + w < 0 ? 0xffffffffu : (at + w < p.mask_words ? mrow_bits[at + w] : 0u);
+            };
             float m_ref = -INFINITY, l_run = 0.f;
             bool first = true;
             // This group's first step, and from there every second one (one tile)
             // or every key tile (two).
-            int i0 = (k & 1) == x ? 0 : 1;
+            const int i0 = (k & 1) == x ? 0 : 1;
+            fetch_mask(a.t0 + (a.two ? 0 : i0));
             for (int i = i0; i < nsteps; i += 2) {
                 const int t = a.t0 + (a.two ? i >> 1 : i);
                 const int kt = ktile + (a.two ? i >> 1 : i);
@@ -689,85 +753,129 @@ rows_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                     break;
                 }
                 tc_fence_after();
-                uint32_t msk[4];
-#pragma unroll
-                for (int w = 0; w < 4; ++w) msk[w] = misc->mask[kt & (C_::kMasks - 1)][w];
-                // V rows of keys outside the sequence or behind a bad table entry
-                // may hold stale or non-finite bits; the MMA multiplies them by 0,
-                // so the first group to use the tile zeroes them (thread <-> key row)
-                // once V has landed.
-                const uint32_t mrow = quad == 0 ? msk[0] : quad == 1 ? msk[1] : quad == 2 ? msk[2] : msk[3];
-                const bool stale = !((mrow >> lane) & 1u) && (!a.two || (i & 1) == 0);
                 if (busy) {
                     uint32_t vis[4];
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) vis[w] = msk[w];
-                    const int over = t * kKeys + kKeys - base_pos;   // > 0: the tile holds nodes of the tree
-                    if (mrow_bits && over > 0) {
+                    for (int w = 0; w < 4; ++w) vis[w] = misc->mask[kt & (C_::kMasks - 1)][w];
+                    if (mrow_bits && ((t * kKeys - base_pos) >> 5) > -5) {
+                        const int sh = (t * kKeys - base_pos) & 31;
 #pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            // Bits of the nodes at this word's 32 keys; the keys before
-                            // node 0 are context.
-                            const int n0 = t * kKeys + 32 * w - base_pos;
-                            const int at = n0 >> 5;                  // (rounds down)
-                            const uint32_t lo = at >= 0 && at < p.mask_words ? mrow_bits[at] : (at < 0 ? 0xffffffffu : 0u);
-                            const uint32_t hi = at + 1 >= 0 && at + 1 < p.mask_words ? mrow_bits[at + 1]
-                                                                                    : (at + 1 < 0 ? 0xffffffffu : 0u);
-                            vis[w] &= __funnelshift_r(lo, hi, n0 & 31);
-                        }
+                        for (int w = 0; w < 4; ++w) vis[w] &= __funnelshift_r(mw[w], mw[w + 1], sh);
                     }
+                    fetch_mask(t + (a.two ? 1 : 2));
                     // Rows in use that see every key of the tile (warp-uniform: the
                     // tensor-memory moves below are warp-collective).
-                    const bool easy = __all_sync(0xffffffffu, rr >= ntok || (vis[0] & vis[1] & vis[2] & vis[3]) == 0xffffffffu);
-                    auto visible = [&](int kk) -> bool { return (vis[kk >> 5] >> (kk & 31)) & 1u; };
-                    // The row's max, 32 scores at a time with the next load in flight, in
-                    // eight independent chains; a masked key is NaN, which max and min
-                    // skip.  The max of c s is that of c times the largest s (c >= 0) or
-                    // smallest: rounding is monotone.
-                    auto gather = [&](auto easy_tag, auto max_tag) -> float {
-                        constexpr bool kEasy = decltype(easy_tag)::value;
-                        constexpr bool kMax = decltype(max_tag)::value;
-                        auto pick3 = [&](float e0, float e1, float e2) {
-                            return kMax ? max3(e0, e1, e2) : min3(e0, e1, e2);
-                        };
-                        float e[8];
+                    const bool idle_row = rr >= ntok;
+                    const bool easy = __all_sync(0xffffffffu, idle_row || (vis[0] & vis[1] & vis[2] & vis[3]) == 0xffffffffu);
+                    // One pass over the row: weights against the reference max as it is,
+                    // and the largest score beside them.  Only where that moves the
+                    // reference (the first tile, seldom later) is the pass made again:
+                    // S is overwritten by P after it.  P is bf16 pairs over the first
+                    // 64 columns of S (the A operand of P.V): half the tensor work of
+                    // fp32 weights at an error of 2^-9 of each; the denominator sums the
+                    // rounded weights, so that their mean stays a mean.
+                    uint32_t packed[64];
+                    float lsum;
+                    // The extreme score of a chunk joins ext: the largest for c >= 0, the
+                    // smallest otherwise, so that c times it is the largest c s (rounding
+                    // is monotone).  A masked key counts as NaN, which max and min skip.
+                    const uint32_t flip = cs >= 0.f ? 0u : 0x80000000u;      // max of -s for the min of s
+                    float tmax;
+                    if (first) {
+                        float e[4];
 #pragma unroll
-                        for (int n = 0; n < 8; ++n) e[n] = __int_as_float(0x7fffffff);
-                        uint32_t cb[2][32];
-                        tmemw::ld32(s_col, cb[0]);
-                        tmemw::wait_ld(cb[0]);
-#pragma unroll
+                        for (int u = 0; u < 4; ++u) e[u] = __int_as_float(0x7fffffff);
+#pragma unroll 1
                         for (int cc = 0; cc < 4; ++cc) {
-                            if (cc < 3) tmemw::ld32(s_col + 32 * (cc + 1), cb[(cc + 1) & 1]);
-                            auto v = [&](int n) -> float {
-                                const float sc = __uint_as_float(cb[cc & 1][n]);
-                                return kEasy || visible(cc * 32 + n) ? sc : __int_as_float(0x7fffffff);
-                            };
+                            const uint32_t m = cc == 0 ? vis[0] : cc == 1 ? vis[1] : cc == 2 ? vis[2] : vis[3];
+                            uint32_t cb[32];
+                            tmemw::ld32(s_col + 32 * cc, cb);
+                            tmemw::wait_ld(cb);
 #pragma unroll
-                            for (int n = 0; n < 32; n += 16) {
+                            for (int n = 0; n < 32; n += 8) {
 #pragma unroll
-                                for (int u = 0; u < 8; ++u) e[u] = pick3(e[u], v(n + u), v(n + 8 + u));
+                                for (int u = 0; u < 4; ++u) {
+                                    const float v0 = __uint_as_float(cb[n + u] ^ flip), v1 = __uint_as_float(cb[n + 4 + u] ^ flip);
+                                    e[u] = max3(e[u], (m >> (n + u)) & 1u ? v0 : __int_as_float(0x7fffffff),
+                                                (m >> (n + 4 + u)) & 1u ? v1 : __int_as_float(0x7fffffff));
+                                }
                             }
-                            if (cc < 3) tmemw::wait_ld(cb[(cc + 1) & 1]);
                         }
-                        const float e0 = pick3(e[0], e[1], e[2]), e1 = pick3(e[3], e[4], e[5]);
-                        return pick3(e0, e1, kMax ? fmaxf(e[6], e[7]) : fminf(e[6], e[7]));
-                    };
-                    const float ext = easy ? (cs >= 0.f ? gather(std::true_type{}, std::true_type{})
-                                                        : gather(std::true_type{}, std::false_type{}))
-                                           : (cs >= 0.f ? gather(std::false_type{}, std::true_type{})
-                                                        : gather(std::false_type{}, std::false_type{}));
-                    // No visible key (NaN): no candidate for the reference max.
-                    const float tmax = ext == ext ? ext * cs : -INFINITY;
-                    const bool need = tmax > m_ref + kRescaleLog2;
-                    if (__any_sync(0xffffffffu, need)) {
-                        // Move this row's reference max and rescale its O (complete up
-                        // to this group's last step) and denominator; rare after the
-                        // first tile.
-                        const float mn = need ? tmax : m_ref;
+                        const float ext = fmaxf(max3(e[0], e[1], e[2]), e[3]);
+                        // No visible key (NaN): no candidate for the reference max.
+                        m_ref = ext == ext ? __uint_as_float(__float_as_uint(ext) ^ flip) * cs : -INFINITY;
+                    }
+                    // (Two moves at most: scores whose rounding exceeds the threshold would
+                    // ask for ever.)
+                    for (int pass = 0;; ++pass) {
+                        const float nm = m_ref == -INFINITY ? 0.f : -m_ref;
+                        const uint64_t nm2 = f2(nm, nm);
+                        uint64_t lacc[2] = {0ull, 0ull};
+                        float ext;
+                        if (easy) {
+                            float e[8];
+#pragma unroll
+                            for (int u = 0; u < 8; ++u) e[u] = __int_as_float(0x7fffffff);
+                            uint32_t cb[2][32];
+                            tmemw::ld32(s_col, cb[0]);
+                            tmemw::wait_ld(cb[0]);
+#pragma unroll
+                            for (int cc = 0; cc < 4; ++cc) {
+                                if (cc < 3) tmemw::ld32(s_col + 32 * (cc + 1), cb[(cc + 1) & 1]);
+#pragma unroll
+                                for (int n = 0; n < 32; n += 2) {
+                                    const float s0 = __uint_as_float(cb[cc & 1][n]), s1 = __uint_as_float(cb[cc & 1][n + 1]);
+                                    const float2 arg = unf2(fma2(f2(s0, s1), c2, nm2));
+                                    // (The argument grows with c s whatever the sign of c.)
+                                    e[(n >> 1) & 7] = max3(e[(n >> 1) & 7], arg.x, arg.y);
+                                    const uint32_t w = pack_bf16x2(ex2(arg.x), ex2(arg.y));
+                                    packed[cc * 16 + n / 2] = w;
+                                    lacc[(n >> 1) & 1] = add2(lacc[(n >> 1) & 1], f2(bf16_lo(w), bf16_hi(w)));
+                                }
+                                if (cc < 3) tmemw::wait_ld(cb[(cc + 1) & 1]);
+                            }
+                            ext = max3(max3(e[0], e[1], e[2]), max3(e[3], e[4], e[5]), fmaxf(e[6], e[7]));
+                        } else {
+                            float e[4];
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) e[u] = __int_as_float(0x7fffffff);
+#pragma unroll
+                            for (int cc = 0; cc < 4; ++cc) {
+                                const uint32_t m = vis[cc];
+                                if (__all_sync(0xffffffffu, idle_row || m == 0u)) {       // nothing seen here
+#pragma unroll
+                                    for (int n = 0; n < 16; ++n) packed[cc * 16 + n] = 0u;
+                                    continue;
+                                }
+                                uint32_t cb[32];
+                                tmemw::ld32(s_col + 32 * cc, cb);
+                                tmemw::wait_ld(cb);
+#pragma unroll
+                                for (int n = 0; n < 32; n += 2) {
+                                    const float2 arg = unf2(fma2(f2(__uint_as_float(cb[n]), __uint_as_float(cb[n + 1])), c2, nm2));
+                                    const bool v0 = (m >> n) & 1u, v1 = (m >> (n + 1)) & 1u;
+                                    e[(n >> 1) & 3] = max3(e[(n >> 1) & 3], v0 ? arg.x : __int_as_float(0x7fffffff),
+                                                           v1 ? arg.y : __int_as_float(0x7fffffff));
+                                    const uint32_t w = pack_bf16x2(v0 ? ex2(arg.x) : 0.f, v1 ? ex2(arg.y) : 0.f);
+                                    packed[cc * 16 + n / 2] = w;
+                                    lacc[(n >> 1) & 1] = add2(lacc[(n >> 1) & 1], f2(bf16_lo(w), bf16_hi(w)));
+                                }
+                            }
+                            ext = fmaxf(max3(e[0], e[1], e[2]), e[3]);
+                        }
+                        const float2 la = unf2(lacc[0]), lb = unf2(lacc[1]);
+                        lsum = (la.x + la.y) + (lb.x + lb.y);
+                        // ext is the largest c s - m_ref (c s where there is no m_ref yet);
+                        // NaN, no visible key, moves nothing.
+                        tmax = ext;
+                        const bool need = !idle_row && (m_ref == -INFINITY ? tmax > -INFINITY : tmax > kRescaleLog2);
+                        if (pass == 2 || !__any_sync(0xffffffffu, need)) break;
+                        // Move this row's reference max and rescale its O (complete up to
+                        // this group's last step) and denominator.
+                        const float mn = need ? (m_ref == -INFINITY ? tmax : m_ref + tmax) : m_ref;
                         const float f = rescale(m_ref, mn);
                         if (!first) {
-#pragma unroll
+#pragma unroll 1
                             for (int cc = 0; cc < D / 8; ++cc) {
                                 float ov[8];
                                 tmem_ld<8>(o_col + cc * 8, ov);
@@ -779,62 +887,14 @@ rows_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                         l_run *= f;
                         m_ref = mn;
                     }
-                    // p = 2^(c s - m_ref) as bf16 pairs over the first 64 columns of S
-                    // (the A operand of P.V): half the tensor work of fp32 weights at
-                    // an error of 2^-9 of each weight; the denominator sums the rounded
-                    // weights, so that their mean stays a mean.  The scores are read
-                    // again, 32 columns at a time: P of columns 32cc.. goes to columns
-                    // 16cc.., already read.
-                    const float nm = m_ref == -INFINITY ? 0.f : -m_ref;
-                    const uint64_t nm2 = f2(nm, nm);
-                    uint64_t lacc[2] = {0ull, 0ull};
-                    auto emit = [&](auto easy_tag) {
-                        constexpr bool kEasy = decltype(easy_tag)::value;
-                        uint32_t cb[2][32];
-                        tmemw::ld32(s_col, cb[0]);
-                        tmemw::wait_ld(cb[0]);
 #pragma unroll
-                        for (int cc = 0; cc < 4; ++cc) {
-                            if (cc < 3) tmemw::ld32(s_col + 32 * (cc + 1), cb[(cc + 1) & 1]);
-                            uint32_t packed[16];
+                    for (int cc = 0; cc < 4; ++cc) {
+                        uint32_t pk16[16];
 #pragma unroll
-                            for (int n = 0; n < 32; n += 2) {
-                                const int kk = cc * 32 + n;
-                                const float2 arg = unf2(fma2(f2(__uint_as_float(cb[cc & 1][n]),
-                                                                __uint_as_float(cb[cc & 1][n + 1])), c2, nm2));
-                                float p0 = ex2(arg.x), p1 = ex2(arg.y);
-                                if constexpr (!kEasy) {
-                                    p0 = visible(kk) ? p0 : 0.f;
-                                    p1 = visible(kk + 1) ? p1 : 0.f;
-                                }
-                                const uint32_t w = pack_bf16x2(p0, p1);
-                                packed[n / 2] = w;
-                                lacc[(n >> 1) & 1] = add2(lacc[(n >> 1) & 1], f2(bf16_lo(w), bf16_hi(w)));
-                            }
-                            tmem_st16(s_col + cc * 16, packed);   // keys 32cc .. 32cc+31 of this row
-                            if (cc < 3) tmemw::wait_ld(cb[(cc + 1) & 1]);
-                        }
-                    };
-                    if (easy) emit(std::true_type{});
-                    else emit(std::false_type{});
-                    const float2 la = unf2(lacc[0]), lb = unf2(lacc[1]);
-                    l_run += (la.x + la.y) + (lb.x + lb.y);
-                }
-                if (__any_sync(0xffffffffu, stale)) {
-                    if (!wait(&misc->vfull[kt % VS], kt / VS)) {
-                        alive = false;
-                        break;
+                        for (int n = 0; n < 16; ++n) pk16[n] = packed[cc * 16 + n];
+                        tmem_st16(s_col + cc * 16, pk16);      // keys 32cc .. 32cc+31 of this row
                     }
-                    if (stale) {
-#pragma unroll
-                        for (int ch = 0; ch < NCH; ++ch) {
-                            uint4 *vrow = reinterpret_cast<uint4 *>(smem + C_::kVOff + (kt % VS) * kTile +
-                                                                    (row >> 3) * kAtomStride + ch * 1024 + (row & 7) * 128);
-#pragma unroll
-                            for (int n = 0; n < 8; ++n) vrow[n] = make_uint4(0, 0, 0, 0);
-                        }
-                    }
-                    fence_proxy_async_smem();       // zeroed V rows are visible to the MMA
+                    l_run += lsum;
                 }
                 // The first product of a part overwrites O: the other group has to have
                 // read it, where it joined the last part.
@@ -866,9 +926,11 @@ rows_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                 owe = true;
             }
             if (mine) {
-                // P.V of this group's last step done; the other group's last one was
-                // issued before it, so that is done too.
-                if (!wait(&misc->pv_done[x], jobs - 1) || (joined && !wait(&misc->ml_ready, joins))) {
+                // P.V of the last steps done.  (The other group has left m and l, so it has
+                // seen every phase of its pv_done but the last, and it starts no other
+                // before o_taken: the probe of that phase is exact.)
+                if (!wait(&misc->pv_done[x], jobs - 1) ||
+                    (joined && (!wait(&misc->ml_ready, joins) || !wait(&misc->pv_done[1 - x], (k + nsteps - 2) >> 1)))) {
                     alive = false;
                     break;
                 }
@@ -891,25 +953,54 @@ rows_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                 const float g_own = complete ? f_own * inv : f_own, g_other = complete ? f_other * inv : f_other;
                 const size_t oidx = (static_cast<size_t>(q.q0 + tok0 + rr) * H + a.h * G + (row & (G - 1))) *
                                     static_cast<size_t>(D);
-                if (busy) {
+                auto chunk = [&](int cc, float (&f)[32]) {
+                    uint32_t ov[32];
+                    tmemw::ld32(o_col + cc * 32, ov);
+                    if (joined) {
+                        uint32_t ow[32];
+                        tmemw::ld32(o_other + cc * 32, ow);
+                        tmemw::wait_ld(ov);
+                        tmemw::wait_ld(ow);
+#pragma unroll
+                        for (int n = 0; n < 32; ++n)
+                            f[n] = __uint_as_float(ov[n]) * g_own + __uint_as_float(ow[n]) * g_other;
+                    } else {
+                        tmemw::wait_ld(ov);
+#pragma unroll
+                        for (int n = 0; n < 32; ++n) f[n] = __uint_as_float(ov[n]) * g_own;
+                    }
+                };
+                auto taken = [&]() {                // the other group may overwrite its O
+                    if (!joined) return;
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&misc->o_taken));
+                };
+                if (!busy) {
+                    taken();
+                } else if (complete && !p.out_fp32) {
+                    // All of the row first, so that the stores, slow while the copies
+                    // fill the memory, do not hold up the other group.
+                    uint32_t w[D / 2];
 #pragma unroll
                     for (int cc = 0; cc < D / 32; ++cc) {
-                        uint32_t ov[32];
-                        tmemw::ld32(o_col + cc * 32, ov);
                         float f[32];
-                        if (joined) {
-                            uint32_t ow[32];
-                            tmemw::ld32(o_other + cc * 32, ow);
-                            tmemw::wait_ld(ov);
-                            tmemw::wait_ld(ow);
+                        chunk(cc, f);
 #pragma unroll
-                            for (int n = 0; n < 32; ++n)
-                                f[n] = __uint_as_float(ov[n]) * g_own + __uint_as_float(ow[n]) * g_other;
-                        } else {
-                            tmemw::wait_ld(ov);
+                        for (int n = 0; n < 16; ++n) w[cc * 16 + n] = pack_bf16x2(f[2 * n], f[2 * n + 1]);
+                    }
+                    taken();
+                    if (use) {
+                        uint4 *o = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + oidx);
 #pragma unroll
-                            for (int n = 0; n < 32; ++n) f[n] = __uint_as_float(ov[n]) * g_own;
-                        }
+                        for (int n = 0; n < D / 8; ++n)
+                            o[n] = make_uint4(w[4 * n], w[4 * n + 1], w[4 * n + 2], w[4 * n + 3]);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int cc = 0; cc < D / 32; ++cc) {
+                        float f[32];
+                        chunk(cc, f);
                         if (complete) {
                             if (use) store_row<32>(p, oidx + cc * 32, f);
                         } else {
@@ -918,11 +1009,7 @@ rows_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                             for (int n = 0; n < 32; ++n) so[n * kRows] = f[n];
                         }
                     }
-                }
-                if (joined) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&misc->o_taken));
+                    taken();
                 }
                 if (!complete) {
                     float *sm = slot_m(slot, tile_x, D);
