@@ -10,27 +10,28 @@
 //
 // Shapes.  A query tile is 128 rows -- 128 / G tokens x the G heads of one KV
 // head -- on the M of both products, as in the prefill kernel:
-//   S[128 x 128] = Q K_tile^T,  O[128 x D] += P V_tile   (tcgen05, fp32 in TMEM).
+//   S[128 x 64] = Q K_half^T,  O[128 x D] += P V_half   (tcgen05, fp32 in TMEM).
 // A segment is one (sequence, KV head, block of query tiles) over all of the
 // sequence's 128-key tiles.  A block is two query tiles that share every K and V
-// tile, or one.  With one, the two softmax groups take the key tiles in turn,
-// each with its own O and m, and join at the end of the part through tensor
-// memory, where both see the same lanes: a single tile's chain of scores, weights
-// and product takes longer than the 1.6 us in which an SM's share of the memory
-// bandwidth brings a tile, two chains side by side do not.
+// tile, or one.  Two softmax groups of 128 threads: with two query tiles, each has
+// its own; with one, each takes one half of every key tile, with an O and m of its
+// own, and they join at the end of the part through tensor memory, where both see
+// the same lanes.
+//
+// Jobs.  A group's job is 64 keys of a tile: S, weights, P.V.  Its S has two
+// buffers, which the jobs take in turn, so that while the weights of one job are
+// worked out the tensor core does P.V of the job before and S of the next: with one
+// buffer of 128 keys a group's chain of S, weights and product took 2.4 us a tile
+// however few instructions each had.  (The price: an S of 64 columns reads Q from
+// shared memory twice as often.)
 //
 // Work.  The flattened (segment, key tile) space is cut into one range of equal
 // cost for each persistent CTA, so few long sequences fill the GPU as many short
 // ones do; a segment that is cut leaves (m, l, O) in a workspace slot, and a merge
 // kernel joins its parts.
 //
-// Steps.  Step k belongs to group x = k mod 2.  A block of one tile has a step per
-// key tile, a block of two has two.  The MMA warp issues, at step k, P.V of step
-// k - 2 (the same group's last one, whose P lies where S is going) and S of step
-// k, across parts without a pause.
-//
 // Per CTA (384 threads): warps 0-3 and 4-7 the softmax groups (thread <-> query
-// row = TMEM lane), warp 8 copies K, 9 V, 10 issues MMAs, 11 copies Q.
+// row = TMEM lane), warp 8 copies Q and K, 9 V, 10 and 11 issue the groups' MMAs.
 #include "rows_attention.cuh"
 #include "block_scan.cuh"
 #include "sm100.cuh"
@@ -49,11 +50,12 @@ namespace {
 using namespace sm100;
 
 constexpr int kRows = 128;                      // query rows per tile = MMA M
-constexpr int kKeys = 128;                      // keys per tile = MMA N of S
+constexpr int kKeys = 128;                      // keys per tile
+constexpr int kHalf = 64;                       // keys of a job = MMA N of S
 constexpr int kThreads = 384;
 constexpr uint32_t kChunk = 128 * 128;          // 128 rows x 128 bytes (64 bf16)
 constexpr uint32_t kTmemCols = 512;             // S_0, S_1, O_0, O_1 (128 columns each)
-constexpr uint32_t kTmemS = 0;                  // + x * 128; P_x over its first 64 columns
+constexpr uint32_t kTmemS = 0;                  // + x * 128 + buffer * 64; P over its first 32 columns
 constexpr uint32_t kTmemO = 256;                // + x * 128
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
 constexpr float kRescaleLog2 = 8.0f;
@@ -77,15 +79,16 @@ struct Cfg {
     static constexpr uint32_t kVOff = kKOff + kKS * kTile;
     static constexpr uint32_t kEnd = kVOff + kVS * kTile;
     // Tile masks in flight: the K producer runs at most kKS + 1 tiles ahead of a
-    // softmax group (its S done frees a slot; the step two on waits for its P).
+    // softmax group (a slot is free when both groups' S is done; the job two on waits
+    // for its P).
     static constexpr int kMasks = D == 128 ? 8 : 16;
     static_assert(kMasks > kKS + 2, "masks in flight");
 };
 
-// A tile in the MMA warp's eyes: the block has two query tiles; this is the first tile
-// of its part for the group at hand; the part's last tile; the query buffer of a block
-// of one; keys of the 16-key groups are not there; the number of those groups.
-constexpr int kMetaTwo = 1, kMetaFirst = 2, kMetaDone = 4, kMetaBuffer = 16, kMetaStale = 32, kMetaKeysShift = 8;
+// A tile in the MMA warps' eyes: its block has two query tiles; the first and the last
+// tile of its part; rows of the 16-key groups that hold no key; its keys.
+constexpr uint32_t kMetaTwo = 1, kMetaFirst = 2, kMetaLast = 4, kMetaStale = 8;
+constexpr int kMetaKeysShift = 8;
 
 struct Pos {          // a place in the flattened (segment, key tile) space
     int64_t tile;     // index of the key tile
@@ -96,24 +99,23 @@ template <int KS, int VS, int MASKS>
 struct Misc {
     uint64_t kfull[KS], kempty[KS], vfull[VS], vempty[VS];
     uint64_t qfull[2], qempty[2];
-    uint64_t s_full[2], p_full[2], pv_done[2];
+    uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];   // [group][buffer]
     uint64_t ml_ready, o_taken;   // the join of two groups' parts
-    uint64_t drain;
+    uint64_t drain[2];
     Pos pos[2];                   // start of this range and of the next one
     int32_t first_cta;            // the CTA in whose range this range's first segment starts
     uint32_t tmem_base;
     int abort;
     int never;
     uint32_t mask[MASKS][4];      // valid keys of a tile
-    int4 meta[MASKS];             // of a tile, for the MMA warp: kMeta* bits (y), and which fill of
-                                  // its query buffer(s) it reads (z, w)
+    uint32_t meta[MASKS];         // of a tile, for the MMA warps: kMeta* bits
     union {
         struct {
             int64_t tiles[kThreads / 32 + 1], costs[kThreads / 32 + 1];
         } scan;                   // while planning
         struct {
             float m[kRows], l[kRows];
-        } part;                   // what the group that is not the last one leaves
+        } part;                   // what the group leaves that does not give the result out
     };
 };
 
@@ -309,6 +311,25 @@ __device__ __forceinline__ int64_t plan(const RowsParams &p, M *misc, int lgG, i
 }
 
 __device__ __forceinline__ float ex2(float x) { return fast_exp2(x); }
+
+// A warp's wait for a phase, one decision for all lanes; false on give-up.  What does
+// not come at once is waited for out of line: the warps' different loops share one
+// instruction cache, and a wait's code in every place is as long as the work.
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int *abort, uint64_t limit_ns) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, limit_ns));
+}
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, int phase, volatile int *abort, uint64_t limit_ns) {
+    const uint32_t b = smem_u32(bar);
+    return __all_sync(0xffffffffu, mbar_try_wait(b, phase & 1)) || wait_on(b, phase & 1, abort, limit_ns);
+}
+// One lane of the warp, by the instruction whose predicate the compiler knows to be
+// one lane's: the operands of what it issues stay in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.b32 %0, 1, 0, P;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // Three-input max (NaN inputs are skipped, as by fmaxf).
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
@@ -366,22 +387,24 @@ rows_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
     if (threadIdx.x == 0) {
         for (int i = 0; i < KS; ++i) {
             mbar_init(smem_u32(&misc->kfull[i]), 1);
-            mbar_init(smem_u32(&misc->kempty[i]), 1);
+            mbar_init(smem_u32(&misc->kempty[i]), 2);
         }
         for (int i = 0; i < VS; ++i) {
             mbar_init(smem_u32(&misc->vfull[i]), 1);
-            mbar_init(smem_u32(&misc->vempty[i]), 1);
+            mbar_init(smem_u32(&misc->vempty[i]), 2);
         }
         for (int x = 0; x < 2; ++x) {
             mbar_init(smem_u32(&misc->qfull[x]), 1);
-            mbar_init(smem_u32(&misc->qempty[x]), 1);
-            mbar_init(smem_u32(&misc->s_full[x]), 1);
-            mbar_init(smem_u32(&misc->p_full[x]), 4);
-            mbar_init(smem_u32(&misc->pv_done[x]), 1);
+            mbar_init(smem_u32(&misc->qempty[x]), TWO ? 1 : 2);
+            for (int u = 0; u < 2; ++u) {
+                mbar_init(smem_u32(&misc->s_full[x][u]), 1);
+                mbar_init(smem_u32(&misc->p_full[x][u]), 4);
+                mbar_init(smem_u32(&misc->pv_done[x][u]), 1);
+            }
+            mbar_init(smem_u32(&misc->drain[x]), 1);
         }
         mbar_init(smem_u32(&misc->ml_ready), 4);
         mbar_init(smem_u32(&misc->o_taken), 4);
-        mbar_init(smem_u32(&misc->drain), 1);
         misc->abort = 0;
         misc->never = 0;
         fence_mbar_init();
@@ -431,23 +454,48 @@ rows_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
         misc->abort = 1;
         set_error(p.err, PK_DEVERR_TIMEOUT);
     };
-    // Query buffers: a block of two tiles fills both; blocks of one take them in turn.
+    // Query buffers.  TWO: one for each group, whose query tile it holds (the same one in
+    // both where the block has one).  Otherwise one of 128 rows, or two of at most 64
+    // that the parts take in turn.
     const uint32_t q_chunk = static_cast<uint32_t>(max(8, q_box << lgG)) * 128u;
-    const uint32_t q_slot = TWO ? kTile : q_chunk * NCH;
+    const uint32_t q_slot = q_chunk * NCH;
 
     if (warp == 8 || warp == 9) {
-        // ================= producers: warp 8 K, warp 9 V =================
+        // ================= producers: warp 8 Q and K, warp 9 V =================
         const bool kprod = warp == 8;
         const int MB = p.max_blocks_per_seq;
         const int nst = kprod ? KS : VS;
         uint64_t *full = kprod ? misc->kfull : misc->vfull, *empty = kprod ? misc->kempty : misc->vempty;
         const uint32_t ring = base + (kprod ? C_::kKOff : C_::kVOff);
         const void *tm = kprod ? static_cast<const void *>(&tm_k) : static_cast<const void *>(&tm_v);
-        int issued = 0, st = 0;
+        int issued = 0, st = 0, q_issued = 0;
         uint32_t ph = 1;
         bool ok_run = true, stalled = false;
-        int turn = 0, fill0 = 0, fill1 = 0;    // query buffers, as the warp that fills them counts
+        int part = 0;
         while (ok_run && walk.next(a)) {
+            if (kprod) {
+                int got = 1;
+                if (lane == 0) {
+                    const uint32_t bytes = static_cast<uint32_t>(q_box << lgG) * 128u * NCH;
+                    for (int x = 0; x < (TWO ? 2 : 1); ++x) {
+                        const int sl = TWO ? x : (q_slots == 2 ? part & 1 : 0);
+                        const int fill = TWO || q_slots == 1 ? part : part >> 1;
+                        got = mbar_wait(smem_u32(&misc->qempty[sl]), (fill & 1) ^ 1, &misc->abort, lim);
+                        if (!got) break;
+                        const uint32_t bar = smem_u32(&misc->qfull[sl]);
+                        mbar_arrive_expect_tx(bar, bytes);
+#pragma unroll
+                        for (int ch = 0; ch < NCH; ++ch)
+                            tma_load_3d(base + sl * q_slot + ch * q_chunk, &tm_q, bar, ch * 64, a.h * G,
+                                        walk.q.q0 + a.tok0 + (a.two ? x * QT : 0));
+                        ++q_issued;
+                    }
+                }
+                if (!__shfl_sync(0xffffffffu, got, 0)) {
+                    if (lane == 0) give_up();
+                    break;
+                }
+            }
             const int L = walk.q.L;
             const int32_t *table = p.block_tables + static_cast<size_t>(a.s) * MB;
             // Block-table entries of a key tile, one page per lane; the next
@@ -495,13 +543,10 @@ rows_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                         const uint32_t m = __reduce_or_sync(0xffffffffu, word == w ? bits : 0u);
                         if (lane == 0) misc->mask[issued & (C_::kMasks - 1)][w] = m;
                     }
-                    // (A block of one: a group's first tile is the part's first or second.)
                     if (lane == 0)
                         misc->meta[issued & (C_::kMasks - 1)] =
-                            make_int4(0, (a.two ? kMetaTwo : 0) | (t - a.t0 < (a.two ? 1 : 2) ? kMetaFirst : 0) |
-                                             (t == a.t1 - 1 ? kMetaDone : 0) | (turn ? kMetaBuffer : 0) |
-                                             (stale ? kMetaStale : 0) | ((vlen + 15) >> 4) << kMetaKeysShift,
-                                      !a.two && turn ? fill1 : fill0, fill1);
+                            (a.two ? kMetaTwo : 0u) | (t == a.t0 ? kMetaFirst : 0u) | (t == a.t1 - 1 ? kMetaLast : 0u) |
+                            (stale ? kMetaStale : 0u) | static_cast<uint32_t>(vlen) << kMetaKeysShift;
                 }
                 if (lane == 0) mbar_arrive_expect_tx(bar, nok * B * 128u * NCH);
                 __syncwarp();
@@ -514,367 +559,294 @@ rows_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                 }
                 if (t + 1 < a.t1) phys_next = fetch(t + 1);
             }
-            if (a.two || !turn) ++fill0;
-            if (a.two || turn) ++fill1;
-            if (!a.two && q_slots == 2) turn ^= 1;
+            ++part;
             walk.advance();
         }
         if ((misc->abort || stalled) && lane == 0) {
             // Let the copies in flight land before the CTA can exit.
             for (int i = max(0, issued - nst); i < issued; ++i)
                 mbar_wait(smem_u32(&full[i % nst]), (i / nst) & 1, &misc->never, lim);
+            // (The last fill of each query buffer: fills come in turn.)
+            const int bufs = TWO || q_slots == 2 ? 2 : 1;
+            for (int i = max(0, q_issued - bufs); i < q_issued; ++i)
+                mbar_wait(smem_u32(&misc->qfull[i % bufs]), (i / bufs) & 1, &misc->never, lim);
         }
-    } else if (warp == 11) {
-        // ================= producer of the queries =================
-        if (lane == 0) {
-            int fill0 = 0, fill1 = 0;
-            int turn = 0;
-            bool ok_run = true;
-            const uint32_t bytes = static_cast<uint32_t>(q_box << lgG) * 128u * NCH;
-            while (ok_run && walk.next(a)) {
-                const int q0 = walk.q.q0;
-                for (int x = 0; x < (a.two ? 2 : 1) && ok_run; ++x) {
-                    const int sl = a.two ? x : turn;
-                    if (!mbar_wait(smem_u32(&misc->qempty[sl]), ((sl ? fill1 : fill0) & 1) ^ 1, &misc->abort, lim)) {
-                        give_up();
-                        ok_run = false;
-                        break;
-                    }
-                    const uint32_t bar = smem_u32(&misc->qfull[sl]);
-                    mbar_arrive_expect_tx(bar, bytes);
-#pragma unroll
-                    for (int ch = 0; ch < NCH; ++ch)
-                        tma_load_3d(base + sl * q_slot + ch * q_chunk, &tm_q, bar, ch * 64, a.h * G,
-                                    q0 + a.tok0 + x * QT);
-                    if (sl) ++fill1;
-                    else ++fill0;
-                }
-                if (!a.two && q_slots == 2) turn ^= 1;
-                walk.advance();
-            }
-            if (misc->abort)
-                for (int sl = 0; sl < 2; ++sl) {
-                    const int n = sl ? fill1 : fill0;
-                    if (n > 0) mbar_wait(smem_u32(&misc->qfull[sl]), (n - 1) & 1, &misc->never, lim);
-                }
-        }
-        __syncwarp();
-    } else if (warp == 10) {
-        // ================= MMA issuer =================
-        // One thread.  Steps come in order: P.V of step k - 2, then S of step k.  (A loop that probed for
-        // whichever group is ready let the groups drift a whole tile apart, each K and V
-        // slot then held that much longer: 15-30 % slower.)
-        if (lane == 0) {
+    } else if (warp >= 10) {
+        // ================= MMA issuers: warp 10 of group 0, 11 of group 1 =================
+        // At job j, P.V of job j - 2 (whose P lies in the buffer that S is going to) and S of
+        // job j.  Every tile is used by both groups, so both see every phase of the rings
+        // in order.
+        const int x = __shfl_sync(0xffffffffu, warp, 0) - 10;
         constexpr uint32_t kIdescO = idesc_bf16(kRows, D, 0, 1);           // A = P (TMEM), B = V (MN-major)
-        constexpr uint32_t kIdescS = idesc_bf16(kRows, kKeys, 0, 0);       // A = Q, B = K, both K-major
         // Descriptors of the rings' starts; an address moves on in 16-byte units.
         const uint64_t qdesc = smem_desc(base, 16, 1024, kLayoutSw128);
         const uint64_t kdesc = smem_desc(base + C_::kKOff, 16, kAtomStride, kLayoutSw128);
         const uint64_t vdesc = smem_desc(base + C_::kVOff, 1024, kAtomStride, kLayoutSw128);
-        auto wait = [&](uint64_t *bar, int phase) -> bool {
-            return mbar_wait(smem_u32(bar), phase & 1, &misc->abort, lim);
+        const uint32_t scol = __shfl_sync(0xffffffffu, tmem, 0) + kTmemS + x * 128, ocol = scol + kTmemO - kTmemS;
+        auto wait = [&](uint64_t *bar, int phase) -> bool { return warp_wait(bar, phase, &misc->abort, lim); };
+        auto there = [&](uint64_t *bar, int phase) -> bool {
+            return __all_sync(0xffffffffu, mbar_test_wait(smem_u32(bar), phase & 1));
         };
+        const int n_all = __shfl_sync(0xffffffffu, static_cast<int>(n_tiles), 0);
         bool alive = true;
-        int kslot = 0, kpar = 0, vslot = 0, vpar = 0;
+        int kt = 0, kslot = 0, kpar = 0, vslot = 0, vpar = 0;
         bool vready = false;                   // the V tile at the ring's head has been waited for
-        uint32_t pend = 0, jobs = 0;           // by group (bit x): a P.V to come; parity of those issued
-        int pflags0 = 0, pflags1 = 0, pkt0 = 0, pkt1 = 0;   // of the step whose P.V is to come
-        auto pv = [&](int x, bool last_use) {
-            const int flags = x ? pflags1 : pflags0, kt = x ? pkt1 : pkt0;
-            alive = wait(&misc->p_full[x], jobs >> x) && (vready || wait(&misc->vfull[vslot], vpar));
-            if (!alive) return;
-            const int n16 = flags >> kMetaKeysShift;
-            if (!vready && (flags & kMetaStale)) {
-                // V rows of keys outside the sequence or behind a bad table entry may hold
-                // stale or non-finite bits, which weights of 0 do not cancel: zero those
-                // that the product reads.
-#pragma unroll 1
-                for (int q4 = 0; q4 < 4; ++q4) {
-                    const int nrow = max(0, min(32, n16 * 16 - 32 * q4));
-                    uint32_t gone = ~misc->mask[kt & (C_::kMasks - 1)][q4];
-                    if (nrow < 32) gone &= (1u << nrow) - 1u;
-                    while (gone) {
-                        const int r = 32 * q4 + __ffs(gone) - 1;
-                        gone &= gone - 1;
-                        uint8_t *vrow = smem + C_::kVOff + vslot * kTile + (r >> 3) * kAtomStride + (r & 7) * 128;
-#pragma unroll
-                        for (int n = 0; n < 8 * NCH; ++n)
-                            *reinterpret_cast<uint4 *>(vrow + (n >> 3) * 1024 + (n & 7) * 16) = make_uint4(0, 0, 0, 0);
+        int s_jobs = 0, pv_jobs = 0;           // S and P.V issued
+        // The jobs whose P.V is to come, by buffer: kMeta* bits (first and last as they are
+        // for this job), keys (0-64) and half.
+        uint32_t jinfo0 = 0, jinfo1 = 0;
+        int jkt0 = 0, jkt1 = 0;
+        int part = -1, half = 0, h_hi = 0;
+        uint32_t mt = 0;                       // the current tile, once it has been opened
+        bool opened = false;
+        while (alive && (kt < n_all || pv_jobs < s_jobs)) {
+            // What is next: the product of the job two before; or, where the next tile (or
+            // the part's queries) is not there yet, that of a job before, so that its part
+            // can end; or S.
+            if (!opened && kt < n_all) {
+                if (pv_jobs == s_jobs && !wait(&misc->kfull[kslot], kpar)) break;
+                if (pv_jobs == s_jobs || there(&misc->kfull[kslot], kpar)) {
+                    mt = __shfl_sync(0xffffffffu, misc->meta[kt & (C_::kMasks - 1)], 0);
+                    opened = true;
+                    if (mt & kMetaFirst) {
+                        const int sl = TWO ? x : (q_slots == 2 ? (part + 1) & 1 : 0);
+                        const int fill = TWO || q_slots == 1 ? part + 1 : (part + 1) >> 1;
+                        if (pv_jobs == s_jobs && !wait(&misc->qfull[sl], fill)) break;
+                        opened = pv_jobs == s_jobs || there(&misc->qfull[sl], fill);
+                        part += opened;
                     }
+                    half = mt & kMetaTwo ? 0 : x;
+                    h_hi = mt & kMetaTwo ? 1 : x;
                 }
-                fence_proxy_async_smem();
             }
-            vready = true;
-            tc_fence_after();
-            {
-                const uint32_t acol = tmem + kTmemS + x * 128, ocol = tmem + kTmemO + x * 128;
-                const uint64_t vd = vdesc + static_cast<uint32_t>(vslot) * (kTile >> 4);
-                const uint32_t acc = flags & kMetaFirst ? 0u : 1u;
-                // Keys 16kk .. 16kk+15: 8-row blocks 2kk and 2kk + 1; the two 64-element
-                // halves 1,024 bytes apart.
-                auto product = [&](int kk) {
-                    mma_bf16_tmem_a(ocol, acol + kk * 8, vd + kk * (2 * kAtomStride >> 4), kIdescO, kk > 0 ? 1u : acc);
-                };
-                if (n16 == kKeys / 16) {
-#pragma unroll
-                    for (int kk = 0; kk < kKeys / 16; ++kk) product(kk);
-                } else {
+            if (pv_jobs < s_jobs && (!opened || s_jobs - pv_jobs == 2)) {
+                const int u = pv_jobs & 1;
+                const uint32_t info = u ? jinfo1 : jinfo0;
+                const int n16 = (((info >> kMetaKeysShift) & 255) + 15) >> 4, hf = info >> 16;
+                if (!wait(&misc->p_full[x][u], pv_jobs >> 1) || (!vready && !wait(&misc->vfull[vslot], vpar))) {
+                    alive = false;
+                    break;
+                }
+                vready = true;
+                if (info & kMetaStale) {
+                    // V rows of keys outside the sequence or behind a bad table entry may hold
+                    // stale or non-finite bits, which weights of 0 do not cancel: zero those
+                    // that the product reads.  (Both groups may do so, with the same zeros.)
+                    const int pkt = u ? jkt1 : jkt0;
 #pragma unroll 1
-                    for (int kk = 0; kk < n16; ++kk) product(kk);
-                }
-                mma_commit(smem_u32(&misc->pv_done[x]));
-                if (last_use) mma_commit(smem_u32(&misc->vempty[vslot]));
-            }
-            if (last_use) {
-                vready = false;
-                if (++vslot == VS) {
-                    vslot = 0;
-                    vpar ^= 1;
-                }
-            }
-            jobs ^= 1u << x;
-            pend &= ~(1u << x);
-        };
-        // P.V of group x: the last use of its V tile if the block has one query tile, or if
-        // it is the later of the two groups (the other's P.V of this tile has been issued).
-        auto flush = [&](int x) {
-            if (!((pend >> x) & 1)) return;
-            const bool two = (x ? pflags1 : pflags0) & kMetaTwo;
-            pv(x, !two || vready);
-        };
-        int k = 0;                             // step
-        for (int kt = 0; kt < static_cast<int>(n_tiles) && alive; ++kt) {
-            bool kready = false;
-            int per = 1;
-            for (int y = 0; y < per && alive; ++y, ++k) {
-                const int x = k & 1;
-                flush(x);
-                if (!alive) break;
-                if (!kready && !wait(&misc->kfull[kslot], kpar)) {
-                    alive = false;
-                    break;
-                }
-                kready = true;
-                const int4 mt = misc->meta[kt & (C_::kMasks - 1)];
-                const bool two = mt.y & kMetaTwo;
-                per = two ? 2 : 1;
-                const int sl = two ? x : (mt.y & kMetaBuffer ? 1 : 0);
-                if ((mt.y & kMetaFirst) && !wait(&misc->qfull[sl], two && x ? mt.w : mt.z)) {
-                    alive = false;
-                    break;
+                    for (int q4 = 0; q4 < 2; ++q4) {
+                        const int nrow = max(0, min(32, n16 * 16 - 32 * q4));
+                        uint32_t gone = ~misc->mask[pkt & (C_::kMasks - 1)][2 * hf + q4];
+                        if (nrow < 32) gone &= (1u << nrow) - 1u;
+#pragma unroll 1
+                        while (gone) {
+                            const int r = 64 * hf + 32 * q4 + __ffs(gone) - 1;
+                            gone &= gone - 1;
+                            if (lane < 8 * NCH)
+                                *reinterpret_cast<uint4 *>(smem + C_::kVOff + vslot * kTile + (r >> 3) * kAtomStride +
+                                                           (lane >> 3) * 1024 + (r & 7) * 128 + (lane & 7) * 16) =
+                                    make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
                 }
                 tc_fence_after();
-                {
-                    const int n16 = mt.y >> kMetaKeysShift;
-                    const uint64_t kd = kdesc + static_cast<uint32_t>(kslot) * (kTile >> 4);
-                    const uint64_t qd = qdesc + ((static_cast<uint32_t>(sl) * q_slot) >> 4);
-                    const uint32_t idesc = n16 == kKeys / 16 ? kIdescS : idesc_bf16(kRows, n16 * 16, 0, 0);
+                if (elect_one()) {
+                    // Keys 16kk .. 16kk+15: 8-row blocks 2kk and 2kk + 1; the two 64-element
+                    // halves of the head 1,024 bytes apart.
+                    const uint64_t vd = vdesc + static_cast<uint32_t>(vslot) * (kTile >> 4) + hf * (8 * kAtomStride >> 4);
+                    const uint32_t acol = scol + u * kHalf;
+#pragma unroll
+                    for (int kk = 0; kk < kHalf / 16; ++kk)
+                        if (kk < n16)
+                            mma_bf16_tmem_a(ocol, acol + kk * 8, vd + kk * (2 * kAtomStride >> 4), kIdescO,
+                                            kk > 0 || !(info & kMetaFirst) ? 1u : 0u);
+                    mma_commit(smem_u32(&misc->pv_done[x][u]));
+                    if (info & kMetaLast) mma_commit(smem_u32(&misc->vempty[vslot]));   // the group's last of this tile
+                }
+                __syncwarp();
+                if (info & kMetaLast) {
+                    vready = false;
+                    if (++vslot == VS) {
+                        vslot = 0;
+                        vpar ^= 1;
+                    }
+                }
+                ++pv_jobs;
+                continue;
+            }
+            if (!opened) continue;
+            const int u = s_jobs & 1;
+            const int sl = TWO ? x : (q_slots == 2 ? part & 1 : 0);
+            const int n = max(0, min(kHalf, static_cast<int>(mt >> kMetaKeysShift) - half * kHalf));
+            const bool done = half == h_hi;        // the group's last S of this tile
+            tc_fence_after();
+            if (elect_one()) {
+                const uint64_t kd = kdesc + static_cast<uint32_t>(kslot) * (kTile >> 4) + half * (8 * kAtomStride >> 4);
+                const uint64_t qd = qdesc + ((static_cast<uint32_t>(sl) * q_slot) >> 4);
+                const uint32_t idesc = idesc_bf16(kRows, (n + 15) & ~15, 0, 0);   // A = Q, B = K, both K-major
+                if (n > 0) {
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk)
-                        mma_bf16(tmem + kTmemS + x * 128, qd + (((kk >> 2) * q_chunk + (kk & 3) * 32) >> 4),
+                        mma_bf16(scol + u * kHalf, qd + (((kk >> 2) * q_chunk + (kk & 3) * 32) >> 4),
                                  kd + (((kk >> 2) * 1024u + (kk & 3) * 32) >> 4), idesc, kk > 0 ? 1u : 0u);
-                    mma_commit(smem_u32(&misc->s_full[x]));
-                    if (y == per - 1) mma_commit(smem_u32(&misc->kempty[kslot]));
-                    if (mt.y & kMetaDone) mma_commit(smem_u32(&misc->qempty[sl]));   // the part's last scores
                 }
-                pend |= 1u << x;
-                if (x) {
-                    pflags1 = mt.y;
-                    pkt1 = kt;
-                } else {
-                    pflags0 = mt.y;
-                    pkt0 = kt;
+                mma_commit(smem_u32(&misc->s_full[x][u]));
+                if (done) {
+                    mma_commit(smem_u32(&misc->kempty[kslot]));
+                    if (mt & kMetaLast) mma_commit(smem_u32(&misc->qempty[sl]));   // the part's last scores
                 }
             }
-            if (++kslot == KS) {
-                kslot = 0;
-                kpar ^= 1;
+            __syncwarp();
+            const uint32_t info = (mt & kMetaStale) | ((mt & kMetaFirst) && (half == 0 || !(mt & kMetaTwo)) ? kMetaFirst : 0u) |
+                                  (done ? kMetaLast : 0u) | static_cast<uint32_t>(n) << kMetaKeysShift |
+                                  static_cast<uint32_t>(half) << 16;
+            if (u) {
+                jinfo1 = info;
+                jkt1 = kt;
+            } else {
+                jinfo0 = info;
+                jkt0 = kt;
+            }
+            ++s_jobs;
+            ++half;
+            if (done) {
+                opened = false;
+                ++kt;
+                if (++kslot == KS) {
+                    kslot = 0;
+                    kpar ^= 1;
+                }
             }
         }
-        for (int e = 0; e < 2 && alive; ++e, ++k) flush(k & 1);
-        if (!alive) give_up();
+        if ((!alive || kt < n_all || pv_jobs < s_jobs) && lane == 0) give_up();
         // Let every issued MMA finish before the CTA can release TMEM.
-        mma_commit(smem_u32(&misc->drain));
-        mbar_wait(smem_u32(&misc->drain), 0, &misc->never, lim);
-        }
+        if (elect_one()) mma_commit(smem_u32(&misc->drain[x]));
         __syncwarp();
+        wait_on(smem_u32(&misc->drain[x]), 0, &misc->never, lim);
     } else {
         // ================= softmax: warps 0-3 group 0, 4-7 group 1; thread <-> query row =================
         const int x = warp >> 2;
         const int quad = warp & 3;                      // TMEM lanes 32 * (warp % 4) ..
         const int row = quad * 32 + lane;
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-        const uint32_t s_col = lane_addr + kTmemS + x * 128;
         const uint32_t o_col = lane_addr + kTmemO + x * 128;
         const uint32_t o_other = lane_addr + kTmemO + (1 - x) * 128;
         const int rr = row >> lgG;                      // query token of this row in its tile
         const float cs = p.scale_log2;
         const uint64_t c2 = f2(cs, cs);
-        int k = 0;                                      // step at the start of the part
-        int ktile = 0;                                  // key tile (of the CTA's range) there
-        int jobs = 0;                                   // this group's steps so far
+        int ktile = 0;                                  // key tile (of the CTA's range) at the part's start
+        int jobs = 0;                                   // jobs so far (both groups have as many)
         int joins = 0;                                  // joins of two groups so far
         bool owe = false;                               // the other group still reads this group's O
         bool alive = true;
-        auto wait = [&](uint64_t *bar, int phase) -> bool {
-            return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), phase & 1, &misc->abort, lim));
-        };
+        auto wait = [&](uint64_t *bar, int phase) -> bool { return warp_wait(bar, phase, &misc->abort, lim); };
         while (alive && walk.next(a)) {
             const Seq q = walk.q;
             const int per = a.two ? 2 : 1;
-            const int nsteps = (a.t1 - a.t0) * per;
+            const int njobs = (a.t1 - a.t0) * per;
             const int tok0 = a.tok0 + (a.two ? x * QT : 0);   // first query token of this tile
             const int ntok = min(q.qn - tok0, QT);
             const bool busy = (quad * 32) >> lgG < ntok;      // this warp has a row in use
+            const bool idle_row = rr >= ntok;
             const int base_pos = q.L - q.qn;                  // position of the tree's node 0
             const uint32_t *mrow_bits = p.tree_mask && busy
                 ? p.tree_mask + static_cast<size_t>(q.q0 + tok0 + min(rr, ntok - 1)) * p.mask_words : nullptr;
-            // The mask words that 128 keys of tile t can touch, read a step ahead:
-            // all ones before node 0 (the context), zeros behind the row's words.
-            uint32_t mw[5];
-            auto fetch_mask = [&](int t) {
-                const int at = (t * kKeys - base_pos) >> 5;          // (rounds down)
-                if (!mrow_bits || t >= a.t1 || at <= -5) return;     // (-5: nothing of the tree in these keys)
+            // The first key of job i of the part.
+            auto job_key = [&](int i) -> int {
+                return a.two ? a.t0 * kKeys + i * kHalf : (a.t0 + i) * kKeys + x * kHalf;
+            };
+            // The mask words that the 64 keys of a job can touch, read a job ahead: all
+            // ones before node 0 (the context), zeros behind the row's words.
+            uint32_t mw[3];
+            auto fetch_mask = [&](int i) {
+                const int at = (job_key(i) - base_pos) >> 5;         // (rounds down)
+                if (!mrow_bits || i >= njobs || at <= -3) return;    // (-3: nothing of the tree in these keys)
 #pragma unroll
-                for (int w = 0; w < 5; ++w)
+                for (int w = 0; w < 3; ++w)
                     mw[w] = at + w < 0 ? 0xffffffffu : (at + w < p.mask_words ? mrow_bits[at + w] : 0u);
             };
             float m_ref = -INFINITY, l_run = 0.f;
-            bool first = true;
-            // This group's first step, and from there every second one (one tile)
-            // or every key tile (two).
-            const int i0 = (k & 1) == x ? 0 : 1;
-            fetch_mask(a.t0 + (a.two ? 0 : i0));
-            for (int i = i0; i < nsteps; i += 2) {
-                const int t = a.t0 + (a.two ? i >> 1 : i);
-                const int kt = ktile + (a.two ? i >> 1 : i);
-                if (!wait(&misc->s_full[x], jobs) || (jobs > 0 && !wait(&misc->pv_done[x], jobs - 1))) {
+            fetch_mask(0);
+            for (int i = 0; i < njobs; ++i, ++jobs) {
+                const int u = jobs & 1;
+                const int key0 = job_key(i);
+                const int kt = ktile + (key0 >> 7) - a.t0;
+                if (!wait(&misc->s_full[x][u], jobs >> 1)) {
                     alive = false;
                     break;
                 }
                 tc_fence_after();
+                const uint32_t s_col = lane_addr + kTmemS + x * 128 + u * kHalf;
                 if (busy) {
-                    uint32_t vis[4];
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) vis[w] = misc->mask[kt & (C_::kMasks - 1)][w];
-                    if (mrow_bits && ((t * kKeys - base_pos) >> 5) > -5) {
-                        const int sh = (t * kKeys - base_pos) & 31;
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) vis[w] &= __funnelshift_r(mw[w], mw[w + 1], sh);
+                    uint32_t sc[64];
+                    tmemw::ld64(s_col, sc);
+                    const uint32_t *valid = &misc->mask[kt & (C_::kMasks - 1)][(key0 >> 5) & 2];
+                    uint32_t v0 = valid[0], v1 = valid[1];
+                    const int off = key0 - base_pos;
+                    if (mrow_bits && (off >> 5) > -3) {
+                        v0 &= __funnelshift_r(mw[0], mw[1], off & 31);
+                        v1 &= __funnelshift_r(mw[1], mw[2], off & 31);
                     }
-                    fetch_mask(t + (a.two ? 1 : 2));
-                    // Rows in use that see every key of the tile (warp-uniform: the
-                    // tensor-memory moves below are warp-collective).
-                    const bool idle_row = rr >= ntok;
-                    const bool easy = __all_sync(0xffffffffu, idle_row || (vis[0] & vis[1] & vis[2] & vis[3]) == 0xffffffffu);
+                    fetch_mask(i + 1);
+                    // Rows in use that see every key of the job (warp-uniform: the
+                    // tensor-memory moves are warp-collective).
+                    const bool easy = __all_sync(0xffffffffu, idle_row || (v0 & v1) == 0xffffffffu);
                     // One pass over the row: weights against the reference max as it is,
                     // and the largest score beside them.  Only where that moves the
-                    // reference (the first tile, seldom later) is the pass made again:
-                    // S is overwritten by P after it.  P is bf16 pairs over the first
-                    // 64 columns of S (the A operand of P.V): half the tensor work of
-                    // fp32 weights at an error of 2^-9 of each; the denominator sums the
-                    // rounded weights, so that their mean stays a mean.
-                    uint32_t packed[64];
+                    // reference (a part's first job, seldom later) is the pass made again.
+                    // P is bf16 pairs over the first half of S (the A operand of P.V): half
+                    // the tensor work of fp32 weights at an error of 2^-9 of each; the
+                    // denominator sums the rounded weights, so that their mean stays one.
+                    uint32_t packed[32];
                     float lsum;
-                    // The extreme score of a chunk joins ext: the largest for c >= 0, the
-                    // smallest otherwise, so that c times it is the largest c s (rounding
-                    // is monotone).  A masked key counts as NaN, which max and min skip.
-                    const uint32_t flip = cs >= 0.f ? 0u : 0x80000000u;      // max of -s for the min of s
-                    float tmax;
-                    if (first) {
-                        float e[4];
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) e[u] = __int_as_float(0x7fffffff);
-#pragma unroll 1
-                        for (int cc = 0; cc < 4; ++cc) {
-                            const uint32_t m = cc == 0 ? vis[0] : cc == 1 ? vis[1] : cc == 2 ? vis[2] : vis[3];
-                            uint32_t cb[32];
-                            tmemw::ld32(s_col + 32 * cc, cb);
-                            tmemw::wait_ld(cb);
-#pragma unroll
-                            for (int n = 0; n < 32; n += 8) {
-#pragma unroll
-                                for (int u = 0; u < 4; ++u) {
-                                    const float v0 = __uint_as_float(cb[n + u] ^ flip), v1 = __uint_as_float(cb[n + 4 + u] ^ flip);
-                                    e[u] = max3(e[u], (m >> (n + u)) & 1u ? v0 : __int_as_float(0x7fffffff),
-                                                (m >> (n + 4 + u)) & 1u ? v1 : __int_as_float(0x7fffffff));
-                                }
-                            }
-                        }
-                        const float ext = fmaxf(max3(e[0], e[1], e[2]), e[3]);
-                        // No visible key (NaN): no candidate for the reference max.
-                        m_ref = ext == ext ? __uint_as_float(__float_as_uint(ext) ^ flip) * cs : -INFINITY;
-                    }
+                    tmemw::wait_ld(sc);
                     // (Two moves at most: scores whose rounding exceeds the threshold would
                     // ask for ever.)
                     for (int pass = 0;; ++pass) {
                         const float nm = m_ref == -INFINITY ? 0.f : -m_ref;
                         const uint64_t nm2 = f2(nm, nm);
                         uint64_t lacc[2] = {0ull, 0ull};
-                        float ext;
+                        // The largest c s - m_ref of the keys seen (c s where there is no m_ref
+                        // yet); a masked key counts as NaN, which max skips.
+                        float e[4];
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) e[n] = __int_as_float(0x7fffffff);
+                        auto pass_over = [&](auto easy_tag) {
+                            constexpr bool kEasy = decltype(easy_tag)::value;
+#pragma unroll
+                            for (int n = 0; n < 64; n += 2) {
+                                const float2 arg = unf2(fma2(f2(__uint_as_float(sc[n]), __uint_as_float(sc[n + 1])), c2, nm2));
+                                const uint32_t m = n < 32 ? v0 : v1;
+                                const bool in0 = kEasy || ((m >> (n & 31)) & 1u), in1 = kEasy || ((m >> ((n + 1) & 31)) & 1u);
+                                e[(n >> 1) & 3] = max3(e[(n >> 1) & 3], in0 ? arg.x : __int_as_float(0x7fffffff),
+                                                       in1 ? arg.y : __int_as_float(0x7fffffff));
+                                const uint32_t w = pack_bf16x2(in0 ? ex2(arg.x) : 0.f, in1 ? ex2(arg.y) : 0.f);
+                                packed[n / 2] = w;
+                                lacc[(n >> 1) & 1] = add2(lacc[(n >> 1) & 1], f2(bf16_lo(w), bf16_hi(w)));
+                            }
+                        };
                         if (easy) {
-                            float e[8];
-#pragma unroll
-                            for (int u = 0; u < 8; ++u) e[u] = __int_as_float(0x7fffffff);
-                            uint32_t cb[2][32];
-                            tmemw::ld32(s_col, cb[0]);
-                            tmemw::wait_ld(cb[0]);
-#pragma unroll
-                            for (int cc = 0; cc < 4; ++cc) {
-                                if (cc < 3) tmemw::ld32(s_col + 32 * (cc + 1), cb[(cc + 1) & 1]);
-#pragma unroll
-                                for (int n = 0; n < 32; n += 2) {
-                                    const float s0 = __uint_as_float(cb[cc & 1][n]), s1 = __uint_as_float(cb[cc & 1][n + 1]);
-                                    const float2 arg = unf2(fma2(f2(s0, s1), c2, nm2));
-                                    // (The argument grows with c s whatever the sign of c.)
-                                    e[(n >> 1) & 7] = max3(e[(n >> 1) & 7], arg.x, arg.y);
-                                    const uint32_t w = pack_bf16x2(ex2(arg.x), ex2(arg.y));
-                                    packed[cc * 16 + n / 2] = w;
-                                    lacc[(n >> 1) & 1] = add2(lacc[(n >> 1) & 1], f2(bf16_lo(w), bf16_hi(w)));
-                                }
-                                if (cc < 3) tmemw::wait_ld(cb[(cc + 1) & 1]);
-                            }
-                            ext = max3(max3(e[0], e[1], e[2]), max3(e[3], e[4], e[5]), fmaxf(e[6], e[7]));
+                            pass_over(std::true_type{});
                         } else {
-                            float e[4];
-#pragma unroll
-                            for (int u = 0; u < 4; ++u) e[u] = __int_as_float(0x7fffffff);
-#pragma unroll
-                            for (int cc = 0; cc < 4; ++cc) {
-                                const uint32_t m = vis[cc];
-                                if (__all_sync(0xffffffffu, idle_row || m == 0u)) {       // nothing seen here
-#pragma unroll
-                                    for (int n = 0; n < 16; ++n) packed[cc * 16 + n] = 0u;
-                                    continue;
-                                }
-                                uint32_t cb[32];
-                                tmemw::ld32(s_col + 32 * cc, cb);
-                                tmemw::wait_ld(cb);
-#pragma unroll
-                                for (int n = 0; n < 32; n += 2) {
-                                    const float2 arg = unf2(fma2(f2(__uint_as_float(cb[n]), __uint_as_float(cb[n + 1])), c2, nm2));
-                                    const bool v0 = (m >> n) & 1u, v1 = (m >> (n + 1)) & 1u;
-                                    e[(n >> 1) & 3] = max3(e[(n >> 1) & 3], v0 ? arg.x : __int_as_float(0x7fffffff),
-                                                           v1 ? arg.y : __int_as_float(0x7fffffff));
-                                    const uint32_t w = pack_bf16x2(v0 ? ex2(arg.x) : 0.f, v1 ? ex2(arg.y) : 0.f);
-                                    packed[cc * 16 + n / 2] = w;
-                                    lacc[(n >> 1) & 1] = add2(lacc[(n >> 1) & 1], f2(bf16_lo(w), bf16_hi(w)));
-                                }
-                            }
-                            ext = fmaxf(max3(e[0], e[1], e[2]), e[3]);
+                            pass_over(std::false_type{});
                         }
+                        const float tmax = fmaxf(max3(e[0], e[1], e[2]), e[3]);
                         const float2 la = unf2(lacc[0]), lb = unf2(lacc[1]);
                         lsum = (la.x + la.y) + (lb.x + lb.y);
-                        // ext is the largest c s - m_ref (c s where there is no m_ref yet);
-                        // NaN, no visible key, moves nothing.
-                        tmax = ext;
                         const bool need = !idle_row && (m_ref == -INFINITY ? tmax > -INFINITY : tmax > kRescaleLog2);
                         if (pass == 2 || !__any_sync(0xffffffffu, need)) break;
-                        // Move this row's reference max and rescale its O (complete up to
-                        // this group's last step) and denominator.
+                        // Move this row's reference max and rescale its O (of the jobs so
+                        // far) and denominator.
                         const float mn = need ? (m_ref == -INFINITY ? tmax : m_ref + tmax) : m_ref;
                         const float f = rescale(m_ref, mn);
-                        if (!first) {
+                        if (i > 0) {
+                            if (!wait(&misc->pv_done[x][u ^ 1], (jobs - 1) >> 1)) {
+                                alive = false;
+                                break;
+                            }
+                            tc_fence_after();
 #pragma unroll 1
                             for (int cc = 0; cc < D / 8; ++cc) {
                                 float ov[8];
@@ -887,8 +859,9 @@ rows_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                         l_run *= f;
                         m_ref = mn;
                     }
+                    if (!alive) break;
 #pragma unroll
-                    for (int cc = 0; cc < 4; ++cc) {
+                    for (int cc = 0; cc < 2; ++cc) {
                         uint32_t pk16[16];
 #pragma unroll
                         for (int n = 0; n < 16; ++n) pk16[n] = packed[cc * 16 + n];
@@ -897,7 +870,7 @@ rows_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                     l_run += lsum;
                 }
                 // The first product of a part overwrites O: the other group has to have
-                // read it, where it joined the last part.
+                // read it, where it gave the last part's result out.
                 if (owe) {
                     if (!wait(&misc->o_taken, joins - 1)) {
                         alive = false;
@@ -908,15 +881,13 @@ rows_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                 tmem_wait_st();                     // P is in TMEM before the MMA may read it
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&misc->p_full[x]));
-                ++jobs;
-                first = false;
+                if (lane == 0) mbar_arrive(smem_u32(&misc->p_full[x][u]));
             }
             if (!alive) break;
             // ---- the part's end ----
-            const int last_x = (k + nsteps - 1) & 1;
-            const bool joined = !a.two && nsteps > 1;
-            const bool mine = a.two || last_x == x;     // this group gives the result out
+            const bool joined = !a.two;
+            const bool mine = a.two || x == (joins & 1);    // this group gives the result out
+            const int last = jobs - 1;                      // both groups' last job
             if (joined && !mine) {
                 // Leave m and l to the other group, which reads this group's O itself.
                 misc->part.m[row] = m_ref;
@@ -926,11 +897,11 @@ rows_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                 owe = true;
             }
             if (mine) {
-                // P.V of the last steps done.  (The other group has left m and l, so it has
-                // seen every phase of its pv_done but the last, and it starts no other
-                // before o_taken: the probe of that phase is exact.)
-                if (!wait(&misc->pv_done[x], jobs - 1) ||
-                    (joined && (!wait(&misc->ml_ready, joins) || !wait(&misc->pv_done[1 - x], (k + nsteps - 2) >> 1)))) {
+                // P.V of the last jobs done.  (Probes of a phase are exact when the one before
+                // is known to be over: S of the last job followed P.V of the one before in
+                // its buffer; the other group has left m and l after its last S.)
+                if (!wait(&misc->pv_done[x][last & 1], last >> 1) ||
+                    (joined && (!wait(&misc->ml_ready, joins) || !wait(&misc->pv_done[1 - x][last & 1], last >> 1)))) {
                     alive = false;
                     break;
                 }
@@ -953,6 +924,8 @@ rows_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                 const float g_own = complete ? f_own * inv : f_own, g_other = complete ? f_other * inv : f_other;
                 const size_t oidx = (static_cast<size_t>(q.q0 + tok0 + rr) * H + a.h * G + (row & (G - 1))) *
                                     static_cast<size_t>(D);
+                // (A group whose halves held no key has written no O at all.)
+                auto part_of = [](uint32_t v, float g) -> float { return g == 0.f ? 0.f : __uint_as_float(v) * g; };
                 auto chunk = [&](int cc, float (&f)[32]) {
                     uint32_t ov[32];
                     tmemw::ld32(o_col + cc * 32, ov);
@@ -963,7 +936,7 @@ rows_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                         tmemw::wait_ld(ow);
 #pragma unroll
                         for (int n = 0; n < 32; ++n)
-                            f[n] = __uint_as_float(ov[n]) * g_own + __uint_as_float(ow[n]) * g_other;
+                            f[n] = part_of(ov[n], g_own) + part_of(ow[n], g_other);
                     } else {
                         tmemw::wait_ld(ov);
 #pragma unroll
@@ -1032,7 +1005,6 @@ rows_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                 }
             }
             if (joined) ++joins;
-            k += nsteps;
             ktile += a.t1 - a.t0;
             walk.advance();
         }
