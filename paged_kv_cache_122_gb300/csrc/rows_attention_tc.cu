@@ -42,7 +42,6 @@
 
 #include <algorithm>
 #include <mutex>
-#include <type_traits>
 
 namespace pk {
 namespace {
@@ -100,7 +99,7 @@ struct Misc {
     uint64_t kfull[KS], kempty[KS], vfull[VS], vempty[VS];
     uint64_t qfull[2], qempty[2];
     uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];   // [group][buffer]
-    uint64_t ml_ready, o_taken;   // the join of two groups' parts
+    uint64_t ml_ready[2], o_taken[2];   // the join of the groups' parts, by the group that arrives
     uint64_t drain[2];
     Pos pos[2];                   // start of this range and of the next one
     int32_t first_cta;            // the CTA in whose range this range's first segment starts
@@ -115,7 +114,7 @@ struct Misc {
         } scan;                   // while planning
         struct {
             float m[kRows], l[kRows];
-        } part;                   // what the group leaves that does not give the result out
+        } part;                   // what the groups tell each other of a part, one after the other
     };
 };
 
@@ -336,19 +335,40 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
-// N results of a row, to element idx of the output (idx and N multiples of 8).
+// 32 bytes at once (a whole sector), where the output's alignment allows it.
+__device__ __forceinline__ void store32(void *dst, const uint32_t (&w)[8], bool aligned) {
+    if (aligned) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                     ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        static_cast<uint4 *>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        static_cast<uint4 *>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
+// N results of a row, to element idx of the output (idx and N multiples of 16).
 template <int N>
 __device__ __forceinline__ void store_row(const RowsParams &p, size_t idx, const float (&f)[N]) {
+    const bool aligned = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
     if (p.out_fp32) {
-        float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + idx);
+        float *o = static_cast<float *>(p.out) + idx;
 #pragma unroll
-        for (int k = 0; k < N / 4; ++k) o[k] = make_float4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
+        for (int k = 0; k < N; k += 8) {
+            uint32_t w[8];
+#pragma unroll
+            for (int n = 0; n < 8; ++n) w[n] = __float_as_uint(f[k + n]);
+            store32(o + k, w, aligned);
+        }
     } else {
-        uint4 *o = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + idx);
+        uint16_t *o = static_cast<uint16_t *>(p.out) + idx;
 #pragma unroll
-        for (int k = 0; k < N / 8; ++k)
-            o[k] = make_uint4(pack_bf16x2(f[8 * k], f[8 * k + 1]), pack_bf16x2(f[8 * k + 2], f[8 * k + 3]),
-                              pack_bf16x2(f[8 * k + 4], f[8 * k + 5]), pack_bf16x2(f[8 * k + 6], f[8 * k + 7]));
+        for (int k = 0; k < N; k += 16) {
+            uint32_t w[8];
+#pragma unroll
+            for (int n = 0; n < 8; ++n) w[n] = pack_bf16x2(f[k + 2 * n], f[k + 2 * n + 1]);
+            store32(o + k, w, aligned);
+        }
     }
 }
 
@@ -402,9 +422,9 @@ rows_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                 mbar_init(smem_u32(&misc->pv_done[x][u]), 1);
             }
             mbar_init(smem_u32(&misc->drain[x]), 1);
+            mbar_init(smem_u32(&misc->ml_ready[x]), 4);
+            mbar_init(smem_u32(&misc->o_taken[x]), 4);
         }
-        mbar_init(smem_u32(&misc->ml_ready), 4);
-        mbar_init(smem_u32(&misc->o_taken), 4);
         misc->abort = 0;
         misc->never = 0;
         fence_mbar_init();
@@ -437,10 +457,10 @@ rows_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
             const Seq q = load_seq<TWO>(p, s, lgG);
             if (q.bad && threadIdx.x == 0) set_error(p.err, PK_DEVERR_SEQ_LEN);
             if (q.qn == 0 || q.L != 0) continue;
-            const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            const float zero[16] = {};
             const size_t first = static_cast<size_t>(q.q0) * H * D;
-            for (int64_t i = threadIdx.x; i < static_cast<int64_t>(q.qn) * H * (D / 8); i += kThreads)
-                store_row<8>(p, first + 8 * i, zero);
+            for (int64_t i = threadIdx.x; i < static_cast<int64_t>(q.qn) * H * (D / 16); i += kThreads)
+                store_row<16>(p, first + 16 * i, zero);
         }
     }
     tc_fence_before();
@@ -733,9 +753,11 @@ rows_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quad * 32) << 16);
         const uint32_t o_col = lane_addr + kTmemO + x * 128;
         const uint32_t o_other = lane_addr + kTmemO + (1 - x) * 128;
+        const int half_d = x * (D / 2);                 // of a joined part, a group gives out half of each row
         const int rr = row >> lgG;                      // query token of this row in its tile
         const float cs = p.scale_log2;
         const uint64_t c2 = f2(cs, cs);
+        const uint32_t unseen = __float_as_uint(cs > 0.f ? -INFINITY : INFINITY);
         int ktile = 0;                                  // key tile (of the CTA's range) at the part's start
         int jobs = 0;                                   // jobs so far (both groups have as many)
         int joins = 0;                                  // joins of two groups so far
@@ -790,9 +812,6 @@ rows_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                         v1 &= __funnelshift_r(mw[1], mw[2], off & 31);
                     }
                     fetch_mask(i + 1);
-                    // Rows in use that see every key of the job (warp-uniform: the
-                    // tensor-memory moves are warp-collective).
-                    const bool easy = __all_sync(0xffffffffu, idle_row || (v0 & v1) == 0xffffffffu);
                     // One pass over the row: weights against the reference max as it is,
                     // and the largest score beside them.  Only where that moves the
                     // reference (a part's first job, seldom later) is the pass made again.
@@ -802,35 +821,30 @@ rows_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                     uint32_t packed[32];
                     float lsum;
                     tmemw::wait_ld(sc);
+                    // Scores of keys that the row does not see become the one that weighs
+                    // nothing (c is not 0), unless every row in use sees all of them.
+                    if (!__all_sync(0xffffffffu, idle_row || (v0 & v1) == 0xffffffffu)) {
+#pragma unroll
+                        for (int n = 0; n < 64; ++n)
+                            sc[n] = ((n < 32 ? v0 : v1) >> (n & 31)) & 1u ? sc[n] : unseen;
+                    }
                     // (Two moves at most: scores whose rounding exceeds the threshold would
                     // ask for ever.)
                     for (int pass = 0;; ++pass) {
                         const float nm = m_ref == -INFINITY ? 0.f : -m_ref;
                         const uint64_t nm2 = f2(nm, nm);
                         uint64_t lacc[2] = {0ull, 0ull};
-                        // The largest c s - m_ref of the keys seen (c s where there is no m_ref
-                        // yet); a masked key counts as NaN, which max skips.
+                        // The largest c s - m_ref (c s where there is no m_ref yet).
                         float e[4];
 #pragma unroll
-                        for (int n = 0; n < 4; ++n) e[n] = __int_as_float(0x7fffffff);
-                        auto pass_over = [&](auto easy_tag) {
-                            constexpr bool kEasy = decltype(easy_tag)::value;
+                        for (int n = 0; n < 4; ++n) e[n] = -INFINITY;
 #pragma unroll
-                            for (int n = 0; n < 64; n += 2) {
-                                const float2 arg = unf2(fma2(f2(__uint_as_float(sc[n]), __uint_as_float(sc[n + 1])), c2, nm2));
-                                const uint32_t m = n < 32 ? v0 : v1;
-                                const bool in0 = kEasy || ((m >> (n & 31)) & 1u), in1 = kEasy || ((m >> ((n + 1) & 31)) & 1u);
-                                e[(n >> 1) & 3] = max3(e[(n >> 1) & 3], in0 ? arg.x : __int_as_float(0x7fffffff),
-                                                       in1 ? arg.y : __int_as_float(0x7fffffff));
-                                const uint32_t w = pack_bf16x2(in0 ? ex2(arg.x) : 0.f, in1 ? ex2(arg.y) : 0.f);
-                                packed[n / 2] = w;
-                                lacc[(n >> 1) & 1] = add2(lacc[(n >> 1) & 1], f2(bf16_lo(w), bf16_hi(w)));
-                            }
-                        };
-                        if (easy) {
-                            pass_over(std::true_type{});
-                        } else {
-                            pass_over(std::false_type{});
+                        for (int n = 0; n < 64; n += 2) {
+                            const float2 arg = unf2(fma2(f2(__uint_as_float(sc[n]), __uint_as_float(sc[n + 1])), c2, nm2));
+                            e[(n >> 1) & 3] = max3(e[(n >> 1) & 3], arg.x, arg.y);
+                            const uint32_t w = pack_bf16x2(ex2(arg.x), ex2(arg.y));
+                            packed[n / 2] = w;
+                            lacc[(n >> 1) & 1] = add2(lacc[(n >> 1) & 1], f2(bf16_lo(w), bf16_hi(w)));
                         }
                         const float tmax = fmaxf(max3(e[0], e[1], e[2]), e[3]);
                         const float2 la = unf2(lacc[0]), lb = unf2(lacc[1]);
@@ -870,9 +884,9 @@ rows_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                     l_run += lsum;
                 }
                 // The first product of a part overwrites O: the other group has to have
-                // read it, where it gave the last part's result out.
+                // read its half of it, where they joined the last part.
                 if (owe) {
-                    if (!wait(&misc->o_taken, joins - 1)) {
+                    if (!wait(&misc->o_taken[1 - x], joins - 1)) {
                         alive = false;
                         break;
                     }
@@ -885,126 +899,117 @@ rows_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
             }
             if (!alive) break;
             // ---- the part's end ----
+            // P.V of the last jobs done.  (Probes of a phase are exact when the one before is
+            // known to be over: S of the last job followed P.V of the one before in its
+            // buffer; the other group has left m and l after its last S.)
             const bool joined = !a.two;
-            const bool mine = a.two || x == (joins & 1);    // this group gives the result out
             const int last = jobs - 1;                      // both groups' last job
-            if (joined && !mine) {
-                // Leave m and l to the other group, which reads this group's O itself.
-                misc->part.m[row] = m_ref;
-                misc->part.l[row] = l_run;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&misc->ml_ready));
-                owe = true;
-            }
-            if (mine) {
-                // P.V of the last jobs done.  (Probes of a phase are exact when the one before
-                // is known to be over: S of the last job followed P.V of the one before in
-                // its buffer; the other group has left m and l after its last S.)
-                if (!wait(&misc->pv_done[x][last & 1], last >> 1) ||
-                    (joined && (!wait(&misc->ml_ready, joins) || !wait(&misc->pv_done[1 - x][last & 1], last >> 1)))) {
+            const bool complete = a.t0 == 0 && a.t1 == q.nt;
+            float f_own = 1.f, f_other = 0.f;
+            if (joined) {
+                // m and l of both groups, through one place: group 0's, then group 1's.
+                if (x == 0) {
+                    misc->part.m[row] = m_ref;
+                    misc->part.l[row] = l_run;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&misc->ml_ready[0]));
+                }
+                if (!wait(&misc->ml_ready[1 - x], joins)) {
                     alive = false;
                     break;
                 }
-                tc_fence_after();
-                float f_own = 1.f, f_other = 0.f;
-                if (joined) {
-                    const float m2 = misc->part.m[row], l2 = misc->part.l[row];
-                    const float mm = fmaxf(m_ref, m2);
-                    f_own = rescale(m_ref, mm);
-                    f_other = rescale(m2, mm);
-                    l_run = l_run * f_own + l2 * f_other;
-                    m_ref = mm;
+                const float m2 = misc->part.m[row], l2 = misc->part.l[row];
+                if (x == 1) {
+                    misc->part.m[row] = m_ref;
+                    misc->part.l[row] = l_run;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&misc->ml_ready[1]));
                 }
-                const bool complete = a.t0 == 0 && a.t1 == q.nt;
-                const int tile_x = a.two ? x : 0;
-                const bool first_part = a.s == from.s && a.h == from.h && a.j == from.j;
-                char *slot = complete ? nullptr : slot_at(p, slot_sz, c, first_part ? 0 : 1);
-                const bool use = rr < ntok;
+                const float mm = fmaxf(m_ref, m2);
+                f_own = rescale(m_ref, mm);
+                f_other = rescale(m2, mm);
+                l_run = l_run * f_own + l2 * f_other;
+                m_ref = mm;
+            }
+            if (!wait(&misc->pv_done[x][last & 1], last >> 1) ||
+                (joined && !wait(&misc->pv_done[1 - x][last & 1], last >> 1))) {
+                alive = false;
+                break;
+            }
+            tc_fence_after();
+            if (complete) {
                 const float inv = l_run > 0.f ? 1.f / l_run : (l_run == 0.f ? 0.f : l_run);
-                const float g_own = complete ? f_own * inv : f_own, g_other = complete ? f_other * inv : f_other;
+                f_own *= inv;
+                f_other *= inv;
+            }
+            const int tile_x = a.two ? x : 0;
+            const bool first_part = a.s == from.s && a.h == from.h && a.j == from.j;
+            char *slot = complete ? nullptr : slot_at(p, slot_sz, c, first_part ? 0 : 1);
+            if (busy) {
+                const bool use = rr < ntok;
                 const size_t oidx = (static_cast<size_t>(q.q0 + tok0 + rr) * H + a.h * G + (row & (G - 1))) *
                                     static_cast<size_t>(D);
                 // (A group whose halves held no key has written no O at all.)
                 auto part_of = [](uint32_t v, float g) -> float { return g == 0.f ? 0.f : __uint_as_float(v) * g; };
-                auto chunk = [&](int cc, float (&f)[32]) {
+                const int lo = joined ? half_d : 0, hi = joined ? half_d + D / 2 : D;
+#pragma unroll 1
+                for (int d = lo; d < hi; d += 32) {
+                    float f[32];
                     uint32_t ov[32];
-                    tmemw::ld32(o_col + cc * 32, ov);
+                    tmemw::ld32(o_col + d, ov);
                     if (joined) {
                         uint32_t ow[32];
-                        tmemw::ld32(o_other + cc * 32, ow);
+                        tmemw::ld32(o_other + d, ow);
                         tmemw::wait_ld(ov);
                         tmemw::wait_ld(ow);
 #pragma unroll
-                        for (int n = 0; n < 32; ++n)
-                            f[n] = part_of(ov[n], g_own) + part_of(ow[n], g_other);
+                        for (int n = 0; n < 32; ++n) f[n] = part_of(ov[n], f_own) + part_of(ow[n], f_other);
                     } else {
                         tmemw::wait_ld(ov);
 #pragma unroll
-                        for (int n = 0; n < 32; ++n) f[n] = __uint_as_float(ov[n]) * g_own;
+                        for (int n = 0; n < 32; ++n) f[n] = __uint_as_float(ov[n]) * f_own;
                     }
-                };
-                auto taken = [&]() {                // the other group may overwrite its O
-                    if (!joined) return;
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&misc->o_taken));
-                };
-                if (!busy) {
-                    taken();
-                } else if (complete && !p.out_fp32) {
-                    // All of the row first, so that the stores, slow while the copies
-                    // fill the memory, do not hold up the other group.
-                    uint32_t w[D / 2];
-#pragma unroll
-                    for (int cc = 0; cc < D / 32; ++cc) {
-                        float f[32];
-                        chunk(cc, f);
-#pragma unroll
-                        for (int n = 0; n < 16; ++n) w[cc * 16 + n] = pack_bf16x2(f[2 * n], f[2 * n + 1]);
+                    // (The last reads of O: the other group may overwrite its own before the
+                    // stores, slow while the copies fill the memory, are out.)
+                    if (joined && d + 32 == hi) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&misc->o_taken[x]));
                     }
-                    taken();
-                    if (use) {
-                        uint4 *o = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + oidx);
+                    if (!complete) {
+                        float *so = slot_m(slot, tile_x, D) + 2 * kRows + static_cast<size_t>(d) * kRows + row;
 #pragma unroll
-                        for (int n = 0; n < D / 8; ++n)
-                            o[n] = make_uint4(w[4 * n], w[4 * n + 1], w[4 * n + 2], w[4 * n + 3]);
+                        for (int n = 0; n < 32; ++n) so[n * kRows] = f[n];
+                    } else if (use) {
+                        store_row<32>(p, oidx + d, f);
                     }
-                } else {
-#pragma unroll 1
-                    for (int cc = 0; cc < D / 32; ++cc) {
-                        float f[32];
-                        chunk(cc, f);
-                        if (complete) {
-                            if (use) store_row<32>(p, oidx + cc * 32, f);
-                        } else {
-                            float *so = slot_m(slot, tile_x, D) + 2 * kRows + static_cast<size_t>(cc) * 32 * kRows + row;
-#pragma unroll
-                            for (int n = 0; n < 32; ++n) so[n * kRows] = f[n];
-                        }
-                    }
-                    taken();
                 }
-                if (!complete) {
-                    float *sm = slot_m(slot, tile_x, D);
-                    sm[row] = m_ref;
-                    sm[kRows + row] = l_run;
-                    if (row == 0 && tile_x == 0) {
-                        SlotHead *hd = reinterpret_cast<SlotHead *>(slot);
-                        hd->s = a.s;
-                        hd->h = a.h;
-                        hd->tok0 = a.tok0;
-                        hd->ntiles = per;
-                        if (first_part) {
-                            // Cut at its start and finished here: this CTA's merge joins it.
-                            hd->start_tile = from.tile - a.t0;
-                            hd->total_tiles = T;
-                            hd->first_cta = misc->first_cta;
-                            hd->flag = a.t0 > 0 && a.t1 == q.nt ? 1 : 0;
-                        }
+            } else if (joined && lane == 0) {
+                mbar_arrive(smem_u32(&misc->o_taken[x]));
+            }
+            if (!complete && (a.two || x == 0)) {
+                float *sm = slot_m(slot, tile_x, D);
+                sm[row] = m_ref;
+                sm[kRows + row] = l_run;
+                if (row == 0 && tile_x == 0) {
+                    SlotHead *hd = reinterpret_cast<SlotHead *>(slot);
+                    hd->s = a.s;
+                    hd->h = a.h;
+                    hd->tok0 = a.tok0;
+                    hd->ntiles = per;
+                    if (first_part) {
+                        // Cut at its start and finished here: this CTA's merge joins it.
+                        hd->start_tile = from.tile - a.t0;
+                        hd->total_tiles = T;
+                        hd->first_cta = misc->first_cta;
+                        hd->flag = a.t0 > 0 && a.t1 == q.nt ? 1 : 0;
                     }
                 }
             }
-            if (joined) ++joins;
+            if (joined) {
+                owe = true;
+                ++joins;
+            }
             ktile += a.t1 - a.t0;
             walk.advance();
         }

@@ -62,7 +62,10 @@ int attend(void *out, int out_dtype, const void *q, int total_q, const int32_t *
     p.head_dim = head_dim;
     p.num_blocks = num_blocks;
     p.block_size = block_size;
+    // (Not 0: the kernel multiplies it with infinities, and a factor this small makes
+    // every finite score 0 all the same.)
     p.scale_log2 = scale * pk::kLog2e;
+    if (p.scale_log2 == 0.f) p.scale_log2 = 1.17549435e-38f;
     p.wait_limit_ns = wait_limit_ns;
     p.stall_tile = stall_tile;
     p.err = pk::error_word_ptr();
