@@ -149,23 +149,50 @@ struct Seq {
     bool bad;
 };
 
+// A load that bypasses L1: what is read before the programmatic wait and again after it
+// cannot come back stale from there.
+__device__ __forceinline__ int load_cg(const int32_t *p) {
+    int v;
+    asm volatile("ld.global.cg.s32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+
+// A sequence's length and first rows (its own and the next one's).
+struct Raw {
+    int L, q0, q1;
+};
+__device__ __forceinline__ Raw load_raw(const RowsParams &p, int s) {
+    return {load_cg(p.seq_lens + s), load_cg(p.cu_q_lens + s), load_cg(p.cu_q_lens + s + 1)};
+}
+
 template <bool TWO>
-__device__ __forceinline__ Seq load_seq(const RowsParams &p, int s, int lgG) {
+__device__ __forceinline__ Seq seq_of(const RowsParams &p, const Raw &w, int lgG) {
     Seq r;
-    r.L = p.seq_lens[s];
-    r.q0 = p.cu_q_lens[s];
-    const int q1 = p.cu_q_lens[s + 1];
+    r.L = w.L;
+    r.q0 = w.q0;
     const int64_t cap = min(static_cast<int64_t>(p.max_seq_len),
                             static_cast<int64_t>(p.max_blocks_per_seq) * p.block_size);
-    r.bad = r.L < 0 || r.L > cap || r.q0 < 0 || q1 < r.q0 || q1 > p.total_q || q1 - r.q0 > p.max_q_len ||
-            (p.tree_mask && q1 - r.q0 > r.L);
-    r.qn = r.bad ? 0 : q1 - r.q0;
+    r.bad = r.L < 0 || r.L > cap || r.q0 < 0 || w.q1 < r.q0 || w.q1 > p.total_q || w.q1 - r.q0 > p.max_q_len ||
+            (p.tree_mask && w.q1 - r.q0 > r.L);
+    r.qn = r.bad ? 0 : w.q1 - r.q0;
     r.nt = r.qn > 0 ? (r.L >> 7) + ((r.L & 127) != 0) : 0;
-    const int qt = kRows >> lgG;
-    const int tiles = r.nt > 0 ? (r.qn + qt - 1) / qt : 0;
+    const int lgqt = 7 - lgG;
+    const int tiles = r.nt > 0 ? (r.qn + (1 << lgqt) - 1) >> lgqt : 0;
     r.n2 = TWO ? tiles >> 1 : 0;
     r.n1 = tiles - 2 * r.n2;
     return r;
+}
+template <bool TWO>
+__device__ __forceinline__ Seq load_seq(const RowsParams &p, int s, int lgG) {
+    return seq_of<TWO>(p, load_raw(p, s), lgG);
+}
+
+// A quotient of two numbers >= 0 and > 0, out of line (one copy of the code), by 32 bits
+// where they fit: the plan divides a dozen times, and 64-bit divisions were half of its
+// 3.6 us.
+__device__ __noinline__ int64_t quotient(int64_t a, int64_t b) {
+    if ((static_cast<uint64_t>(a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
 }
 
 __device__ __forceinline__ int64_t block_cost(const Seq &q, bool two) {
@@ -244,8 +271,8 @@ __device__ __forceinline__ int64_t plan(const RowsParams &p, M *misc, int lgG, i
     int64_t T, W;
     const int64_t off = block_exclusive_scan<kThreads>(mine, misc->scan.tiles, &T);
     const int64_t off_w = block_exclusive_scan<kThreads>(mine_w, misc->scan.costs, &W);
-    const int64_t Ce = max(static_cast<int64_t>(1), min(static_cast<int64_t>(C), W / kMinCost));
-    auto bound = [&](int64_t k) -> int64_t { return k >= Ce ? W : k * W / Ce; };
+    const int64_t Ce = max(static_cast<int64_t>(1), min(static_cast<int64_t>(C), W / kMinCost));   // (kMinCost: 2^5)
+    auto bound = [&](int64_t k) -> int64_t { return k >= Ce ? W : quotient(k * W, Ce); };
 #pragma unroll 1
     for (int k = 0; k < 2; ++k) {
         const int64_t P = bound(c + k);
@@ -265,14 +292,14 @@ __device__ __forceinline__ int64_t plan(const RowsParams &p, M *misc, int lgG, i
                 continue;
             }
             int64_t r = P - at_w;
-            int64_t h = r / hc;
+            int64_t h = quotient(r, hc);
             r -= h * hc;
             const int64_t b2 = block_cost(q, true);
-            int64_t j = min(r / b2, static_cast<int64_t>(q.n2));
+            int64_t j = min(quotient(r, b2), static_cast<int64_t>(q.n2));
             r -= j * b2;
             const int64_t tc = j < q.n2 ? kTileCost2 : kTileCost1;
             // The first tile that starts at or after r.
-            int64_t t = r == 0 ? 0 : max(static_cast<int64_t>(1), (r - kSegCost + tc - 1) / tc);
+            int64_t t = r == 0 ? 0 : r <= kSegCost ? 1 : quotient(r - kSegCost + tc - 1, tc);
             int64_t a = P - r;                        // where the segment starts
             if (t >= q.nt) {                          // behind its last one: the next segment
                 a += block_cost(q, j < q.n2);
@@ -297,7 +324,7 @@ __device__ __forceinline__ int64_t plan(const RowsParams &p, M *misc, int lgG, i
             o.j = static_cast<int>(j);
             o.t = static_cast<int>(t);
             if (k == 0) {
-                int64_t f = min(a * Ce / W, Ce - 1);
+                int64_t f = min(quotient(a * Ce, W), Ce - 1);
                 while (f + 1 < Ce && bound(f + 1) <= a) ++f;
                 while (f > 0 && bound(f) > a) --f;
                 misc->first_cta = static_cast<int>(f);
@@ -438,12 +465,34 @@ rows_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
         prefetch_tmap(&tm_v);
         prefetch_tmap(&tm_q);
     }
-    // A programmatic dependent of the previous kernel in the stream: nothing
-    // global is read or written before this wait.
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // A programmatic dependent of the previous kernel in the stream: what comes before the
+    // wait overlaps that kernel's tail.  With a sequence a thread at most, the range is
+    // planned before it; afterwards the lengths are read again, and the plan is made again
+    // if one changed.  Nothing else global is read before the wait, and nothing written.
+    auto wait_prev = [&]() {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    };
+    const int own_seq = static_cast<int>(threadIdx.x) < p.num_seqs ? static_cast<int>(threadIdx.x) : -1;
+    bool ahead = p.num_seqs <= kThreads;
+    Raw seen{0, 0, 0};
+    if (!ahead) wait_prev();
+    else if (own_seq >= 0) seen = load_raw(p, own_seq);
     int odd;
-    const int64_t T = plan<TWO>(p, misc, lgG, c, C, &odd);
+    int64_t T;
+#pragma unroll 1
+    for (;;) {
+        T = plan<TWO>(p, misc, lgG, c, C, &odd);
+        if (!ahead) break;
+        ahead = false;
+        wait_prev();
+        bool changed = false;
+        if (own_seq >= 0) {
+            const Raw now = load_raw(p, own_seq);
+            changed = now.L != seen.L || now.q0 != seen.q0 || now.q1 != seen.q1;
+        }
+        if (!__syncthreads_or(changed)) break;
+    }
     const Pos from = misc->pos[0];
     const int64_t n_tiles = misc->pos[1].tile - from.tile;
     if (threadIdx.x == 0 && p.slots) {
