@@ -1073,57 +1073,67 @@ rows_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
     }
 }
 
-// grid (CTAs, D / 16, query tiles of a block), 128 threads: where CTA c's first
-// segment was cut at its start and ends in c, join its parts.  Thread <-> query
-// row, 16 elements of the head; O^T in the slots makes the reads whole lines.
+// One block per CTA c of the attention grid: where c's first segment was cut at its
+// start and ends in c, join its parts.  A thread has a query row and 16 elements of the
+// head (O^T in the slots makes the reads whole lines); the parts come two at a time,
+// their loads in flight together.  Few large blocks: 152 of them are launched in 1.5 us,
+// 2,432 of 128 threads in 3.8 us.
+constexpr int kMergeThreads = 1024;
+
 template <int D>
-__global__ void __launch_bounds__(kRows)
-rows_merge_kernel(const RowsParams p, int C, int slot_tiles) {
+__global__ void __launch_bounds__(kMergeThreads)
+rows_merge_kernel(const __grid_constant__ RowsParams p, int C, int slot_tiles) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const size_t slot_sz = slot_bytes<D>(slot_tiles);
-    const int c = blockIdx.x, x = blockIdx.z, row = threadIdx.x, d0 = blockIdx.y * 16;
-    const SlotHead *hd = reinterpret_cast<const SlotHead *>(slot_at(p, slot_sz, c, 0));
-    if (hd->flag != 1 || x >= hd->ntiles) return;
-    const int64_t start = hd->start_tile, T = hd->total_tiles;
-    const int s = hd->s, h = hd->h;
-    auto range_beg = [&](int cc) -> int64_t {
-        return cc < C ? reinterpret_cast<const SlotHead *>(slot_at(p, slot_sz, cc, 0))->range_beg : T;
+    const int c = blockIdx.x, row = threadIdx.x & (kRows - 1);
+    auto head = [&](int cc) -> const SlotHead * {
+        return reinterpret_cast<const SlotHead *>(slot_at(p, slot_sz, cc, 0));
     };
-    const int lgG = __ffs(p.num_heads / p.num_kv_heads) - 1;
-    const int tok = hd->tok0 + x * (kRows >> lgG) + (row >> lgG);
-    const int q0 = p.cu_q_lens[s];
-    if (tok >= p.cu_q_lens[s + 1] - q0) return;
-    float M = -INFINITY, l = 0.f, o[16];
+    const SlotHead hd = *head(c);
+    const int64_t before = head(c > 0 ? c - 1 : 0)->range_beg;     // (the usual first part's)
+    if (hd.flag != 1) return;
+    const int lgG = __ffs(p.num_heads / p.num_kv_heads) - 1, G = 1 << lgG;
+    const int q0 = p.cu_q_lens[hd.s], qn = p.cu_q_lens[hd.s + 1] - q0;
+    // CTA cc's part, from its slot 0 if the segment is the first of its range, else 1; a
+    // range may be empty (more CTAs than tiles) and then has none.
+    auto range_beg = [&](int cc) -> int64_t { return cc == c ? hd.range_beg : cc == c - 1 ? before : head(cc)->range_beg; };
+    for (int unit = threadIdx.x / kRows; unit < hd.ntiles * (D / 16); unit += kMergeThreads / kRows) {
+        const int x = unit / (D / 16), d0 = unit % (D / 16) * 16;
+        const int tok = hd.tok0 + x * (kRows >> lgG) + (row >> lgG);
+        if (tok >= qn) continue;
+        float M = -INFINITY, l = 0.f, o[16];
 #pragma unroll
-    for (int n = 0; n < 16; ++n) o[n] = 0.f;
-    // Contributors: the CTAs from first_cta to c whose range is not empty.
-    int64_t rb = range_beg(hd->first_cta);
-#pragma unroll 2
-    for (int cc = hd->first_cta; cc <= c; ++cc) {
-        const int64_t rn = range_beg(cc + 1);
-        const bool some = rn > rb;
-        char *slot = slot_at(p, slot_sz, cc, rb >= start ? 0 : 1);
-        rb = rn;
-        if (!some) continue;
-        const float *sm = slot_m(slot, x, D) + row;
-        const float m = sm[0], lp = sm[kRows];
-        float v[16];
+        for (int n = 0; n < 16; ++n) o[n] = 0.f;
+        int64_t rb = range_beg(hd.first_cta);
+#pragma unroll 1
+        for (int cc = hd.first_cta; cc <= c; cc += 2) {
+            const bool two = cc + 1 <= c;
+            const int64_t r1 = two ? range_beg(cc + 1) : hd.total_tiles, r2 = cc + 2 <= c ? range_beg(cc + 2) : hd.total_tiles;
+            float m[2], lp[2], v[2][16];
 #pragma unroll
-        for (int n = 0; n < 16; ++n) v[n] = sm[(2 + d0 + n) * kRows];
-        const float mm = fmaxf(M, m);
-        const float fa = rescale(M, mm), fb = rescale(m, mm);
-        l = l * fa + lp * fb;
+            for (int u = 0; u < 2; ++u) {
+                const bool some = u == 0 ? cc == c || r1 > rb : two && (cc + 1 == c || r2 > r1);
+                const float *sm = slot_m(slot_at(p, slot_sz, two ? cc + u : cc, (u ? r1 : rb) >= hd.start_tile ? 0 : 1), x, D) + row;
+                m[u] = some ? sm[0] : -INFINITY;
+                lp[u] = some ? sm[kRows] : 0.f;
 #pragma unroll
-        for (int n = 0; n < 16; ++n) o[n] = o[n] * fa + v[n] * fb;
-        M = mm;
+                for (int n = 0; n < 16; ++n) v[u][n] = some ? sm[(2 + d0 + n) * kRows] : 0.f;
+            }
+            rb = r2;
+            const float mm = max3(M, m[0], m[1]);
+            const float f = rescale(M, mm), f0 = rescale(m[0], mm), f1 = rescale(m[1], mm);
+            l = l * f + (lp[0] * f0 + lp[1] * f1);
+#pragma unroll
+            for (int n = 0; n < 16; ++n) o[n] = o[n] * f + (v[0][n] * f0 + v[1][n] * f1);
+            M = mm;
+        }
+        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+#pragma unroll
+        for (int n = 0; n < 16; ++n) o[n] *= inv;
+        store_row<16>(p, (static_cast<size_t>(q0 + tok) * p.num_heads + hd.h * G + (row & (G - 1))) * static_cast<size_t>(D) + d0,
+                      o);
     }
-    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-#pragma unroll
-    for (int n = 0; n < 16; ++n) o[n] *= inv;
-    const int G = 1 << lgG;
-    store_row<16>(p, (static_cast<size_t>(q0 + tok) * p.num_heads + h * G + (row & (G - 1))) * static_cast<size_t>(D) + d0,
-                  o);
 }
 
 // ---------------------------------------------------------------- host side
@@ -1213,8 +1223,7 @@ cudaError_t launch(const RowsParams &p, cudaStream_t stream) {
     cfg.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, rows_attention_kernel<D, TWO>, mk, mv, mq, p, q_box, q_slots);
     if (e != cudaSuccess || !p.slots) return e;          // without slots nothing is cut
-    cfg.gridDim = dim3(C, D / 16, TWO ? 2 : 1);
-    cfg.blockDim = dim3(kRows);
+    cfg.blockDim = dim3(kMergeThreads);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, rows_merge_kernel<D>, p, C, TWO ? 2 : 1);
 }
