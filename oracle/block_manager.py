@@ -104,6 +104,17 @@ class CowBlockManager:
             self._drop(b)
         del self.lengths[seq]
 
+    def truncate(self, seq: str, num_tokens: int) -> None:
+        """Keep the first ``num_tokens`` tokens; blocks behind them lose a reference."""
+        if not 0 <= num_tokens <= self.lengths[seq]:
+            raise ValueError("a sequence can only be shortened")
+        table = self.tables[seq]
+        nb = -(-num_tokens // self.block_size)
+        for b in table[nb:]:
+            self._drop(b)
+        del table[nb:]
+        self.lengths[seq] = num_tokens
+
     # -- queries ------------------------------------------------------------
     def take_copies(self) -> List[Tuple[int, int]]:
         out, self.pending_copies = self.pending_copies, []

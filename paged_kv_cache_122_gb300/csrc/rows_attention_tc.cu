@@ -865,7 +865,7 @@ rows_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                     // and the largest score beside them.  Only where that moves the
                     // reference (a part's first job, seldom later) is the pass made again.
                     // P is bf16 pairs over the first half of S (the A operand of P.V): half
-                    // the tensor work of fp32 weights at an error of 2^-9 of each; the
+                    // the tensor work of fp32 weights at an error of 2^-8 of each; the
                     // denominator sums the rounded weights, so that their mean stays one.
                     uint32_t packed[32];
                     float lsum;
