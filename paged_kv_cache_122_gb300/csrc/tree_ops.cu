@@ -3,6 +3,8 @@
 #include "../../include/pagedkv_tree.h"
 #include "common.cuh"
 
+#include <algorithm>
+
 namespace {
 
 template <typename... Params, typename... Args>
@@ -73,14 +75,20 @@ accept_tree_kernel(int32_t *accepted, int32_t *num_accepted, int64_t *next_token
 }
 
 // ------------------------------------------------------------------ keep_tokens
-// grid (sequences, layers x 2 [K, V], chunks of a token's row).  A pass takes as
-// many tokens as give every thread kKeepVecs 16-byte vectors: all are read, then
-// all are written.  Lists increase strictly, so accepted[i] >= i, and a row that a
-// pass writes (i) comes before every row that a later pass reads (accepted[j] >= j
-// > i).  Bound by memory: two rows moved per kept token that is not in its place.
-constexpr int kKeepThreads = 128;
-constexpr int kKeepVecs = 8;
-constexpr int kKeepColumns = 128;    // vectors of a row in one chunk (at most)
+// One CTA per sequence and group of layers.  It checks the list and looks up the rows'
+// places once (a chunk of tokens at a time), then moves them in each of its layers' K
+// and V.  A unit of a warp is 512 bytes of a row; a pass takes kKeepUnits a warp: all
+// are read, then all are written.  Lists increase strictly, so accepted[i] >= i, tokens
+// in their place are a prefix, and a row that a pass writes (i) comes before every row
+// that a later pass reads (accepted[j] >= j > i).  Bound by memory: two rows moved for
+// each kept token that is not in its place.  (A CTA per layer, K or V and sequence
+// looked everything up 64 times for 32 layers: 25 us where this takes 18, for 128
+// sequences.)
+constexpr int kKeepThreads = 256;
+constexpr int kKeepWarps = kKeepThreads / 32;
+constexpr int kKeepUnits = 8;
+constexpr int kKeepChunk = 256;      // tokens whose places are looked up together
+constexpr int kKeepGroup = 64;       // layers of a CTA (at most)
 
 struct KeepParams {
     uint4 *k_cache, *v_cache;                 // one layer, or
@@ -91,75 +99,107 @@ struct KeepParams {
     int accepted_stride;
     const int32_t *num_accepted;
     int row_vecs, num_blocks, log2_block;
+    int num_layers, group;                    // layers; layers of a CTA
     unsigned int *err;
 };
 
 __global__ void __launch_bounds__(kKeepThreads)
 keep_tokens_kernel(const KeepParams p) {
+    __shared__ int64_t src[kKeepChunk], dst[kKeepChunk];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int s = blockIdx.x;
-    const bool reports = blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0;
+    const int s = blockIdx.x, layer0 = blockIdx.y * p.group, layers = min(p.group, p.num_layers - layer0);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool reports = blockIdx.y == 0 && threadIdx.x == 0;
     const int L = p.seq_lens[s], q0 = p.cu_q_lens[s], q1 = p.cu_q_lens[s + 1];
     const int n = p.num_accepted[s];
     const int32_t *list = p.accepted + static_cast<size_t>(s) * p.accepted_stride;
     const int64_t cap = static_cast<int64_t>(p.max_blocks_per_seq) << p.log2_block;
+    if (p.k_layers && s == 0) {
+        // A layer that cannot be used is reported by the first sequence's CTAs.
+        for (int l = threadIdx.x; l < layers; l += kKeepThreads) {
+            const uintptr_t both = reinterpret_cast<uintptr_t>(p.k_layers[layer0 + l]) |
+                                   reinterpret_cast<uintptr_t>(p.v_layers[layer0 + l]);
+            if (!p.k_layers[layer0 + l] || !p.v_layers[layer0 + l] || (both & 15u)) pk::set_error(p.err, PK_DEVERR_POINTER);
+        }
+    }
     if (L < 0 || L > cap || q0 < 0 || q1 < q0 || q1 - q0 > L) {
         if (reports) pk::set_error(p.err, PK_DEVERR_SEQ_LEN);
         return;
     }
     const int nodes = q1 - q0;
     bool bad = n < 0 || n > nodes || n > p.accepted_stride;
+    int moved = 0;                               // tokens that are not in their place
     if (!bad)
         for (int i = threadIdx.x; i < n; i += kKeepThreads) {
             const int at = list[i];
             bad |= at >= nodes || at <= (i > 0 ? list[i - 1] : -1);
+            moved += at != i;
         }
     if (__syncthreads_or(bad)) {
         if (reports) pk::set_error(p.err, PK_DEVERR_DRAFT);
         return;
     }
-    uint4 *cache;
-    if (p.k_layers) {
-        cache = (blockIdx.y & 1 ? p.v_layers : p.k_layers)[blockIdx.y >> 1];
-        if (!cache || (reinterpret_cast<uintptr_t>(cache) & 15u)) {
-            if (s == 0 && blockIdx.z == 0 && threadIdx.x == 0) pk::set_error(p.err, PK_DEVERR_POINTER);
-            return;
-        }
-    } else {
-        cache = blockIdx.y & 1 ? p.v_cache : p.k_cache;
-    }
+    __shared__ int total;
+    if (threadIdx.x == 0) total = 0;
+    __syncthreads();
+    if (moved) atomicAdd(&total, moved);
+    __syncthreads();
+    const int first = n - total;                 // (integer sum: the order does not matter)
     const int32_t *table = p.block_tables + static_cast<size_t>(s) * p.max_blocks_per_seq;
     const int B1 = (1 << p.log2_block) - 1;
     const int base = L - nodes;
-    const int col0 = blockIdx.z * kKeepColumns;
-    const int cols = min(kKeepColumns, p.row_vecs - col0);
-    const int per = kKeepThreads * kKeepVecs / cols;          // tokens of a pass
-    for (int i0 = 0; i0 < n; i0 += per) {
-        const int items = min(per, n - i0) * cols;
-        uint4 buf[kKeepVecs];
-        int64_t dst[kKeepVecs];
-#pragma unroll
-        for (int u = 0; u < kKeepVecs; ++u) {
-            const int e = u * kKeepThreads + threadIdx.x;
-            dst[u] = -1;
-            if (e >= items) continue;
-            const int i = i0 + e / cols, col = e % cols;
-            const int from = list[i];
-            if (from == i) continue;                          // in its place
-            const int sp = base + from, dp = base + i;
+    const int segs = (p.row_vecs + 31) >> 5;     // units of a row
+    for (int i0 = first; i0 < n; i0 += kKeepChunk) {
+        const int count = min(kKeepChunk, n - i0);
+        __syncthreads();                         // the last chunk's places have been used
+        for (int j = threadIdx.x; j < count; j += kKeepThreads) {
+            const int sp = base + list[i0 + j], dp = base + i0 + j;
             const int sb = table[sp >> p.log2_block], db = table[dp >> p.log2_block];
-            if (sb < 0 || sb >= p.num_blocks || db < 0 || db >= p.num_blocks) {
-                pk::set_error(p.err, PK_DEVERR_BLOCK_ID);
-                continue;
-            }
-            buf[u] = cache[((static_cast<int64_t>(sb) << p.log2_block) + (sp & B1)) * p.row_vecs + col0 + col];
-            dst[u] = ((static_cast<int64_t>(db) << p.log2_block) + (dp & B1)) * p.row_vecs + col0 + col;
+            const bool ok = sb >= 0 && sb < p.num_blocks && db >= 0 && db < p.num_blocks;
+            if (!ok) pk::set_error(p.err, PK_DEVERR_BLOCK_ID);
+            src[j] = ok ? ((static_cast<int64_t>(sb) << p.log2_block) + (sp & B1)) * p.row_vecs : -1;
+            dst[j] = ((static_cast<int64_t>(db) << p.log2_block) + (dp & B1)) * p.row_vecs;
         }
         __syncthreads();
+        // Units in the order (layer, K or V, token, piece of its row): of one cache, a
+        // pass's tokens come before the next pass's.
+        const uint32_t row_units = static_cast<uint32_t>(count) * segs;
+        const uint32_t units = row_units * 2 * layers;          // (kKeepGroup keeps it within 32 bits)
+        uint32_t per;
+        for (uint32_t u0 = 0; u0 < units; u0 += kKeepWarps * per) {
+            per = min(static_cast<uint32_t>(kKeepUnits), (units - u0 + kKeepWarps - 1) / kKeepWarps);
+            uint4 buf[kKeepUnits];
+            uint4 *to[kKeepUnits];
+            // A warp's units of the pass lie one behind the other: one division a pass.
+            uint32_t unit = u0 + warp * per;
+            uint32_t lk = unit / row_units, j = unit % row_units / segs, seg = unit % row_units % segs;
 #pragma unroll
-        for (int u = 0; u < kKeepVecs; ++u)
-            if (dst[u] >= 0) cache[dst[u]] = buf[u];
+            for (int u = 0; u < kKeepUnits; ++u, ++unit) {
+                to[u] = nullptr;
+                if (static_cast<uint32_t>(u) < per && unit < units) {
+                    const uint32_t col = seg * 32 + lane;
+                    uint4 *cache = p.k_layers ? (lk & 1 ? p.v_layers : p.k_layers)[layer0 + (lk >> 1)]
+                                              : (lk & 1 ? p.v_cache : p.k_cache);
+                    if (src[j] >= 0 && col < static_cast<uint32_t>(p.row_vecs) && cache &&
+                        (reinterpret_cast<uintptr_t>(cache) & 15u) == 0) {
+                        buf[u] = cache[src[j] + col];
+                        to[u] = cache + dst[j] + col;
+                    }
+                }
+                if (++seg == static_cast<uint32_t>(segs)) {
+                    seg = 0;
+                    if (++j == static_cast<uint32_t>(count)) {
+                        j = 0;
+                        ++lk;
+                    }
+                }
+            }
+            __syncthreads();
+#pragma unroll
+            for (int u = 0; u < kKeepUnits; ++u)
+                if (to[u]) *to[u] = buf[u];
+        }
     }
 }
 
@@ -178,8 +218,13 @@ int keep(KeepParams &p, const void *const *ptrs, int num_seqs, int num_layers, i
     p.row_vecs = num_kv_heads * head_dim / 8;
     p.log2_block = block_size == 8 ? 3 : block_size == 16 ? 4 : 5;
     p.err = pk::error_word_ptr();
-    if (!p.err) return PK_ERR_NO_DEVICE;
-    const dim3 grid(num_seqs, 2 * num_layers, (p.row_vecs + kKeepColumns - 1) / kKeepColumns);
+    const int sms = pk::sm_count();
+    if (!p.err || sms <= 0) return PK_ERR_NO_DEVICE;
+    // As many layers to a CTA as still leave eight CTAs for each SM (128 sequences, 32 layers: 18 us;
+    // four for each SM 20, two 23, one layer to a CTA 24).
+    p.num_layers = num_layers;
+    p.group = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kKeepGroup, static_cast<int64_t>(num_seqs) * num_layers / (8 * sms))));
+    const dim3 grid(num_seqs, (num_layers + p.group - 1) / p.group);
     return launch_dependent(keep_tokens_kernel, grid, kKeepThreads, 0, reinterpret_cast<cudaStream_t>(stream), p) ==
                    cudaSuccess ? PK_OK : PK_ERR_CUDA;
 }
@@ -211,7 +256,7 @@ extern "C" int pk_keep_tokens(void *k_cache, void *v_cache, const int32_t *block
     const void *ptrs[2] = {k_cache, v_cache};
     KeepParams p{static_cast<uint4 *>(k_cache), static_cast<uint4 *>(v_cache), nullptr, nullptr, block_tables,
                  max_blocks_per_seq, seq_lens, cu_q_lens, accepted, accepted_stride, num_accepted, 0, num_blocks, 0,
-                 nullptr};
+                 0, 0, nullptr};
     return keep(p, ptrs, num_seqs, 1, num_kv_heads, head_dim, block_size, true, stream);
 }
 
@@ -223,6 +268,6 @@ extern "C" int pk_keep_tokens_layers(void *const *k_cache_layers, void *const *v
     const void *ptrs[2] = {k_cache_layers, v_cache_layers};
     KeepParams p{nullptr, nullptr, reinterpret_cast<uint4 *const *>(k_cache_layers),
                  reinterpret_cast<uint4 *const *>(v_cache_layers), block_tables, max_blocks_per_seq, seq_lens, cu_q_lens,
-                 accepted, accepted_stride, num_accepted, 0, num_blocks, 0, nullptr};
+                 accepted, accepted_stride, num_accepted, 0, num_blocks, 0, 0, 0, nullptr};
     return keep(p, ptrs, num_seqs, num_layers, num_kv_heads, head_dim, block_size, false, stream);
 }

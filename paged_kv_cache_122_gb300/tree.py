@@ -154,9 +154,10 @@ def pk_accept_tree(draft_tokens: torch.Tensor, parents: torch.Tensor, target_tok
     if max_q_len < 0:
         raise ValueError("max_q_len must not be negative")
     with torch.cuda.stream(stream) if stream is not None else _NOTHING:
-        accepted = torch.empty((N, max_q_len), dtype=torch.int32, device=dev)
+        # (From a tensor at hand: torch.empty with a device takes 2 us longer.)
+        accepted = seq_lens.new_empty((N, max_q_len))
         num = torch.empty_like(seq_lens)
-        following = torch.empty((N,), dtype=torch.int64, device=dev)
+        following = torch.empty_like(seq_lens, dtype=torch.int64)
         lens = torch.empty_like(seq_lens)
     if stream is not None:
         for t in (accepted, num, following, lens):
