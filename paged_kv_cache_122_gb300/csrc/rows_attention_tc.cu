@@ -59,10 +59,15 @@ constexpr uint32_t kTmemO = 256;                // + x * 128
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
 constexpr float kRescaleLog2 = 8.0f;
 
-// What a part costs, in units of 0.1 us: a segment's set-up and read-out, a key
-// tile under one query tile (bound by the copies) and under two (by the softmax
-// groups and the MMAs).
-constexpr int64_t kSegCost = 16, kTileCost1 = 16, kTileCost2 = 24;
+// What a part costs, in sixteenths of a key tile under one query tile: a segment's
+// set-up and read-out, and a key tile under two query tiles.  From a least-squares fit
+// of the CTAs' times to the tiles and segments of their ranges (eight batches): head dim
+// 128, a tile 1.2-1.3 us, or 2.1 under two, a segment 2.3-3.9 us; head dim 64, 0.85-0.95,
+// 1.6 and 2.6-2.8 us.  (With a segment as one tile, the last CTA of 152 ended 15-30 %
+// after the mean on batches of short sequences.)
+constexpr int64_t kTileCost1 = 16, kTileCost2 = 27;
+template <int D>
+constexpr int64_t kSegCost = D == 128 ? 38 : 40;
 // A CTA is not given less than this: a cut costs a merge.
 constexpr int64_t kMinCost = 32;
 
@@ -195,11 +200,13 @@ __device__ __noinline__ int64_t quotient(int64_t a, int64_t b) {
     return a / b;
 }
 
+template <int D>
 __device__ __forceinline__ int64_t block_cost(const Seq &q, bool two) {
-    return kSegCost + (two ? kTileCost2 : kTileCost1) * q.nt;
+    return kSegCost<D> + (two ? kTileCost2 : kTileCost1) * q.nt;
 }
+template <int D>
 __device__ __forceinline__ int64_t head_cost(const Seq &q) {
-    return q.n2 * block_cost(q, true) + q.n1 * block_cost(q, false);
+    return q.n2 * block_cost<D>(q, true) + q.n1 * block_cost<D>(q, false);
 }
 
 // One CTA's part of a segment, and the walk from part to part.
@@ -251,10 +258,10 @@ struct Walk {
 
 // Cuts the flattened space: CTA c of C takes the tiles whose cost starts in
 // [c W / C, (c + 1) W / C), W the total cost, C no more than gives every CTA
-// kMinCost.  A segment's tile 0 starts at its start, tile t at start + kSegCost + t
-// tiles.  Every thread calls it; returns the total tile count, and in *odd whether
+// kMinCost.  A segment's tile 0 starts at its start, tile t at start + the segment's cost +
+// t tiles.  Every thread calls it; returns the total tile count, and in *odd whether
 // a sequence is to be reported or to get zeros.
-template <bool TWO, typename M>
+template <int D, bool TWO, typename M>
 __device__ __forceinline__ int64_t plan(const RowsParams &p, M *misc, int lgG, int c, int C, int *odd) {
     const int N = p.num_seqs, Hkv = p.num_kv_heads;
     const int per = (N + kThreads - 1) / kThreads;
@@ -266,7 +273,7 @@ __device__ __forceinline__ int64_t plan(const RowsParams &p, M *misc, int lgG, i
         const Seq q = load_seq<TWO>(p, s, lgG);
         strange |= q.bad || (q.qn > 0 && q.L == 0);
         mine += static_cast<int64_t>(q.nt) * (q.n2 + q.n1) * Hkv;
-        mine_w += head_cost(q) * Hkv;
+        mine_w += head_cost<D>(q) * Hkv;
     }
     int64_t T, W;
     const int64_t off = block_exclusive_scan<kThreads>(mine, misc->scan.tiles, &T);
@@ -285,7 +292,7 @@ __device__ __forceinline__ int64_t plan(const RowsParams &p, M *misc, int lgG, i
 #pragma unroll 1
         for (int s = s_lo; s < s_hi; ++s) {
             const Seq q = load_seq<TWO>(p, s, lgG);
-            const int64_t hc = head_cost(q);
+            const int64_t hc = head_cost<D>(q);
             if (P >= at_w + hc * Hkv) {
                 at += static_cast<int64_t>(q.nt) * (q.n2 + q.n1) * Hkv;
                 at_w += hc * Hkv;
@@ -294,15 +301,15 @@ __device__ __forceinline__ int64_t plan(const RowsParams &p, M *misc, int lgG, i
             int64_t r = P - at_w;
             int64_t h = quotient(r, hc);
             r -= h * hc;
-            const int64_t b2 = block_cost(q, true);
+            const int64_t b2 = block_cost<D>(q, true);
             int64_t j = min(quotient(r, b2), static_cast<int64_t>(q.n2));
             r -= j * b2;
             const int64_t tc = j < q.n2 ? kTileCost2 : kTileCost1;
             // The first tile that starts at or after r.
-            int64_t t = r == 0 ? 0 : r <= kSegCost ? 1 : quotient(r - kSegCost + tc - 1, tc);
+            int64_t t = r == 0 ? 0 : r <= kSegCost<D> ? 1 : quotient(r - kSegCost<D> + tc - 1, tc);
             int64_t a = P - r;                        // where the segment starts
             if (t >= q.nt) {                          // behind its last one: the next segment
-                a += block_cost(q, j < q.n2);
+                a += block_cost<D>(q, j < q.n2);
                 t = 0;
                 if (++j == q.n2 + q.n1) {
                     j = 0;
@@ -482,7 +489,7 @@ rows_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
     int64_t T;
 #pragma unroll 1
     for (;;) {
-        T = plan<TWO>(p, misc, lgG, c, C, &odd);
+        T = plan<D, TWO>(p, misc, lgG, c, C, &odd);
         if (!ahead) break;
         ahead = false;
         wait_prev();

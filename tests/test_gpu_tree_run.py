@@ -183,7 +183,8 @@ def _timeout_case(rows, lens):
 
 @pytest.mark.parametrize("rows,lens,stall", [(8, [60000, 90000], 1), (8, [60000, 90000], 6), (200, [6000, 9000], 2)])
 def test_wait_runs_out_and_the_next_call_is_correct(rows, lens, stall):
-    # CTA 0 has 15 key tiles of the long sequences' 2,346, or 5 of 4 blocks' 944.
+    # CTA 0's range holds more key tiles than that: 14 of the long sequences' 2,346, 5 of
+    # the wide blocks' 944.
     args, kw = _timeout_case(rows, lens)
     want = pk.paged_attention_cross(*args, **kw)
     clean()
@@ -199,7 +200,7 @@ def test_wait_runs_out_and_the_next_call_is_correct(rows, lens, stall):
 
 @pytest.mark.parametrize("stall", [1, 6])
 def test_a_stall_beyond_the_range_does_nothing(stall):
-    # 236 tiles of 16 and 4 segments of 16 more make 118 ranges of 32: tile 1 starts at 32,
+    # 236 tiles of 16 and 4 segments of 38 more make 122 ranges of 32: tile 1 starts at 54,
     # so CTA 0 has tile 0 alone.
     args, kw = _timeout_case(8, [6000, 9000])
     want = pk.paged_attention_cross(*args, **kw)
