@@ -3,8 +3,8 @@
 // in full) and cross attention (every key).
 //
 // Mathematics.  For a query row, scores s_j = c q.k_j (c holds log2 e) over the
-// visible keys; weights 2^(s_j - m) against a reference max m that moves only when
-// a score exceeds it by more than 8; O = sum of weights times v_j, l = sum of
+// visible keys; weights 2^(s_j - m) against a reference m that moves only when a
+// score exceeds it by more than 16; O = sum of weights times v_j, l = sum of
 // weights, result O / l.  Parts over disjoint keys join by M = max m, factors
 // 2^(m - M): between the two groups of a CTA and between CTAs.
 //
@@ -57,7 +57,14 @@ constexpr uint32_t kTmemCols = 512;             // S_0, S_1, O_0, O_1 (128 colum
 constexpr uint32_t kTmemS = 0;                  // + x * 128 + buffer * 64; P over its first 32 columns
 constexpr uint32_t kTmemO = 256;                // + x * 128
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
-constexpr float kRescaleLog2 = 8.0f;
+// A reference max is whole (weights then round alike whatever it is) and this far above
+// the scores that set it; it moves when a score exceeds it by kRescaleLog2.  Weights of
+// any size are exact to the same number of bits, and stay below 2^16; scores have to
+// climb by 24 before a pass is made again.
+constexpr float kHeadroomLog2 = 8.0f, kRescaleLog2 = 16.0f;
+// A part starts from its row's reference of the part before, if no score of its first
+// job is above it and the largest is not this far below.
+constexpr float kGuessLog2 = -60.0f;
 
 // What a part costs, in sixteenths of a key tile under one query tile: a segment's
 // set-up and read-out, and a key tile under two query tiles.  From a least-squares fit
@@ -817,6 +824,7 @@ rows_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
         int ktile = 0;                                  // key tile (of the CTA's range) at the part's start
         int jobs = 0;                                   // jobs so far (both groups have as many)
         int joins = 0;                                  // joins of two groups so far
+        float m_ref = -INFINITY;                        // the row's reference max
         bool owe = false;                               // the other group still reads this group's O
         bool alive = true;
         auto wait = [&](uint64_t *bar, int phase) -> bool { return warp_wait(bar, phase, &misc->abort, lim); };
@@ -845,7 +853,8 @@ rows_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                 for (int w = 0; w < 3; ++w)
                     mw[w] = at + w < 0 ? 0xffffffffu : (at + w < p.mask_words ? mrow_bits[at + w] : 0u);
             };
-            float m_ref = -INFINITY, l_run = 0.f;
+            if (!(fabsf(m_ref) < 1e30f)) m_ref = -INFINITY;    // (the part before's, as a guess)
+            float l_run = 0.f;
             fetch_mask(0);
             for (int i = 0; i < njobs; ++i, ++jobs) {
                 const int u = jobs & 1;
@@ -870,7 +879,7 @@ rows_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                     fetch_mask(i + 1);
                     // One pass over the row: weights against the reference max as it is,
                     // and the largest score beside them.  Only where that moves the
-                    // reference (a part's first job, seldom later) is the pass made again.
+                    // reference (the first part's first job, seldom later) is the pass made again.
                     // P is bf16 pairs over the first half of S (the A operand of P.V): half
                     // the tensor work of fp32 weights at an error of 2^-8 of each; the
                     // denominator sums the rounded weights, so that their mean stays one.
@@ -905,11 +914,16 @@ rows_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                         const float tmax = fmaxf(max3(e[0], e[1], e[2]), e[3]);
                         const float2 la = unf2(lacc[0]), lb = unf2(lacc[1]);
                         lsum = (la.x + la.y) + (lb.x + lb.y);
-                        const bool need = !idle_row && (m_ref == -INFINITY ? tmax > -INFINITY : tmax > kRescaleLog2);
+                        bool need = m_ref == -INFINITY ? tmax > -INFINITY : tmax > kRescaleLog2;
+                        if (i == 0) {
+                            if (tmax == -INFINITY) m_ref = -INFINITY;      // nothing seen: no reference
+                            else need |= tmax < kGuessLog2;
+                        }
+                        need &= !idle_row;
                         if (pass == 2 || !__any_sync(0xffffffffu, need)) break;
                         // Move this row's reference max and rescale its O (of the jobs so
                         // far) and denominator.
-                        const float mn = need ? (m_ref == -INFINITY ? tmax : m_ref + tmax) : m_ref;
+                        const float mn = need ? ceilf(m_ref == -INFINITY ? tmax : m_ref + tmax) + kHeadroomLog2 : m_ref;
                         const float f = rescale(m_ref, mn);
                         if (i > 0) {
                             if (!wait(&misc->pv_done[x][u ^ 1], (jobs - 1) >> 1)) {
