@@ -266,18 +266,23 @@ struct Walk {
 // Cuts the flattened space: CTA c of C takes the tiles whose cost starts in
 // [c W / C, (c + 1) W / C), W the total cost, C no more than gives every CTA
 // kMinCost.  A segment's tile 0 starts at its start, tile t at start + the segment's cost +
-// t tiles.  Every thread calls it; returns the total tile count, and in *odd whether
+// t tiles.  The sequences (length, first row, next one's first row, kThreads apart) come
+// from `copy` if there is one.  Every thread calls it; returns the total tile count, and in *odd whether
 // a sequence is to be reported or to get zeros.
 template <int D, bool TWO, typename M>
-__device__ __forceinline__ int64_t plan(const RowsParams &p, M *misc, int lgG, int c, int C, int *odd) {
+__device__ __forceinline__ int64_t plan(const RowsParams &p, M *misc, const int32_t *copy, int lgG, int c, int C,
+                                        int *odd) {
     const int N = p.num_seqs, Hkv = p.num_kv_heads;
+    auto seq = [&](int s) -> Seq {
+        return seq_of<TWO>(p, copy ? Raw{copy[s], copy[kThreads + s], copy[2 * kThreads + s]} : load_raw(p, s), lgG);
+    };
     const int per = (N + kThreads - 1) / kThreads;
     const int s_lo = min(N, static_cast<int>(threadIdx.x) * per), s_hi = min(N, s_lo + per);
     int64_t mine = 0, mine_w = 0;
     int strange = 0;
 #pragma unroll 1
     for (int s = s_lo; s < s_hi; ++s) {
-        const Seq q = load_seq<TWO>(p, s, lgG);
+        const Seq q = seq(s);
         strange |= q.bad || (q.qn > 0 && q.L == 0);
         mine += static_cast<int64_t>(q.nt) * (q.n2 + q.n1) * Hkv;
         mine_w += head_cost<D>(q) * Hkv;
@@ -298,7 +303,7 @@ __device__ __forceinline__ int64_t plan(const RowsParams &p, M *misc, int lgG, i
         int64_t at = off, at_w = off_w;
 #pragma unroll 1
         for (int s = s_lo; s < s_hi; ++s) {
-            const Seq q = load_seq<TWO>(p, s, lgG);
+            const Seq q = seq(s);
             const int64_t hc = head_cost<D>(q);
             if (P >= at_w + hc * Hkv) {
                 at += static_cast<int64_t>(q.nt) * (q.n2 + q.n1) * Hkv;
@@ -329,7 +334,7 @@ __device__ __forceinline__ int64_t plan(const RowsParams &p, M *misc, int lgG, i
                 h = 0;
                 int s2 = s;
 #pragma unroll 1
-                while (++s2 < N && load_seq<TWO>(p, s2, lgG).nt == 0) {}
+                while (++s2 < N && seq(s2).nt == 0) {}
                 o.s = s2;
             } else {
                 o.s = s;
@@ -481,32 +486,49 @@ rows_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
     }
     // A programmatic dependent of the previous kernel in the stream: what comes before the
     // wait overlaps that kernel's tail.  With a sequence a thread at most, the range is
-    // planned before it; afterwards the lengths are read again, and the plan is made again
-    // if one changed.  Nothing else global is read before the wait, and nothing written.
+    // planned before it, from a copy of the lengths in what will be the rings; afterwards
+    // they are read again, and the plan is made again if one differs from the copy.  (From
+    // the copy, not from memory: what is written there meanwhile, and written back, would
+    // not show afterwards.)  Nothing else global is read before the wait, and nothing
+    // written.
     auto wait_prev = [&]() {
         asm volatile("griddepcontrol.wait;" ::: "memory");
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     };
-    const int own_seq = static_cast<int>(threadIdx.x) < p.num_seqs ? static_cast<int>(threadIdx.x) : -1;
     bool ahead = p.num_seqs <= kThreads;
+    int32_t *copy = ahead ? reinterpret_cast<int32_t *>(smem + C_::kKOff) : nullptr;
+    static_assert(3 * kThreads * sizeof(int32_t) <= C_::kTile, "room for the copy");
+    const bool owner = ahead && static_cast<int>(threadIdx.x) < p.num_seqs;     // (of a sequence)
     Raw seen{0, 0, 0};
-    if (!ahead) wait_prev();
-    else if (own_seq >= 0) seen = load_raw(p, own_seq);
+    auto put = [&]() {
+        copy[threadIdx.x] = seen.L;
+        copy[kThreads + threadIdx.x] = seen.q0;
+        copy[2 * kThreads + threadIdx.x] = seen.q1;
+    };
+    if (owner) {
+        seen = load_raw(p, threadIdx.x);
+        put();
+    }
+    if (ahead) __syncthreads();
+    else wait_prev();
     int odd;
     int64_t T;
 #pragma unroll 1
     for (;;) {
-        T = plan<D, TWO>(p, misc, lgG, c, C, &odd);
+        T = plan<D, TWO>(p, misc, copy, lgG, c, C, &odd);
         if (!ahead) break;
         ahead = false;
         wait_prev();
         bool changed = false;
-        if (own_seq >= 0) {
-            const Raw now = load_raw(p, own_seq);
+        if (owner) {
+            const Raw now = load_raw(p, threadIdx.x);
             changed = now.L != seen.L || now.q0 != seen.q0 || now.q1 != seen.q1;
+            seen = now;
+            put();
         }
         if (!__syncthreads_or(changed)) break;
     }
+    fence_proxy_async_smem();                // the copy's place goes to the rings
     const Pos from = misc->pos[0];
     const int64_t n_tiles = misc->pos[1].tile - from.tile;
     if (threadIdx.x == 0 && p.slots) {

@@ -67,6 +67,22 @@ def test_accept_bad_rows_are_reported():
         pk.accept_tree(tok, par[:5], tok, dev(np.asarray([0, 6], np.int32)), 6, dev(np.asarray([9], np.int32)))
 
 
+def test_accept_into_the_lengths_themselves():
+    sizes = [3, 70, 1]
+    parents, tokens, targets = _trees(5, sizes, 2)
+    cu = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)
+    lens = dev(np.asarray([9, 70, 4], np.int32))
+    t = [dev(np.concatenate([np.asarray(a, d) for a in x])) for x, d in ((tokens, np.int64), (parents, np.int32), (targets, np.int64))]
+    rows = dev(cu)
+    want = pk.accept_tree(*t, rows, 70, lens)
+    acc, num, nxt = (torch.empty_like(x) for x in want[:3])
+    st = _native.load().pk_accept_tree(acc.data_ptr(), num.data_ptr(), nxt.data_ptr(), lens.data_ptr(), t[0].data_ptr(),
+                                       t[1].data_ptr(), t[2].data_ptr(), 74, rows.data_ptr(), 70, lens.data_ptr(), 3,
+                                       torch.cuda.current_stream().cuda_stream)
+    assert st == 0 and all(torch.equal(a, b) for a, b in zip((acc, num, nxt, lens), want))
+    clean()
+
+
 class Pool:
     def __init__(self, seed, sizes, ctx, Hkv, D, B, layers=1):
         rng = np.random.default_rng(seed)

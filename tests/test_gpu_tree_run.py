@@ -173,6 +173,33 @@ def test_lengths_that_the_kernel_before_writes(busy_mb):
     clean()
 
 
+def test_lengths_that_are_written_and_written_back():
+    # Two calls before the attention change the lengths and change them back while it may
+    # already plan: the plan has to be of the lengths that it compares afterwards.
+    c = Case(16, [700, 40, 333], [4, 4, 4], 4, 2, 64, 16, False)
+    cu, tb = dev(c.cu), dev(c.tables)
+    want = c.run()
+    lib = _native.load()
+    z = torch.zeros(12, dtype=torch.int64, device=DEV)
+    par = dev(np.asarray([-1, 0, 1, 2] * 3, np.int32))
+    acc, num, nxt = (torch.empty(n, dtype=d, device=DEV) for n, d in ((12, torch.int32), (3, torch.int32), (3, torch.int64)))
+    final, other = dev(np.asarray(c.lens, np.int32)), dev(np.asarray([64, 690, 5], np.int32))
+    buf = final.clone()
+    big = torch.empty(128 << 20, dtype=torch.uint8, device=DEV)
+    ws = pk.new_workspace(pk.pk_tree_workspace_bytes(8, 2, 64, 4, 700), DEV)
+    for trial in range(20):
+        out = torch.zeros_like(want)
+        big.fill_(trial)
+        st = torch.cuda.current_stream().cuda_stream
+        for src in (other, final):
+            # (Every node is accepted: the new lengths are the old ones.)
+            assert lib.pk_accept_tree(acc.data_ptr(), num.data_ptr(), nxt.data_ptr(), buf.data_ptr(), z.data_ptr(),
+                                      par.data_ptr(), z.data_ptr(), 12, cu.data_ptr(), 4, src.data_ptr(), 3, st) == 0
+        pk.paged_attention_cross(c.q, cu, 4, c.k, c.v, tb, buf, c.scale, out=out, max_seq_len=700, workspace=ws)
+        assert torch.equal(out, want)
+    clean()
+
+
 def _timeout_case(rows, lens):
     c = Case(rows, lens, [rows] * len(lens), 4, 2, 128, 16, False)
     args = (c.q, dev(c.cu), rows, c.k, c.v, dev(c.tables), dev(np.asarray(c.lens, np.int32)), c.scale)
