@@ -133,13 +133,15 @@ struct Misc {
 // Slot of a cut part: slot 0 of a CTA for its first segment, slot 1 for its last.
 struct SlotHead {
     int32_t flag;          // slot 0: the merge joins this segment at this CTA
-    int32_t s, h, tok0;    // sequence, KV head, first token of the block's first tile
+    int32_t h, tok0;       // KV head, first token of the block's first tile
     int32_t ntiles;        // query tiles
+    int32_t q0, qn;        // the sequence's query rows (the merge saves a trip to memory)
     int32_t first_cta;     // slot 0: the CTA in whose range the segment starts
-    int64_t start_tile;    // flattened index of the segment's key tile 0
+    int32_t pad0;
+    int64_t start_tile;    // slot 0: flattened index of the segment's key tile 0
     int64_t range_beg;     // slot 0: first tile of this CTA's range
     int64_t total_tiles;   // slot 0
-    int64_t pad[2];
+    int64_t pad1;
 };
 static_assert(sizeof(SlotHead) == 64, "slot header");
 
@@ -1085,10 +1087,11 @@ rows_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                 sm[kRows + row] = l_run;
                 if (row == 0 && tile_x == 0) {
                     SlotHead *hd = reinterpret_cast<SlotHead *>(slot);
-                    hd->s = a.s;
                     hd->h = a.h;
                     hd->tok0 = a.tok0;
                     hd->ntiles = per;
+                    hd->q0 = q.q0;
+                    hd->qn = q.qn;
                     if (first_part) {
                         // Cut at its start and finished here: this CTA's merge joins it.
                         hd->start_tile = from.tile - a.t0;
@@ -1137,7 +1140,7 @@ rows_merge_kernel(const __grid_constant__ RowsParams p, int C, int slot_tiles) {
     const int64_t before = head(c > 0 ? c - 1 : 0)->range_beg;     // (the usual first part's)
     if (hd.flag != 1) return;
     const int lgG = __ffs(p.num_heads / p.num_kv_heads) - 1, G = 1 << lgG;
-    const int q0 = p.cu_q_lens[hd.s], qn = p.cu_q_lens[hd.s + 1] - q0;
+    const int q0 = hd.q0, qn = hd.qn;
     // CTA cc's part, from its slot 0 if the segment is the first of its range, else 1; a
     // range may be empty (more CTAs than tiles) and then has none.
     auto range_beg = [&](int cc) -> int64_t { return cc == c ? hd.range_beg : cc == c - 1 ? before : head(cc)->range_beg; };
