@@ -85,6 +85,8 @@ enum pk_dtype { PK_BF16 = 0, PK_FP32 = 1 };
                                     [2^-64, 2^64] or not a number */
 #define PK_DEVERR_DRAFT    0x80u /* a list of accepted drafts (pagedkv_tree.h) is not strictly
                                     increasing or does not fit its tree */
+#define PK_DEVERR_WORKSPACE 0x100u /* partial results in the workspace were another call's: calls
+                                    that share one ran at the same time (the results are invalid) */
 #define PK_DEVERR_POINTER  0x20u /* a per-layer pointer of a *_layers call is NULL or not
                                     16-byte aligned (that layer was skipped) */
 
@@ -142,7 +144,9 @@ size_t pk_decode_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads,
  *                 usual attention)
  *   workspace     device scratch of at least pk_decode_workspace_bytes(...)
  *                 bytes; its contents on entry do not matter.  Calls that share
- *                 one workspace must be ordered on the GPU (same stream).
+ *                 one workspace must be ordered on the GPU (same stream;
+ *                 several host threads may make them, each call's kernels stay
+ *                 together in the stream's order).
  *
  * Long sequences are split into partitions processed in parallel and combined
  * by a log-sum-exp merge ("PagedAttention from First Principles", §17: the

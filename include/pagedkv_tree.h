@@ -49,7 +49,9 @@ size_t pk_tree_workspace_bytes(int num_heads, int num_kv_heads, int head_dim, in
  *   tree_mask     [total_q, mask_words] 64-bit words, row r that of query row r,
  *                 8-byte aligned
  *   mask_words    at least ceil(max_q_len / 64)
- *   workspace     pk_tree_workspace_bytes(...); its contents do not matter
+ *   workspace     pk_tree_workspace_bytes(...); its contents do not matter.
+ *                 Calls that share one must be ordered on the GPU (same stream,
+ *                 from any number of host threads)
  *
  * Any number of nodes and any supported group run on one kernel: 128 (node, head)
  * rows to a tile.  A sequence with a negative length or one beyond max_seq_len or

@@ -91,6 +91,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 // Host-side helpers shared by the translation units (defined in errors.cu).
 namespace pk {
+// The current device (-1 on failure).
+int current_device();
 // Device address of the current device's error word (nullptr on failure).
 unsigned int *error_word_ptr();
 // Multiprocessor count of the current device (0 on failure).

@@ -1,6 +1,7 @@
 // Host entry point of paged decode attention: argument checks, the split-K
 // plan and the launches.
 #include "decode.cuh"
+#include "stream_turn.cuh"
 
 #include <algorithm>
 #include <atomic>
@@ -130,6 +131,7 @@ int decode_impl(void *out, int out_dtype, const void *q, const void *k_cache, co
     p.err = pk::error_word_ptr();
     if (!p.err) return PK_ERR_NO_DEVICE;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const pk::StreamTurn turn(pk::current_device(), stream);
     if (tensor_core) return pk::launch_decode_tensor_core(p, st) == cudaSuccess ? PK_OK : PK_ERR_CUDA;
     if (pk::launch_decode_cuda_core(p, st) != cudaSuccess) return PK_ERR_CUDA;
     if (pk::launch_decode_merge(p, st) != cudaSuccess) return PK_ERR_CUDA;
@@ -243,6 +245,7 @@ extern "C" int pk_paged_attention_multi_query(void *out, int out_dtype, const vo
     if (!narrow)
         return pk::launch_prefill_tensor_core(p, max_q_len, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                    ? PK_OK : PK_ERR_CUDA;
+    const pk::StreamTurn turn(pk::current_device(), stream);
     return pk::launch_multi_query_tensor_core(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? PK_OK : PK_ERR_CUDA;
 }

@@ -1,6 +1,7 @@
 // Host entry points of attention over the 8-bit paged cache: argument checks
 // and the launch.
 #include "decode_fp8.cuh"
+#include "stream_turn.cuh"
 
 #include <cmath>
 
@@ -104,6 +105,7 @@ int attend(void *out, int out_dtype, const void *q, int total_q, const int32_t *
         return cudaLaunchKernelEx(&cfg, empty_sequences_kernel, static_cast<const pk::DecodeParams &>(p)) == cudaSuccess
                    ? PK_OK : PK_ERR_CUDA;
     }
+    const pk::StreamTurn turn(pk::current_device(), stream);
     return pk::launch_decode_fp8_tensor_core(p, st) == cudaSuccess ? PK_OK : PK_ERR_CUDA;
 }
 

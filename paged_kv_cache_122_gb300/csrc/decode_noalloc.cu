@@ -9,6 +9,7 @@
 // with its scratch in a fixed array of this library's own device memory and
 // allocates nothing.
 #include "decode.cuh"
+#include "stream_turn.cuh"
 
 #include <algorithm>
 #include <cmath>
@@ -115,5 +116,6 @@ extern "C" int pk_paged_attention_decode_noalloc(void *out, int out_dtype, const
     }
     p.err = pk::error_word_ptr();
     if (!p.err) return PK_ERR_NO_DEVICE;
+    const pk::StreamTurn turn(pk::current_device(), stream);
     return pk::launch_decode_tensor_core_grid(p, st, ctas) == cudaSuccess ? PK_OK : PK_ERR_CUDA;
 }

@@ -17,15 +17,15 @@ int g_sm_count[kMaxDevices];
 std::mutex g_mu;
 std::set<std::pair<int, const void *>> g_smem_attr_done;   // (device, kernel) pairs already raised
 
+}  // namespace
+
+namespace pk {
+
 int current_device() {
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return -1;
     return dev;
 }
-
-}  // namespace
-
-namespace pk {
 
 unsigned int *error_word_ptr() {
     int dev = current_device();

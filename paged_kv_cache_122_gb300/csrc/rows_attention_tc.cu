@@ -1141,6 +1141,13 @@ rows_merge_kernel(const __grid_constant__ RowsParams p, int C, int slot_tiles) {
     if (hd.flag != 1) return;
     const int lgG = __ffs(p.num_heads / p.num_kv_heads) - 1, G = 1 << lgG;
     const int q0 = hd.q0, qn = hd.qn;
+    // A header of another call (one on another stream that was given the same workspace)
+    // leads nowhere outside the slots and the output.
+    if (hd.first_cta < 0 || hd.first_cta > c || hd.ntiles < 1 || hd.ntiles > slot_tiles || hd.h < 0 ||
+        hd.h >= p.num_kv_heads || hd.tok0 < 0 || hd.tok0 >= qn || q0 < 0 || q0 > p.total_q - qn) {
+        if (threadIdx.x == 0) set_error(p.err, PK_DEVERR_WORKSPACE);
+        return;
+    }
     // CTA cc's part, from its slot 0 if the segment is the first of its range, else 1; a
     // range may be empty (more CTAs than tiles) and then has none.
     auto range_beg = [&](int cc) -> int64_t { return cc == c ? hd.range_beg : cc == c - 1 ? before : head(cc)->range_beg; };

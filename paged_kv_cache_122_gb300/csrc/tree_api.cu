@@ -1,6 +1,7 @@
 // Host entry points of tree and cross attention: argument checks and the launch.
 #include "../../include/pagedkv_tree.h"
 #include "rows_attention.cuh"
+#include "stream_turn.cuh"
 
 #include <cmath>
 
@@ -70,6 +71,7 @@ int attend(void *out, int out_dtype, const void *q, int total_q, const int32_t *
     p.stall_tile = stall_tile;
     p.err = pk::error_word_ptr();
     if (!p.err) return PK_ERR_NO_DEVICE;
+    const pk::StreamTurn turn(pk::current_device(), stream);
     return pk::launch_rows_attention(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? PK_OK : PK_ERR_CUDA;
 }
 
