@@ -148,8 +148,10 @@ int pk_keep_tokens(void *k_cache, void *v_cache, const int32_t *block_tables, in
                    const int32_t *num_accepted, int num_seqs, int num_kv_heads, int head_dim, int num_blocks,
                    int block_size, pk_stream_t stream);
 
-/* The same on every layer in one launch; pointer arrays, layers and
- * PK_DEVERR_POINTER as for pk_copy_blocks_layers (num_layers in [1, 32767]). */
+/* The same on every layer in one launch; pointer arrays and layers as for
+ * pk_copy_blocks_layers (num_layers in [1, 32767]).  A layer whose K or V pointer is
+ * NULL or not 16-byte aligned sets PK_DEVERR_POINTER and neither its K nor its V is
+ * moved, so that both stay rows of the same tokens. */
 int pk_keep_tokens_layers(void *const *k_cache_layers, void *const *v_cache_layers, const int32_t *block_tables,
                           int max_blocks_per_seq, const int32_t *seq_lens, const int32_t *cu_q_lens,
                           const int32_t *accepted, int accepted_stride, const int32_t *num_accepted, int num_seqs,

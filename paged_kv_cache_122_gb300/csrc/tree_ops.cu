@@ -106,6 +106,7 @@ struct KeepParams {
 __global__ void __launch_bounds__(kKeepThreads)
 keep_tokens_kernel(const KeepParams p) {
     __shared__ int64_t src[kKeepChunk], dst[kKeepChunk];
+    __shared__ uint4 *caches[kKeepGroup][2];     // K and V of the layers; NULL for a layer to leave alone
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int s = blockIdx.x, layer0 = blockIdx.y * p.group, layers = min(p.group, p.num_layers - layer0);
@@ -115,13 +116,16 @@ keep_tokens_kernel(const KeepParams p) {
     const int n = p.num_accepted[s];
     const int32_t *list = p.accepted + static_cast<size_t>(s) * p.accepted_stride;
     const int64_t cap = static_cast<int64_t>(p.max_blocks_per_seq) << p.log2_block;
-    if (p.k_layers && s == 0) {
-        // A layer that cannot be used is reported by the first sequence's CTAs.
-        for (int l = threadIdx.x; l < layers; l += kKeepThreads) {
-            const uintptr_t both = reinterpret_cast<uintptr_t>(p.k_layers[layer0 + l]) |
-                                   reinterpret_cast<uintptr_t>(p.v_layers[layer0 + l]);
-            if (!p.k_layers[layer0 + l] || !p.v_layers[layer0 + l] || (both & 15u)) pk::set_error(p.err, PK_DEVERR_POINTER);
+    // A layer of which K or V cannot be used is left alone, both of them: its rows have to
+    // stay those of the same tokens.  (Reported by the first sequence's CTAs.)
+    for (int l = threadIdx.x; l < layers; l += kKeepThreads) {
+        uint4 *k = p.k_layers ? p.k_layers[layer0 + l] : p.k_cache, *v = p.k_layers ? p.v_layers[layer0 + l] : p.v_cache;
+        if (!k || !v || ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 15u)) {
+            if (s == 0) pk::set_error(p.err, PK_DEVERR_POINTER);
+            k = v = nullptr;
         }
+        caches[l][0] = k;
+        caches[l][1] = v;
     }
     if (L < 0 || L > cap || q0 < 0 || q1 < q0 || q1 - q0 > L) {
         if (reports) pk::set_error(p.err, PK_DEVERR_SEQ_LEN);
@@ -179,10 +183,8 @@ keep_tokens_kernel(const KeepParams p) {
                 to[u] = nullptr;
                 if (static_cast<uint32_t>(u) < per && unit < units) {
                     const uint32_t col = seg * 32 + lane;
-                    uint4 *cache = p.k_layers ? (lk & 1 ? p.v_layers : p.k_layers)[layer0 + (lk >> 1)]
-                                              : (lk & 1 ? p.v_cache : p.k_cache);
-                    if (src[j] >= 0 && col < static_cast<uint32_t>(p.row_vecs) && cache &&
-                        (reinterpret_cast<uintptr_t>(cache) & 15u) == 0) {
+                    uint4 *cache = caches[lk >> 1][lk & 1];
+                    if (src[j] >= 0 && col < static_cast<uint32_t>(p.row_vecs) && cache) {
                         buf[u] = cache[src[j] + col];
                         to[u] = cache + dst[j] + col;
                     }
