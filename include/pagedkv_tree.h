@@ -59,7 +59,9 @@ size_t pk_tree_workspace_bytes(int num_heads, int num_kv_heads, int head_dim, in
  * the total_q given, sets PK_DEVERR_SEQ_LEN and its rows are left as they were,
  * as are rows that no sequence owns.  Keys behind a block id outside the pool are
  * not seen (PK_DEVERR_BLOCK_ID).  Weights are rounded to bf16 for the product
- * with V, and the denominator sums the rounded weights.  A value that is not
+ * with V, and the denominator sums the rounded weights, each of which is at most 1:
+ * results are finite while the number of keys times the largest value is below
+ * 2^127 and the scaled scores below 2^27.  A value that is not
  * finite in a node of the tree shows in all rows of its tree; a key that is not
  * finite shows only in the rows that see it.  Deterministic.
  */

@@ -3,8 +3,8 @@
 // in full) and cross attention (every key).
 //
 // Mathematics.  For a query row, scores s_j = c q.k_j (c holds log2 e) over the
-// visible keys; weights 2^(s_j - m) against a reference m that moves only when a
-// score exceeds it by more than 16; O = sum of weights times v_j, l = sum of
+// visible keys; weights 2^(s_j - m) against a reference m that starts above the row's
+// first scores and moves only when a score exceeds it; O = sum of weights times v_j, l = sum of
 // weights, result O / l.  Parts over disjoint keys join by M = max m, factors
 // 2^(m - M): between the two groups of a CTA and between CTAs.
 //
@@ -57,14 +57,15 @@ constexpr uint32_t kTmemCols = 512;             // S_0, S_1, O_0, O_1 (128 colum
 constexpr uint32_t kTmemS = 0;                  // + x * 128 + buffer * 64; P over its first 32 columns
 constexpr uint32_t kTmemO = 256;                // + x * 128
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
-// A reference max is whole (weights then round alike whatever it is) and this far above
-// the scores that set it; it moves when a score exceeds it by kRescaleLog2.  Weights of
-// any size are exact to the same number of bits, and stay below 2^16; scores have to
-// climb by 24 before a pass is made again.
-constexpr float kHeadroomLog2 = 8.0f, kRescaleLog2 = 16.0f;
+// A reference max is whole and this far above the scores that set it; it moves up when a
+// score exceeds it, so that scores have to climb by 24 before a pass is made again.
+// Weights of any size are exact to the same number of bits, and none is above 1: O stays
+// within the number of keys times the largest value, as against the exact maximum.
+constexpr float kHeadroomLog2 = 24.0f;
 // A part starts from its row's reference of the part before, if no score of its first
-// job is above it and the largest is not this far below.
-constexpr float kGuessLog2 = -60.0f;
+// job is above it and the largest is not this far below: as far below the scores that set
+// it as the headroom is above them.
+constexpr float kGuessLog2 = -2.0f * kHeadroomLog2;
 
 // What a part costs, in sixteenths of a key tile under one query tile: a segment's
 // set-up and read-out, and a key tile under two query tiles.  From a least-squares fit
@@ -938,7 +939,7 @@ rows_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                         const float tmax = fmaxf(max3(e[0], e[1], e[2]), e[3]);
                         const float2 la = unf2(lacc[0]), lb = unf2(lacc[1]);
                         lsum = (la.x + la.y) + (lb.x + lb.y);
-                        bool need = m_ref == -INFINITY ? tmax > -INFINITY : tmax > kRescaleLog2;
+                        bool need = m_ref == -INFINITY ? tmax > -INFINITY : tmax > 0.f;
                         if (i == 0) {
                             if (tmax == -INFINITY) m_ref = -INFINITY;      // nothing seen: no reference
                             else need |= tmax < kGuessLog2;
