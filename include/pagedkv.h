@@ -68,7 +68,8 @@ enum pk_status {
     PK_ERR_NO_BLOCKS = -8,     /* the pool has no free block left: the scheduler must preempt */
     PK_ERR_UNKNOWN_SEQUENCE = -9,  /* no sequence with that id */
     PK_ERR_SEQUENCE_EXISTS = -10,  /* a sequence with that id already exists */
-    PK_ERR_HOST_MEMORY = -11   /* a host allocation failed */
+    PK_ERR_HOST_MEMORY = -11,  /* a host allocation failed */
+    PK_ERR_PENDING_COPY = -12  /* a queued copy writes to a block that the call would free */
 };
 
 enum pk_dtype { PK_BF16 = 0, PK_FP32 = 1 };

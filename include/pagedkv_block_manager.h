@@ -68,15 +68,17 @@ int pk_bm_append_slots(pk_block_manager *bm, const int64_t *seq_ids, int n, int6
 int pk_bm_fork(pk_block_manager *bm, int64_t parent, int64_t child, int64_t num_tokens);
 
 /* Drops the sequence; blocks no other sequence holds return to the back of
- * the free list, in table order. */
+ * the free list, in table order.  (Copies queued into them stay queued: take
+ * them before, as pk_bm_truncate demands.) */
 int pk_bm_free_sequence(pk_block_manager *bm, int64_t seq_id);
 
 /* Shortens the sequence to its first num_tokens tokens (rejected drafts, after
  * pk_keep_tokens has moved the kept ones together): blocks behind them lose one
  * reference, and those no other sequence holds return to the back of the free
  * list, in table order.  PK_ERR_SHAPE if num_tokens is negative or more than the
- * sequence has.  Take queued copies (pk_bm_take_copies) before: a pair whose
- * destination is freed here stays in the queue. */
+ * sequence has.  PK_ERR_PENDING_COPY, and nothing changes, if a block that would
+ * be freed is the destination of a queued copy, which would then be made into
+ * another sequence's block: take the copies (pk_bm_take_copies) before. */
 int pk_bm_truncate(pk_block_manager *bm, int64_t seq_id, int64_t num_tokens);
 
 /* Number of copy pairs queued since the last pk_bm_take_copies. */

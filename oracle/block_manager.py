@@ -110,6 +110,8 @@ class CowBlockManager:
             raise ValueError("a sequence can only be shortened")
         table = self.tables[seq]
         nb = -(-num_tokens // self.block_size)
+        if any(dst in table[nb:] and self.ref[dst] == 1 for _, dst in self.pending_copies):
+            raise RuntimeError("a queued copy writes to a block that would be freed")
         for b in table[nb:]:
             self._drop(b)
         del table[nb:]

@@ -161,7 +161,7 @@ STATUS_NAMES = {
     0: "PK_OK", -1: "PK_ERR_NULL", -2: "PK_ERR_SHAPE", -3: "PK_ERR_UNSUPPORTED",
     -4: "PK_ERR_WORKSPACE", -5: "PK_ERR_CUDA", -6: "PK_ERR_ALIGNMENT", -7: "PK_ERR_NO_DEVICE",
     -8: "PK_ERR_NO_BLOCKS", -9: "PK_ERR_UNKNOWN_SEQUENCE", -10: "PK_ERR_SEQUENCE_EXISTS",
-    -11: "PK_ERR_HOST_MEMORY",
+    -11: "PK_ERR_HOST_MEMORY", -12: "PK_ERR_PENDING_COPY",
 }
 PK_ERR_NO_BLOCKS, PK_ERR_UNKNOWN_SEQUENCE, PK_ERR_SEQUENCE_EXISTS = -8, -9, -10
 DEVERR_BLOCK_ID, DEVERR_SLOT, DEVERR_PAIR, DEVERR_SEQ_LEN, DEVERR_TIMEOUT = 0x1, 0x2, 0x4, 0x8, 0x10

@@ -68,7 +68,8 @@ class BlockManager:
         check("pk_bm_free_sequence", self._lib.pk_bm_free_sequence(self._h, int(seq_id)))
 
     def truncate(self, seq_id: int, num_tokens: int) -> None:
-        """Keep the first ``num_tokens`` tokens; blocks behind them are given back."""
+        """Keep the first ``num_tokens`` tokens; blocks behind them are given back.
+        Copies queued into those have to be taken before (``take_copies``)."""
         check("pk_bm_truncate", self._lib.pk_bm_truncate(self._h, int(seq_id), int(num_tokens)))
 
     # -- outputs ------------------------------------------------------------

@@ -233,6 +233,9 @@ extern "C" int pk_bm_truncate(pk_block_manager *bm, int64_t seq_id, int64_t num_
     pk_block_manager::Seq &sq = it->second;
     if (num_tokens < 0 || num_tokens > sq.length) return PK_ERR_SHAPE;
     const size_t keep = static_cast<size_t>(num_tokens / bm->block_size + (num_tokens % bm->block_size != 0));
+    for (size_t c = 1; c < bm->copies.size(); c += 2)      // destinations
+        for (size_t j = keep; j < sq.table.size(); ++j)
+            if (sq.table[j] == bm->copies[c] && bm->ref[sq.table[j]] == 1) return PK_ERR_PENDING_COPY;
     for (size_t j = keep; j < sq.table.size(); ++j) bm->drop(sq.table[j]);
     sq.table.resize(keep);
     sq.length = num_tokens;

@@ -87,6 +87,7 @@ extern "C" const char *pk_status_string(int status) {
         case PK_ERR_UNKNOWN_SEQUENCE: return "no sequence with that id";
         case PK_ERR_SEQUENCE_EXISTS: return "a sequence with that id already exists";
         case PK_ERR_HOST_MEMORY: return "a host allocation failed";
+        case PK_ERR_PENDING_COPY: return "a queued copy writes to a block that would be freed";
         default: return "unknown status";
     }
 }
