@@ -102,6 +102,23 @@ int pk_selftest_cross_wait_timeout(void *out, int out_dtype, const void *q, int 
                                    pk_stream_t stream);
 
 /*
+ * Self-test of the second look at the lengths, as pk_selftest_decode_stale_lengths is
+ * for decode.  The attention kernel plans its work before the programmatic wait on the
+ * kernel before it and plans again where the lengths read after the wait differ; here
+ * the first plan is made from stale_seq_lens [num_seqs] and stale_cu_q_lens
+ * [num_seqs + 1] (any values; out-of-range ones are not reported).  The result is that
+ * of pk_paged_attention_cross, whose arguments the others are.  (With more than 384
+ * sequences nothing is planned ahead.)  PK_ERR_NULL if either array is NULL.
+ */
+int pk_selftest_cross_stale_lengths(void *out, int out_dtype, const void *q, int total_q, const int32_t *cu_q_lens,
+                                    int max_q_len, const void *k_cache, const void *v_cache,
+                                    const int32_t *block_tables, int max_blocks_per_seq, const int32_t *seq_lens,
+                                    int max_seq_len, int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                    int num_blocks, int block_size, float scale, const int32_t *stale_seq_lens,
+                                    const int32_t *stale_cu_q_lens, void *workspace, size_t workspace_bytes,
+                                    pk_stream_t stream);
+
+/*
  * The accepted path of each tree.  Node 0 is the root (the token sampled last, so
  * it is right); node c > 0 hangs below parents[c].  The path starts at node 0 and
  * goes on, from node p, to the lowest c > p of the tree with parents[c] == p and

@@ -70,6 +70,7 @@ from .tree import (  # noqa: F401
     pk_keep_tokens_layers,
     pk_paged_attention_cross,
     pk_paged_attention_tree,
+    pk_selftest_cross_stale_lengths,
     pk_selftest_cross_wait_timeout,
     pk_tree_workspace_bytes,
 )

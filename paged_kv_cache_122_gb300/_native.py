@@ -126,6 +126,11 @@ SIGNATURES = {
         c_void_p, c_void_p, c_void_p, c_int, c_void_p, c_int,
         c_int, c_int, c_int, c_int, c_int, c_int, c_float,
         c_void_p, c_size_t, c_int, c_uint, c_void_p]),           # workspace, bytes, stall_tile, wait_limit_us, stream
+    "pk_selftest_cross_stale_lengths": (c_int, [
+        c_void_p, c_int, c_void_p, c_int, c_void_p, c_int,
+        c_void_p, c_void_p, c_void_p, c_int, c_void_p, c_int,
+        c_int, c_int, c_int, c_int, c_int, c_int, c_float,
+        c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),      # stale_seq_lens, stale_cu_q_lens, workspace, bytes, stream
     "pk_accept_tree": (c_int, [
         c_void_p, c_void_p, c_void_p, c_void_p,                  # accepted, num_accepted, next_tokens, new_seq_lens
         c_void_p, c_void_p, c_void_p, c_int,                     # draft_tokens, parents, target_tokens, total_q

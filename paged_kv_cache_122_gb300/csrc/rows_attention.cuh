@@ -23,6 +23,7 @@ struct RowsParams {
     void *slots;                  // partial results of cut segments, or NULL: nothing is cut
     uint64_t wait_limit_ns;       // bounded waits (0 = 1 s)
     int stall_tile;               // self-test of the bounded waits (0 = off)
+    const int32_t *lens_ahead, *cu_ahead;   // self-test of the second look at the lengths (NULL = off)
     unsigned int *err;
 };
 

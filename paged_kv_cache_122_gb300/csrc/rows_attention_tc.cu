@@ -509,7 +509,9 @@ rows_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
         copy[2 * kThreads + threadIdx.x] = seen.q1;
     };
     if (owner) {
-        seen = load_raw(p, threadIdx.x);
+        // (The self-test of the second look has the first one look elsewhere.)
+        const int32_t *lens = p.lens_ahead ? p.lens_ahead : p.seq_lens, *cu = p.cu_ahead ? p.cu_ahead : p.cu_q_lens;
+        seen = {load_cg(lens + threadIdx.x), load_cg(cu + threadIdx.x), load_cg(cu + threadIdx.x + 1)};
         put();
     }
     if (ahead) __syncthreads();

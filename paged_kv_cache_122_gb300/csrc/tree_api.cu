@@ -13,7 +13,8 @@ int attend(void *out, int out_dtype, const void *q, int total_q, const int32_t *
            bool tree, const uint64_t *tree_mask, int mask_words, const void *k_cache, const void *v_cache,
            const int32_t *block_tables, int max_blocks_per_seq, const int32_t *seq_lens, int max_seq_len, int num_seqs,
            int num_heads, int num_kv_heads, int head_dim, int num_blocks, int block_size, float scale, void *workspace,
-           size_t workspace_bytes, pk_stream_t stream, int stall_tile, uint64_t wait_limit_ns) {
+           size_t workspace_bytes, pk_stream_t stream, int stall_tile, uint64_t wait_limit_ns,
+           const int32_t *lens_ahead, const int32_t *cu_ahead) {
     if (num_seqs < 0 || num_heads <= 0 || num_kv_heads <= 0 || num_blocks < 0 || max_blocks_per_seq < 0 ||
         max_seq_len < 0 || block_size <= 0 || total_q < 0 || max_q_len < 0)
         return PK_ERR_SHAPE;
@@ -69,6 +70,8 @@ int attend(void *out, int out_dtype, const void *q, int total_q, const int32_t *
     if (p.scale_log2 == 0.f) p.scale_log2 = 1.17549435e-38f;
     p.wait_limit_ns = wait_limit_ns;
     p.stall_tile = stall_tile;
+    p.lens_ahead = lens_ahead;
+    p.cu_ahead = cu_ahead;
     p.err = pk::error_word_ptr();
     if (!p.err) return PK_ERR_NO_DEVICE;
     const pk::StreamTurn turn(pk::current_device(), stream);
@@ -93,7 +96,7 @@ extern "C" int pk_paged_attention_tree(void *out, int out_dtype, const void *q, 
                                        void *workspace, size_t workspace_bytes, pk_stream_t stream) {
     return attend(out, out_dtype, q, total_q, cu_q_lens, max_q_len, true, tree_mask, mask_words, k_cache, v_cache,
                   block_tables, max_blocks_per_seq, seq_lens, max_seq_len, num_seqs, num_heads, num_kv_heads, head_dim,
-                  num_blocks, block_size, scale, workspace, workspace_bytes, stream, 0, 0);
+                  num_blocks, block_size, scale, workspace, workspace_bytes, stream, 0, 0, nullptr, nullptr);
 }
 
 extern "C" int pk_paged_attention_cross(void *out, int out_dtype, const void *q, int total_q, const int32_t *cu_q_lens,
@@ -104,7 +107,7 @@ extern "C" int pk_paged_attention_cross(void *out, int out_dtype, const void *q,
                                         size_t workspace_bytes, pk_stream_t stream) {
     return attend(out, out_dtype, q, total_q, cu_q_lens, max_q_len, false, nullptr, 0, k_cache, v_cache, block_tables,
                   max_blocks_per_seq, seq_lens, max_seq_len, num_seqs, num_heads, num_kv_heads, head_dim, num_blocks,
-                  block_size, scale, workspace, workspace_bytes, stream, 0, 0);
+                  block_size, scale, workspace, workspace_bytes, stream, 0, 0, nullptr, nullptr);
 }
 
 extern "C" int pk_selftest_cross_wait_timeout(void *out, int out_dtype, const void *q, int total_q,
@@ -118,5 +121,19 @@ extern "C" int pk_selftest_cross_wait_timeout(void *out, int out_dtype, const vo
     return attend(out, out_dtype, q, total_q, cu_q_lens, max_q_len, false, nullptr, 0, k_cache, v_cache, block_tables,
                   max_blocks_per_seq, seq_lens, max_seq_len, num_seqs, num_heads, num_kv_heads, head_dim, num_blocks,
                   block_size, scale, workspace, workspace_bytes, stream, stall_tile,
-                  static_cast<uint64_t>(wait_limit_us) * 1000u);
+                  static_cast<uint64_t>(wait_limit_us) * 1000u, nullptr, nullptr);
+}
+
+extern "C" int pk_selftest_cross_stale_lengths(void *out, int out_dtype, const void *q, int total_q,
+                                               const int32_t *cu_q_lens, int max_q_len, const void *k_cache,
+                                               const void *v_cache, const int32_t *block_tables, int max_blocks_per_seq,
+                                               const int32_t *seq_lens, int max_seq_len, int num_seqs, int num_heads,
+                                               int num_kv_heads, int head_dim, int num_blocks, int block_size,
+                                               float scale, const int32_t *stale_seq_lens,
+                                               const int32_t *stale_cu_q_lens, void *workspace, size_t workspace_bytes,
+                                               pk_stream_t stream) {
+    if (!stale_seq_lens || !stale_cu_q_lens) return PK_ERR_NULL;
+    return attend(out, out_dtype, q, total_q, cu_q_lens, max_q_len, false, nullptr, 0, k_cache, v_cache, block_tables,
+                  max_blocks_per_seq, seq_lens, max_seq_len, num_seqs, num_heads, num_kv_heads, head_dim, num_blocks,
+                  block_size, scale, workspace, workspace_bytes, stream, 0, 0, stale_seq_lens, stale_cu_q_lens);
 }

@@ -128,6 +128,24 @@ def pk_selftest_cross_wait_timeout(q: torch.Tensor, cu_q_lens: torch.Tensor, max
                    _raw_stream(dev, stream)))
 
 
+def pk_selftest_cross_stale_lengths(q: torch.Tensor, cu_q_lens: torch.Tensor, max_q_len: int, k_cache: torch.Tensor,
+                                    v_cache: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                                    scale: float, stale_seq_lens: torch.Tensor, stale_cu_q_lens: torch.Tensor, *,
+                                    out_dtype=torch.bfloat16, max_seq_len: Optional[int] = None,
+                                    out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                                    stream=None) -> int:
+    """Self-test of the second look at the lengths (see the C header): a cross-attention
+    call whose first plan is made from the stale arrays.  Returns the call's status."""
+    dev, out, head, tail = _args(q, cu_q_lens, max_q_len, k_cache, v_cache, block_tables, seq_lens, scale, out_dtype,
+                                 max_seq_len, out, workspace, stream)
+    for stale, name, like in ((stale_seq_lens, "stale_seq_lens", seq_lens), (stale_cu_q_lens, "stale_cu_q_lens", cu_q_lens)):
+        _need(stale, name, torch.int32, 1, dev)
+        if stale.numel() != like.numel():
+            raise ValueError(f"{name} must have as many entries as the true one")
+    return int(_on(dev, load().pk_selftest_cross_stale_lengths, *head, *tail[:-2], stale_seq_lens.data_ptr(),
+                   stale_cu_q_lens.data_ptr(), *tail[-2:], _raw_stream(dev, stream)))
+
+
 def pk_accept_tree(draft_tokens: torch.Tensor, parents: torch.Tensor, target_tokens: torch.Tensor,
                    cu_q_lens: torch.Tensor, max_q_len: int, seq_lens: torch.Tensor, *,
                    stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
