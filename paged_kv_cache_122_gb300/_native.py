@@ -161,6 +161,7 @@ SIGNATURES = {
 }
 
 PK_OK = 0
+PK_ERR_UNSUPPORTED = -3
 PK_BF16, PK_FP32 = 0, 1
 STATUS_NAMES = {
     0: "PK_OK", -1: "PK_ERR_NULL", -2: "PK_ERR_SHAPE", -3: "PK_ERR_UNSUPPORTED",

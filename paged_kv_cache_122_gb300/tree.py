@@ -21,6 +21,8 @@ from ._native import check, load
 from .api import _at, _empty_like, _layers, _need, _on, _raw_stream
 from .fp8 import _NOTHING, _bound, _workspace
 
+_MAX_TREE = 8192        # nodes of a tree in pk_accept_tree
+
 
 @functools.lru_cache(maxsize=256)
 def pk_tree_workspace_bytes(num_heads: int, num_kv_heads: int, head_dim: int, max_q_len: int, max_seq_len: int) -> int:
@@ -171,6 +173,8 @@ def pk_accept_tree(draft_tokens: torch.Tensor, parents: torch.Tensor, target_tok
     max_q_len = _bound(max_q_len)
     if max_q_len < 0:
         raise ValueError("max_q_len must not be negative")
+    if max_q_len > _MAX_TREE:                                # (before the results are allocated)
+        check("pk_accept_tree", _native.PK_ERR_UNSUPPORTED)
     with torch.cuda.stream(stream) if stream is not None else _NOTHING:
         # (From a tensor at hand: torch.empty with a device takes 2 us longer.)
         accepted = seq_lens.new_empty((N, max_q_len))
