@@ -114,21 +114,28 @@ keep_tokens_kernel(const KeepParams p) {
     const bool reports = blockIdx.y == 0 && threadIdx.x == 0;
     const int L = p.seq_lens[s], q0 = p.cu_q_lens[s], q1 = p.cu_q_lens[s + 1];
     const int n = p.num_accepted[s];
+    // The layers' pointers, a thread each: on their way while the list is checked.
+    static_assert(kKeepGroup <= kKeepThreads, "a thread for each layer");
+    const int mine = static_cast<int>(threadIdx.x) < layers ? layer0 + static_cast<int>(threadIdx.x) : -1;
+    uint4 *own_k = p.k_cache, *own_v = p.v_cache;
+    if (mine >= 0 && p.k_layers) {
+        own_k = p.k_layers[mine];
+        own_v = p.v_layers[mine];
+    }
     const int32_t *list = p.accepted + static_cast<size_t>(s) * p.accepted_stride;
     const int64_t cap = static_cast<int64_t>(p.max_blocks_per_seq) << p.log2_block;
     // A layer of which K or V cannot be used is left alone, both of them: its rows have to
     // stay those of the same tokens.  (Reported by the first sequence's CTAs.)
-    for (int l = threadIdx.x; l < layers; l += kKeepThreads) {
-        uint4 *k = p.k_layers ? p.k_layers[layer0 + l] : p.k_cache, *v = p.k_layers ? p.v_layers[layer0 + l] : p.v_cache;
-        if (!k || !v || ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 15u)) {
-            if (s == 0) pk::set_error(p.err, PK_DEVERR_POINTER);
-            k = v = nullptr;
-        }
-        caches[l][0] = k;
-        caches[l][1] = v;
-    }
+    auto put_pointers = [&]() {
+        if (mine < 0) return;
+        const bool ok = own_k && own_v && !((reinterpret_cast<uintptr_t>(own_k) | reinterpret_cast<uintptr_t>(own_v)) & 15u);
+        if (!ok && s == 0) pk::set_error(p.err, PK_DEVERR_POINTER);
+        caches[threadIdx.x][0] = ok ? own_k : nullptr;
+        caches[threadIdx.x][1] = ok ? own_v : nullptr;
+    };
     if (L < 0 || L > cap || q0 < 0 || q1 < q0 || q1 - q0 > L) {
         if (reports) pk::set_error(p.err, PK_DEVERR_SEQ_LEN);
+        put_pointers();
         return;
     }
     const int nodes = q1 - q0;
@@ -140,6 +147,7 @@ keep_tokens_kernel(const KeepParams p) {
             bad |= at >= nodes || at <= (i > 0 ? list[i - 1] : -1);
             moved += at != i;
         }
+    put_pointers();
     if (__syncthreads_or(bad)) {
         if (reports) pk::set_error(p.err, PK_DEVERR_DRAFT);
         return;
