@@ -410,7 +410,8 @@ int pk_copy_blocks(void *k_cache, void *v_cache, const int64_t *src_dst_pairs,
  *
  * The pointer arrays are caller-owned device memory (8-byte aligned); the
  * host cannot read them, so a NULL or unaligned per-layer pointer is found on
- * the GPU: that layer is skipped and PK_DEVERR_POINTER is set.  Bad slots and
+ * the GPU: that layer is skipped and PK_DEVERR_POINTER is set.  (Block copies skip
+ * that one of K and V: the other one's copy goes on.)  Bad slots and
  * pairs are handled per layer as in the one-layer calls.  num_layers in
  * [1, 65535] (block copies: [1, 32767]); num_layers == 0 or no tokens / pairs
  * is a no-op.  Bit-exact.

@@ -16,7 +16,10 @@
  * pk_paged_attention_cross attends to keys of another length, all visible: the
  * cross attention of a decoder to an encoder's states in the paged cache.
  *
- * Pointers, streams, errors and supported sizes are those of pagedkv.h.
+ * Pointers, streams, errors and supported sizes are those of pagedkv.h.  All of them
+ * take the bf16 cache.  The 8-bit one (pagedkv_fp8.h) has chains of drafts only: its
+ * rows share a block's scale, so none can be moved alone, and its keys can be attended
+ * to here only after pk_gather_kv_fp8 has copied them out as bf16.
  */
 #ifndef PAGEDKV_TREE_H
 #define PAGEDKV_TREE_H
@@ -63,7 +66,9 @@ size_t pk_tree_workspace_bytes(int num_heads, int num_kv_heads, int head_dim, in
  * results are finite while the number of keys times the largest value is below
  * 2^127 and the scaled scores below 2^27.  A value that is not
  * finite in a node of the tree shows in all rows of its tree; a key that is not
- * finite shows only in the rows that see it.  Deterministic.
+ * finite shows only in the rows that see it.  The same call gives the same bits; those
+ * of a sequence may change with the rest of the batch, which decides where it is cut and
+ * against which reference its weights are taken.
  */
 int pk_paged_attention_tree(void *out, int out_dtype, const void *q, int total_q, const int32_t *cu_q_lens,
                             int max_q_len, const uint64_t *tree_mask, int mask_words, const void *k_cache,

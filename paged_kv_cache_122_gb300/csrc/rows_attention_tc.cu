@@ -76,7 +76,8 @@ constexpr float kGuessLog2 = -2.0f * kHeadroomLog2;
 constexpr int64_t kTileCost1 = 16, kTileCost2 = 27;
 template <int D>
 constexpr int64_t kSegCost = D == 128 ? 38 : 40;
-// A CTA is not given less than this: a cut costs a merge.
+// A CTA is not given less than this: a cut costs a merge.  (The plan does not know what:
+// one block of the merge joins all parts of a segment, one after the other.)
 constexpr int64_t kMinCost = 32;
 
 // Rings of 128-key tiles: what 224 KB hold.  TWO: segments may have two query

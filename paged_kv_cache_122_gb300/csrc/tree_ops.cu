@@ -29,7 +29,7 @@ cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, 
 // looked at side by side; the path is then a chain of shared-memory reads by one
 // thread.  Bound by two dependent trips to memory (node -> its parent's target).
 constexpr int kAcceptThreads = 128;
-constexpr int kMaxTree = 8192;      // next[] and the path in 48 KB
+constexpr int kMaxTree = 8192;      // next[], which the path is written over, in 32 KB
 constexpr int kNone = 0x7fffffff;
 
 __global__ void __launch_bounds__(kAcceptThreads)
@@ -82,7 +82,7 @@ accept_tree_kernel(int32_t *accepted, int32_t *num_accepted, int64_t *next_token
 // in their place are a prefix, and a row that a pass writes (i) comes before every row
 // that a later pass reads (accepted[j] >= j > i).  Bound by memory: two rows moved for
 // each kept token that is not in its place.  (A CTA per layer, K or V and sequence
-// looked everything up 64 times for 32 layers: 25 us where this takes 18, for 128
+// looked everything up 64 times for 32 layers: 25 us where this takes 17, for 128
 // sequences.)
 constexpr int kKeepThreads = 256;
 constexpr int kKeepWarps = kKeepThreads / 32;
@@ -230,8 +230,8 @@ int keep(KeepParams &p, const void *const *ptrs, int num_seqs, int num_layers, i
     p.err = pk::error_word_ptr();
     const int sms = pk::sm_count();
     if (!p.err || sms <= 0) return PK_ERR_NO_DEVICE;
-    // As many layers to a CTA as still leave eight CTAs for each SM (128 sequences, 32 layers: 18 us;
-    // four for each SM 20, two 23, one layer to a CTA 24).
+    // As many layers to a CTA as still leave eight CTAs for each SM (128 sequences, 32 layers: 17 us;
+    // measured when eight took 18: four for each SM 20, two 23, one layer to a CTA 24).
     p.num_layers = num_layers;
     p.group = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kKeepGroup, static_cast<int64_t>(num_seqs) * num_layers / (8 * sms))));
     const dim3 grid(num_seqs, (num_layers + p.group - 1) / p.group);
